@@ -151,7 +151,7 @@ def work(case):
 
 
 def _pack_k(q):
-    """[..., D] whole numbers -8..7 -> [..., D/2] bytes of K rows."""
+    """[..., D] whole numbers -7..7 -> [..., D/2] bytes of K rows."""
     d = q.shape[-1]
     u = (q + 8).to(torch.uint8).unflatten(-1, (d // 32, 4, 8))[..., list(_SLOT_ELEMENT)].transpose(-3, -2)
     return (u[..., 0::2] | (u[..., 1::2] << 4)).flatten(-3)
@@ -164,7 +164,7 @@ def _unpack_k(b):
 
 
 def _pack_v(q):
-    """[..., D] whole numbers -8..7 -> [..., D/8, 4] bytes: the words of one token."""
+    """[..., D] whole numbers -7..7 -> [..., D/8, 4] bytes: the words of one token."""
     d = q.shape[-1]
     u = (q + 8).to(torch.uint8).unflatten(-1, (d // 64, 4, 16)).movedim(-1, -3)
     return (u[..., 0::2] | (u[..., 1::2] << 4)).flatten(-3).unflatten(-1, (d // 8, 4))
@@ -181,7 +181,7 @@ def _quantize(x, group):
     x = x.float().unflatten(-1, (-1, group))
     s = (x.abs().amax(-1) / 7).clamp(max=_SCALE_MAX).half()
     f = s.float().unsqueeze(-1)
-    q = torch.where(f > 0, torch.round(x / f), torch.zeros_like(x)).clamp(-8, 7)
+    q = torch.where(f > 0, torch.round(x / f), torch.zeros_like(x)).clamp(-7, 7)
     return q.flatten(-2), s
 
 
@@ -472,7 +472,7 @@ def _exact_append(c, seed):
         y = x.double().reshape(c["tokens"], c["heads"], c["dim"] // c["group"], c["group"])
         step = torch.minimum(y.abs().max(-1, keepdim=True).values / 7, torch.tensor(_SCALE_MAX, device="cuda").double())
         step = step.to(torch.float16).double()
-        whole = torch.nan_to_num(torch.round(y / step), nan=0.0).clamp(-8, 7)
+        whole = torch.nan_to_num(torch.round(y / step), nan=0.0).clamp(-7, 7)
         out.append((whole * step).reshape(c["tokens"], c["heads"], c["dim"]))
     return tuple(out)
 
