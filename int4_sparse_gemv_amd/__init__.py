@@ -8,6 +8,11 @@ call the HIP kernels of ``libi4s.so`` through its C ABI (``include/i4s.h``);
 PyTorch only provides device memory and the current stream.  The method is
 the one of "Efficient LLM-based Advertising via Model Compression and
 Parallel Verification", sections 3.2 and 3.3.
+
+The rest of a decode or verification step is in ``serving``: a 4-bit paged KV
+cache (``kv_cache``, ``kv_extend``, ``kv_append``, ``kv_read``), attention
+over it (``kv_attention``) and token scores (``token_logprobs``), declared in
+``include/i4s_serve.h``.
 """
 
 from __future__ import annotations
@@ -26,6 +31,20 @@ from ._binding import (  # noqa: F401  (the C names)
 __all__ = ["PackedWeight", "pack", "run", "run_multi", "pack_sizes", "run_workspace_size", "I4SError",
            "i4s_pack_sizes", "i4s_pack", "i4s_pack_ex", "i4s_run", "i4s_run_multi", "i4s_run_workspace_size", "i4s_run_ws",
            "i4s_status_string", "i4s_last_error", "i4s_version", "i4s_format_version"]
+
+_SERVING = ("KVCache", "KVStep", "TokenLogprobs", "kv_cache", "kv_extend", "kv_append", "kv_read", "kv_attention",
+            "token_logprobs")
+__all__ += _SERVING
+
+
+def __getattr__(name):
+    # the serving operators need torch when they are defined, packing only when it is called
+    if name in _SERVING or name == "serving":
+        import importlib
+        serving = importlib.import_module(".serving", __name__)
+        globals().update({n: getattr(serving, n) for n in _SERVING})
+        return serving if name == "serving" else globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def _torch():

@@ -19,6 +19,10 @@ namespace {
 
 thread_local std::string g_last_error;
 
+}  // namespace
+
+namespace i4s {
+
 i4s_status fail(i4s_status st, const char *fmt, ...) {
   char buf[512];
   va_list ap;
@@ -33,12 +37,15 @@ i4s_status device_error(hipError_t e, const char *what) {
   return fail(I4S_ERR_DEVICE, "%s: %s", what, hipGetErrorString(e));
 }
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+}  // namespace i4s
 
-bool overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
-  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-  return pa < pb + nb && pb < pa + na;
-}
+using i4s::aligned;
+using i4s::check_device;
+using i4s::device_error;
+using i4s::fail;
+using i4s::overlap;
+
+namespace {
 
 // Shape/pattern checks shared by pack_sizes, pack and run.  `allow_adaptive`
 // admits group_size 0 (pack only).
@@ -68,6 +75,10 @@ i4s_status check_shape(int32_t rows, int32_t cols, int32_t n_keep, int32_t group
 // gfx950 only.  The answer per device is cached (a benign, monotonic cache).
 std::atomic<int> g_arch_ok[64];
 
+}  // namespace
+
+namespace i4s {
+
 i4s_status check_device() {
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
@@ -85,6 +96,10 @@ i4s_status check_device() {
   if (!ok) return fail(I4S_ERR_UNSUPPORTED, "device %d is %s, not gfx950", dev, prop.gcnArchName);
   return I4S_OK;
 }
+
+}  // namespace i4s
+
+namespace {
 
 struct U128 {
   uint64_t lo, hi;

@@ -1,0 +1,559 @@
+// Attention of a few query tokens per sequence over the 4-bit paged KV cache
+// (format: include/i4s_serve.h), for gfx950.
+//
+// A block takes the query rows (tokens x query heads) of one sequence that
+// read one KV head, up to 16 * RT of them, and a piece of the keys; its waves
+// take steps of 32 keys in turn, each with a softmax of its own (running
+// maximum and sum), and join at the end.  Pieces join in a second launch.
+//
+// Everything is computed transposed, so that no value moves between lanes on
+// the way: lane l = i + 16a of a wave.
+//   S^T = K Q^T: v_mfma_f32_16x16x32 with 16 keys as rows, 16 query rows as
+//     columns and 32 channels.  A lane loads key i's words of the channels
+//     32j + 8a .. +7, j = 0..D/32-1: neighbours in the format, so that one
+//     wide load per lane covers 16 keys without a gap.  The tile comes out
+//     with query row i and keys 4a .. 4a+3 in lane l.
+//   O^T = V^T P^T: v_mfma_f32_16x16x32_f16 with 16 channels as rows, 16 query
+//     rows as columns and 32 keys.  Its B operand wants query row i and 8
+//     keys in lane l: take the keys 4a .. 4a+3 of two tiles, and P is in
+//     place as S came out.  Its A operand wants channel i (of 16) and the
+//     same 8 keys: the format keeps the words of channel i for 4 neighbouring
+//     tokens together, and a v_perm_b32 of two tokens' words puts their
+//     halves into one dword, whose nibbles then widen to fp16 pairs (token,
+//     next token) of one channel.
+// 4-bit values are widened with bit operations: for K the nibble goes into
+// the mantissa of 16.0 (16 + u, exact in fp16 and bf16), and the offset 24 =
+// 16 + 8 leaves with the sum: the products start from -24 * sum(q) of the
+// group's channels, in fp32.  For V the values become exact fp16 integers.
+// Scales: K's multiply the fp32 sums of a group's channels; V's multiply the
+// probabilities, which are rounded to fp16 once, after that.  So that no
+// probability loses bits to fp16's range the offset of the exponent includes
+// a power of two that brings (largest probability) x (largest V scale seen so
+// far) just below 2^15.
+//
+// Bound by: memory.  A key of one head is D + 4D/G bytes.
+
+#include <float.h>
+
+#include "i4s_gemv_common.h"
+#include "i4s_serve_internal.h"
+
+namespace i4s {
+namespace {
+
+typedef _Float16 hf8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf8_t __attribute__((ext_vector_type(8)));
+typedef float f4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t w4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t w2_t __attribute__((ext_vector_type(2)));
+
+// fp16 and bf16 query types: the matrix instruction, and how nibble p (and
+// p + 4, 16 bits on) of a word becomes 16 + u.
+struct F16 {
+  typedef hf8_t vec;
+  static constexpr uint32_t kMask = 0x03C003C0u, kSixteen = 0x4C004C00u;
+  static constexpr int kShift = 6;  // left shift of nibble 0
+  static __device__ f4_t mfma(vec a, vec b, f4_t c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+  static __device__ float to_float(uint32_t bits) { return fp16_bits_to_float(bits); }
+  static __device__ uint32_t from_float(float f) { return float_to_fp16_bits(f); }
+};
+struct BF16 {
+  typedef bf8_t vec;
+  static constexpr uint32_t kMask = 0x00780078u, kSixteen = 0x41804180u;
+  static constexpr int kShift = 3;
+  static __device__ f4_t mfma(vec a, vec b, f4_t c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+  static __device__ float to_float(uint32_t bits) { return __builtin_bit_cast(float, bits << 16); }
+  static __device__ uint32_t from_float(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+};
+
+constexpr float kOffset = 24.0f;   // 16 of the widening + 8 of the nibble
+constexpr float kLowest = -1e38f;  // exponent offset of a row that has seen no key
+
+// (a & m) | c, one v_and_or_b32.  Left to the compiler here: it does not see
+// which registers an instruction in inline asm writes when it places the
+// waits that a VALU write to a matrix instruction's registers needs.
+__device__ inline uint32_t mask_or(uint32_t a, uint32_t m, uint32_t c) { return (a & m) | c; }
+
+// Nibbles p and p + 4 of w, p = 0..3, as exact fp16 pairs u - 8: the nibble
+// goes into the mantissa of 1024 at its place 0..3 or 4..7.
+__device__ inline void widen_v(uint32_t w, h2_t q[4]) {
+  const uint32_t magic = 0x64006400u, t = w >> 8;
+  const h2_t bias = {(_Float16)-1032.0f, (_Float16)-1032.0f};
+  const h2_t sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
+  const h2_t bias16 = {(_Float16)-72.0f, (_Float16)-72.0f};
+  q[0] = as_h2(mask_or(w, 0x000F000Fu, magic)) + bias;
+  q[2] = as_h2(mask_or(t, 0x000F000Fu, magic)) + bias;
+  q[1] = __builtin_elementwise_fma(as_h2(mask_or(w, 0x00F000F0u, magic)), sixteenth, bias16);
+  q[3] = __builtin_elementwise_fma(as_h2(mask_or(t, 0x00F000F0u, magic)), sixteenth, bias16);
+}
+
+// The eight channels of a K word as 16 + u.
+template <typename T>
+__device__ inline typename T::vec widen_k(uint32_t w) {
+  w4_t r;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const int s = T::kShift - 4 * p;
+    r[p] = mask_or(s >= 0 ? w << (s & 31) : w >> (-s & 31), T::kMask, T::kSixteen);
+  }
+  return __builtin_bit_cast(typename T::vec, r);
+}
+
+// Maximum and sum over the four lanes i, i + 16, i + 32, i + 48.  (The bits of
+// a vector's element are copied out before they are taken for a float:
+// __builtin_bit_cast of the element itself reads element 0.)
+struct Two {
+  float a, b;
+};
+__device__ inline Two halves_of(float v) {
+  const uint32_t x = __builtin_bit_cast(uint32_t, v);
+  const auto s = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  const uint32_t a = s[0], b = s[1];
+  return {__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)};
+}
+__device__ inline Two quarters_of(float v) {
+  const uint32_t x = __builtin_bit_cast(uint32_t, v);
+  const auto s = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  const uint32_t a = s[0], b = s[1];
+  return {__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)};
+}
+__device__ inline float max4(float v) {
+  const Two h = halves_of(v), q = quarters_of(fmaxf(h.a, h.b));
+  return fmaxf(q.a, q.b);
+}
+__device__ inline float sum4(float v) {
+  const Two h = halves_of(v), q = quarters_of(h.a + h.b);
+  return q.a + q.b;
+}
+
+// What a block works on: its sequence's lengths, all made safe.
+struct Work {
+  int len, q0, q_len, ctx, used;
+};
+__device__ inline Work work_of(const AttentionKernelArgs &a, int seq) {
+  Work w;
+  w.len = (int)clamp_to<int64_t>(a.lens[seq], 0, (int64_t)a.width << a.shift);
+  w.q0 = seq;
+  int q1 = seq + 1;
+  if (a.q_start) {
+    w.q0 = clamp_to(a.q_start[seq], 0, a.num_tokens);
+    q1 = clamp_to(a.q_start[seq + 1], w.q0, a.num_tokens);
+  }
+  w.q_len = q1 - w.q0;
+  w.ctx = w.len - w.q_len;
+  w.used = clamp_to((int)(((int64_t)w.len + a.chunk - 1) / a.chunk), 1, a.splits);
+  return w;
+}
+
+// The registers of one step of 32 keys (two tiles of 16) for one lane.
+template <int D, int G>
+struct Step {
+  static constexpr int kVWords = D == 256 ? 8 : 4;
+  uint32_t k[2][D / 32], v[2][kVWords];
+  uint32_t ks[2][D / G][2], vs[2][D / G][2];  // fp16 scales of four keys
+};
+
+template <int N>
+__device__ inline void load_words(uint32_t *to, const void *from) {
+  if constexpr (N == 2) {
+    const w2_t x = *static_cast<const w2_t *>(from);
+    to[0] = x.x, to[1] = x.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const w4_t x = static_cast<const w4_t *>(from)[i];
+      to[4 * i] = x.x, to[4 * i + 1] = x.y, to[4 * i + 2] = x.z, to[4 * i + 3] = x.w;
+    }
+  }
+}
+
+template <typename T, int D, int G, int RT>
+__global__ __launch_bounds__(256) void attention_kernel(AttentionKernelArgs a) {
+  constexpr int NG = D / G, KJ = D / 32, NC = D / 64;
+  constexpr bool kBiasInSum = NG * RT <= 8;  // else the registers are needed elsewhere
+  constexpr int kRowStride = D + 4;          // floats; the 16 rows of a store fall in distinct banks
+  extern __shared__ float lds[];
+  const int waves = blockDim.x / 64;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int lane = threadIdx.x % 64, li = lane % 16, la = lane / 16;
+
+  const int rb = blockIdx.x % a.row_blocks;
+  const int head = (blockIdx.x / a.row_blocks) % a.kv_heads;
+  const int seq = blockIdx.x / a.row_blocks / a.kv_heads;
+  const int split = blockIdx.y;
+  const Work w = work_of(a, seq);
+  const int rows = min(w.q_len, a.max_q) * a.share;
+  const int row0 = rb * 16 * RT;
+  if (row0 >= rows || split >= w.used) return;
+  const int key0 = split * a.chunk;
+  const int key1 = split == a.splits - 1 ? w.len : min(w.len, key0 + a.chunk);
+
+  // the query rows: lane (i, a) holds channels 32j + 8a .. +7 of row i
+  typename T::vec q[RT][KJ];
+  float bias[RT][NG];
+  int limit[RT];          // last visible key (causal)
+  uint64_t tree[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int row = row0 + 16 * r + li;
+    const bool has = row < rows;
+    const int token = w.q0 + (has ? row / a.share : 0), qh = head * a.share + (has ? row % a.share : 0);
+    const uint16_t *p = static_cast<const uint16_t *>(a.q) + token * a.q_token + qh * a.q_head + 8 * la;
+    float s[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) s[g] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < KJ; ++j) {
+      w4_t x = *reinterpret_cast<const w4_t *>(p + 32 * j);
+      if (!has) x = w4_t{0, 0, 0, 0};
+      q[r][j] = __builtin_bit_cast(typename T::vec, x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[32 * j / G] += T::to_float(x[e] & 0xFFFFu) + T::to_float(x[e] >> 16);
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) bias[r][g] = -kOffset * sum4(s[g]);
+    limit[r] = w.ctx + (token - w.q0);
+    tree[r] = a.tree ? (uint64_t)a.tree[token] : 0;
+  }
+
+  f4_t o[RT][NC][4];
+  float mx[RT], mo[RT], l[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    mx[r] = -FLT_MAX;
+    mo[r] = kLowest;
+    l[r] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[r][c][e] = f4_t{0, 0, 0, 0};
+  }
+  uint32_t cap = 0;   // fp16 bits: no V scale so far was larger
+  float cap_log2 = 0.0f;
+
+  const int step1 = (key1 + kStepKeys - 1) / kStepKeys;
+  const int last_tile = (w.len - 1) >> 4;
+  const int tile_shift = a.shift - 4;
+  const int32_t *row_of_table = a.table + (int64_t)seq * a.width;
+
+  const auto page_of = [&](int s, int t) {
+    const int tile = min(2 * s + t, last_tile);
+    return row_of_table[tile >> tile_shift];
+  };
+  const auto load = [&](Step<D, G> &st, int s, const int32_t(&page)[2]) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int tile = min(2 * s + t, last_tile);
+      const int64_t number = clamp_to(page[t], 0, a.num_pages - 1);
+      const int64_t token = ((number * a.kv_heads + head) << a.shift) + ((tile & ((1 << tile_shift) - 1)) << 4);
+      load_words<KJ>(st.k[t], a.k_vals + token * (D / 2) + (li * (D / 2) + la * (D / 8)));
+      load_words<Step<D, G>::kVWords>(st.v[t], a.v_vals + token * (D / 2) + la * (2 * D) +
+                                                   (D == 64 ? (li / 2) * 16 : li * (D / 8)));
+      load_words<2 * NG>(&st.ks[t][0][0], a.k_scales + token * NG + la * (4 * NG));
+      load_words<2 * NG>(&st.vs[t][0][0], a.v_scales + token * NG + la * (4 * NG));
+    }
+  };
+
+  const auto compute = [&](Step<D, G> &st, int s) {
+    const int key = s * kStepKeys;
+    const bool edge = key + kStepKeys > w.ctx;  // some key is not seen by every row
+    f4_t sc[RT][2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      typename T::vec kf[KJ];
+#pragma unroll
+      for (int j = 0; j < KJ; ++j) kf[j] = widen_k<T>(st.k[t][j]);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        f4_t sum = {0, 0, 0, 0};
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const float b = bias[r][g];
+          f4_t acc = kBiasInSum ? f4_t{b, b, b, b} : f4_t{0, 0, 0, 0};
+#pragma unroll
+          for (int j = g * (G / 32); j < (g + 1) * (G / 32); ++j) acc = T::mfma(kf[j], q[r][j], acc);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float f = fp16_bits_to_float((st.ks[t][g][x / 2] >> (16 * (x % 2))) & 0xFFFFu);
+            sum[x] = fmaf(f, kBiasInSum ? acc[x] : acc[x] + b, sum[x]);
+          }
+        }
+        sc[r][t] = sum;
+      }
+    }
+    if (edge) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int pos = key + 16 * t + 4 * la + x;
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            bool seen = pos < w.len;
+            if (a.tree) {
+              const int b = pos - w.ctx;
+              seen = seen && (b < 0 || (b < 64 && ((tree[r] >> (b & 63)) & 1)));
+            } else {
+              seen = seen && pos <= limit[r];
+            }
+            if (!seen) sc[r][t][x] = -INFINITY;
+          }
+          // what lies behind the last key may be anything: 0 * that must be 0
+          if (pos >= w.len) {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) st.vs[t][g][x / 2] &= x % 2 ? 0x0000FFFFu : 0xFFFF0000u;
+          }
+        }
+    }
+    // the largest V scale of this lane's keys (fp16 bits of positive numbers order like the numbers)
+    uint32_t top = 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          typedef uint16_t us2 __attribute__((ext_vector_type(2)));
+          top = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2, top),
+                                                                       __builtin_bit_cast(us2, st.vs[t][g][x])));
+        }
+    top = max(top & 0xFFFFu, top >> 16);
+    bool grows = top > cap;
+    float m_new[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      float m = fmaxf(fmaxf(fmaxf(sc[r][0][0], sc[r][0][1]), fmaxf(sc[r][0][2], sc[r][0][3])),
+                      fmaxf(fmaxf(sc[r][1][0], sc[r][1][1]), fmaxf(sc[r][1][2], sc[r][1][3])));
+      m_new[r] = fmaxf(mx[r], max4(m));
+      grows |= m_new[r] > mx[r];
+    }
+    if (__any(grows)) {
+      if (__any(top > cap)) {
+        uint32_t all = cap;  // the keys of lanes i, i + 16, i + 32, i + 48
+#pragma unroll
+        for (int x = 0; x < 64; x += 16) all = max(all, (uint32_t)__builtin_amdgcn_readlane(top, x));
+        cap = all | 0x3FFu;
+        cap_log2 = 29.0f - (float)(cap >> 10);  // 2^15 / 2^(exponent + 1); subnormal scales count as 2^-14
+      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        mx[r] = m_new[r];
+        const float next = fmaxf(mx[r] * a.scale_log2, kLowest) - cap_log2;
+        const float f = __builtin_amdgcn_exp2f(mo[r] - next);
+        mo[r] = next;
+        l[r] *= f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[r][c][e] *= f;
+      }
+    }
+    hf8_t p[RT][NG];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      float e[2][4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          e[t][x] = __builtin_amdgcn_exp2f(fmaf(sc[r][t][x], a.scale_log2, -mo[r]));
+          l[r] += e[t][x];
+        }
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            p[r][g][4 * t + x] =
+                (_Float16)(e[t][x] * fp16_bits_to_float((st.vs[t][g][x / 2] >> (16 * (x % 2))) & 0xFFFFu));
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      h2_t vq[2][2][4];  // [tile][token pair][e]
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t w0 = st.v[t][4 * (c / 2) + 2 * x], w1 = st.v[t][4 * (c / 2) + 2 * x + 1];
+          const uint32_t upper = D == 64 ? (uint32_t)(li & 1) : (uint32_t)(c & 1);
+          widen_v(__builtin_amdgcn_perm(w1, w0, upper ? 0x07060302u : 0x05040100u), vq[t][x]);
+        }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const w4_t x = {__builtin_bit_cast(uint32_t, vq[0][0][e]), __builtin_bit_cast(uint32_t, vq[0][1][e]),
+                        __builtin_bit_cast(uint32_t, vq[1][0][e]), __builtin_bit_cast(uint32_t, vq[1][1][e])};
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          o[r][c][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(hf8_t, x), p[r][(64 * c + 16 * e) / G],
+                                                              o[r][c][e], 0, 0, 0);
+      }
+    }
+  };
+
+  // Two sets of registers: one step loads while the other computes.  Loads
+  // past the wave's last step read that step again (unconditional loads: with
+  // a branch around them every wait would be for all of them).
+  const int first = key0 / kStepKeys + wave;
+  if (first < step1) {
+    const int final_step = first + (step1 - 1 - first) / waves * waves;
+    const auto clip = [&](int s) { return min(s, final_step); };
+    Step<D, G> even, odd;
+    int32_t page[2] = {page_of(first, 0), page_of(first, 1)};
+    load(even, first, page);
+    int32_t next[2] = {page_of(clip(first + waves), 0), page_of(clip(first + waves), 1)};
+    int s = first;
+    while (true) {
+      load(odd, clip(s + waves), next);
+      page[0] = page_of(clip(s + 2 * waves), 0), page[1] = page_of(clip(s + 2 * waves), 1);
+      issue_fence();
+      compute(even, s);
+      s += waves;
+      if (s >= step1) break;
+      load(even, clip(s + waves), page);
+      next[0] = page_of(clip(s + 2 * waves), 0), next[1] = page_of(clip(s + 2 * waves), 1);
+      issue_fence();
+      compute(odd, s);
+      s += waves;
+      if (s >= step1) break;
+    }
+  }
+
+  // the waves join: offsets and sums first, then the outputs of one 16-row
+  // tile at a time, each scaled to the common offset
+  float *ml = lds;                         // [waves][16 * RT][2]
+  float *ob = lds + waves * 16 * RT * 2;   // [waves][16][kRowStride]
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    l[r] = sum4(l[r]);
+    if (la == 0) {
+      ml[(wave * 16 * RT + 16 * r + li) * 2] = mo[r];
+      ml[(wave * 16 * RT + 16 * r + li) * 2 + 1] = l[r];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    if (r) __syncthreads();
+    float top = kLowest;
+    for (int x = 0; x < waves; ++x) top = fmaxf(top, ml[(x * 16 * RT + 16 * r + li) * 2]);
+    const float f = __builtin_amdgcn_exp2f(mo[r] - top);
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<f4_t *>(ob + (wave * 16 + li) * kRowStride + 64 * c + 16 * e + 4 * la) = o[r][c][e] * f;
+    __syncthreads();
+    for (int at = threadIdx.x; at < 16 * (D / 4); at += blockDim.x) {
+      const int i = at / (D / 4), d = at % (D / 4) * 4, row = row0 + 16 * r + i;
+      if (row >= rows) break;
+      float m = kLowest, sum = 0.0f;
+      for (int x = 0; x < waves; ++x) m = fmaxf(m, ml[(x * 16 * RT + 16 * r + i) * 2]);
+      f4_t v = {0, 0, 0, 0};
+      for (int x = 0; x < waves; ++x) {
+        const float *e = ml + (x * 16 * RT + 16 * r + i) * 2;
+        sum = fmaf(e[1], __builtin_amdgcn_exp2f(e[0] - m), sum);
+        v += *reinterpret_cast<const f4_t *>(ob + (x * 16 + i) * kRowStride + d);
+      }
+      const int64_t token = w.q0 + row / a.share;
+      const int64_t at_row = token * (a.kv_heads * a.share) + head * a.share + row % a.share;
+      if (w.used == 1) {
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        v *= inv;
+        const w2_t bits = {T::from_float(v[0]) | T::from_float(v[1]) << 16,
+                           T::from_float(v[2]) | T::from_float(v[3]) << 16};
+        *reinterpret_cast<w2_t *>(static_cast<uint16_t *>(a.out) + at_row * D + d) = bits;
+        if (d == 0 && a.lse) a.lse[at_row] = sum == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+      } else {
+        const int64_t part = (int64_t)split * a.num_tokens * (a.kv_heads * a.share) + at_row;
+        *reinterpret_cast<f4_t *>(a.part_o + part * D + d) = v;
+        if (d == 0) {
+          a.part_ml[2 * part] = m;
+          a.part_ml[2 * part + 1] = sum;
+        }
+      }
+    }
+  }
+}
+
+// Joins the pieces of a row: block (row of the sequence, sequence).  D/4
+// neighbouring threads hold a row, 1024/D such groups take the pieces in turn.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttentionKernelArgs a) {
+  constexpr int kGroups = 1024 / D;
+  __shared__ f4_t part[256];
+  __shared__ float sums[kGroups];
+  const int q_heads = a.kv_heads * a.share;
+  const Work w = work_of(a, blockIdx.y);
+  const int t = blockIdx.x / q_heads;
+  if (t >= min(w.q_len, a.max_q) || w.used == 1) return;
+  const int64_t rows = (int64_t)a.num_tokens * q_heads;
+  const int64_t row = (int64_t)(w.q0 + t) * q_heads + blockIdx.x % q_heads;
+  float m = kLowest;
+  for (int s = 0; s < w.used; ++s) m = fmaxf(m, a.part_ml[2 * (s * rows + row)]);
+  const int group = threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
+  f4_t v = {0, 0, 0, 0};
+  float sum = 0.0f;
+  for (int s = group; s < w.used; s += kGroups) {
+    const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * (s * rows + row)] - m);
+    sum = fmaf(a.part_ml[2 * (s * rows + row) + 1], f, sum);
+    v += *reinterpret_cast<const f4_t *>(a.part_o + (s * rows + row) * D + d) * f;
+  }
+  part[threadIdx.x] = v;
+  if (d == 0) sums[group] = sum;
+  __syncthreads();
+  if (group) return;
+  for (int g = 1; g < kGroups; ++g) {
+    v += part[g * (D / 4) + threadIdx.x];
+    sum += sums[g];
+  }
+  v *= sum == 0.0f ? 0.0f : 1.0f / sum;
+  const w2_t bits = {T::from_float(v[0]) | T::from_float(v[1]) << 16, T::from_float(v[2]) | T::from_float(v[3]) << 16};
+  *reinterpret_cast<w2_t *>(static_cast<uint16_t *>(a.out) + row * D + d) = bits;
+  if (d == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+}
+
+template <typename T, int D, int G, int RT>
+hipError_t go(const AttentionKernelArgs &a, const AttentionPlan &p, hipStream_t stream) {
+  const size_t lds = sizeof(float) * p.waves * (16 * RT * 2 + 16 * (D + 4));
+  if (lds > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(attention_kernel<T, D, G, RT>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  const unsigned blocks = (unsigned)a.row_blocks * a.kv_heads * a.num_seqs;
+  hipLaunchKernelGGL((attention_kernel<T, D, G, RT>), dim3(blocks, p.splits), dim3(64 * p.waves), lds, stream, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3((unsigned)a.max_q * a.kv_heads * a.share, a.num_seqs), dim3(256),
+                     0, stream, a);
+  return hipGetLastError();
+}
+
+template <typename T, int D, int G>
+hipError_t by_rows(const AttentionKernelArgs &a, const AttentionPlan &p, hipStream_t stream) {
+  if (p.row_tiles == 1) return go<T, D, G, 1>(a, p, stream);
+  if constexpr (D == 256) {
+    return go<T, D, G, 2>(a, p, stream);
+  } else {
+    return p.row_tiles == 2 ? go<T, D, G, 2>(a, p, stream) : go<T, D, G, 4>(a, p, stream);
+  }
+}
+
+template <typename T>
+hipError_t by_shape(const AttentionKernelArgs &a, const AttentionPlan &p, int d, int g, hipStream_t s) {
+  if (d == 64) return g == 32 ? by_rows<T, 64, 32>(a, p, s) : by_rows<T, 64, 64>(a, p, s);
+  if (d == 128)
+    return g == 32 ? by_rows<T, 128, 32>(a, p, s) : g == 64 ? by_rows<T, 128, 64>(a, p, s) : by_rows<T, 128, 128>(a, p, s);
+  return g == 32 ? by_rows<T, 256, 32>(a, p, s) : g == 64 ? by_rows<T, 256, 64>(a, p, s) : by_rows<T, 256, 128>(a, p, s);
+}
+
+}  // namespace
+
+hipError_t launch_attention(const AttentionKernelArgs &a, const AttentionPlan &p, int32_t head_dim, int32_t group_size,
+                            int32_t dtype, hipStream_t stream) {
+  return dtype == I4S_F16 ? by_shape<F16>(a, p, head_dim, group_size, stream)
+                          : by_shape<BF16>(a, p, head_dim, group_size, stream);
+}
+
+}  // namespace i4s

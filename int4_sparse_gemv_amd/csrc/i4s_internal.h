@@ -9,6 +9,20 @@
 
 namespace i4s {
 
+// Host-layer helpers (i4s_api.cpp) shared by the entry points.  fail records
+// the calling thread's message and returns its status; check_device accepts
+// gfx950 only.
+i4s_status fail(i4s_status st, const char *fmt, ...);
+i4s_status device_error(hipError_t e, const char *what);
+i4s_status check_device();
+
+inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+inline bool overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+  return pa < pb + nb && pb < pa + na;
+}
+
 // Columns covered by one "segment": the unit of work of a pack thread and of
 // a GEMV lane.  Every supported group size (64, 128, 256) is a multiple of it,
 // so a segment never straddles two quantization groups.

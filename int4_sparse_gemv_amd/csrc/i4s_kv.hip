@@ -1,0 +1,377 @@
+// The paged 4-bit KV cache: block tables and slot maps from request lengths,
+// and the kernels that write tokens into the cache and read them back.  The
+// format is that of include/i4s_serve.h.
+
+#include <hip/hip_bf16.h>
+#include <hip/hip_fp16.h>
+
+#include "i4s_serve_internal.h"
+
+namespace i4s {
+namespace {
+
+typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
+typedef float f8_t __attribute__((ext_vector_type(8)));
+
+constexpr float kScaleMax = 9352.0f;  // largest fp16 whose 7-fold is finite in fp16
+
+// ---------------------------------------------------------------------------
+// block tables and slot maps
+//
+// Every block sums the lengths of all requests by itself (n is at most a few
+// thousand 4-byte words, which stay in L2): exclusive sums of the new tokens
+// and of the new pages go to LDS, and each thread then finds the owner of a
+// token, or of a new page, by bisection there.  So one launch does it all,
+// with no block waiting for another: a token's page is either in the part of
+// the table that the call does not write, or follows from the page sums and
+// the free list without reading the table.
+
+struct Sums {
+  long long tokens, pages;
+};
+
+__global__ __launch_bounds__(1024) void kv_extend_kernel(ExtendArgs a) {
+  extern __shared__ int32_t lds[];
+  __shared__ Sums wave_sums[16];
+  __shared__ int32_t any_flags;
+  int32_t *token_start = lds;              // [n + 1]
+  int32_t *page_start = lds + a.n + 1;     // [n + 1]
+  const int threads = blockDim.x, tid = threadIdx.x, lane = tid % 64, wave = tid / 64, waves = threads / 64;
+  const int page = 1 << a.shift;
+  if (tid == 0) any_flags = 0;
+
+  const int per = (a.n + threads - 1) / threads;
+  const int first = min(tid * per, a.n), last = min(first + per, a.n);
+  Sums mine = {0, 0};
+  int32_t flags = 0;
+  for (int i = first; i < last; ++i) {
+    const long long have = a.lens[i], more = a.new_lens[i];
+    if (have < 0 || more < 0 || have + more > 0x7FFFFFFFll) {
+      flags |= I4S_KV_BAD_LENGTH;
+      continue;
+    }
+    const long long old_pages = (have + page - 1) >> a.shift, pages = (have + more + page - 1) >> a.shift;
+    if (pages > a.width) flags |= I4S_KV_ROW_FULL;
+    mine.tokens += more;
+    mine.pages += pages - old_pages;
+  }
+  Sums sum = mine;  // inclusive over the wave
+  for (int d = 1; d < 64; d <<= 1) {
+    const long long t = __shfl_up(sum.tokens, d), p = __shfl_up(sum.pages, d);
+    if (lane >= d) {
+      sum.tokens += t;
+      sum.pages += p;
+    }
+  }
+  if (lane == 63) wave_sums[wave] = sum;
+  __syncthreads();
+  if (flags) atomicOr(&any_flags, flags);
+  Sums before = {sum.tokens - mine.tokens, sum.pages - mine.pages}, total = {0, 0};
+  for (int w = 0; w < waves; ++w) {
+    if (w < wave) {
+      before.tokens += wave_sums[w].tokens;
+      before.pages += wave_sums[w].pages;
+    }
+    total.tokens += wave_sums[w].tokens;
+    total.pages += wave_sums[w].pages;
+  }
+  const int32_t count = *a.free_count;
+  __syncthreads();
+  int32_t all = any_flags;
+  if (count < 0 || count > a.free_entries) all |= I4S_KV_BAD_COUNT;
+  if (total.pages > (count < 0 ? 0 : count)) all |= I4S_KV_NO_PAGES;
+  if (total.tokens > a.capacity) all |= I4S_KV_NO_SLOTS;
+  const bool fine = all == 0;
+
+  if (blockIdx.x == 0) {
+    if (tid == 0) {
+      *a.flags = all;
+      *a.free_count_out = fine ? count - (int32_t)total.pages : count;
+      a.q_start[a.n] = fine ? (int32_t)total.tokens : 0;
+    }
+    long long t = before.tokens;
+    for (int i = first; i < last; ++i) {
+      const int32_t have = a.lens[i], more = a.new_lens[i];
+      a.lens_out[i] = fine ? have + more : have;
+      a.q_start[i] = fine ? (int32_t)t : 0;
+      t += more;
+    }
+  }
+  if (fine) {
+    Sums at = before;
+    for (int i = first; i < last; ++i) {
+      const long long have = a.lens[i], more = a.new_lens[i];
+      token_start[i] = (int32_t)at.tokens;
+      page_start[i] = (int32_t)at.pages;
+      at.tokens += more;
+      at.pages += ((have + more + page - 1) >> a.shift) - ((have + page - 1) >> a.shift);
+    }
+  }
+  __syncthreads();
+
+  // the last request that starts at or before place v: the owner of v
+  const auto owner = [&](const int32_t *start, int32_t v) {
+    int lo = 0, hi = a.n;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (start[mid] <= v) lo = mid; else hi = mid;
+    }
+    return lo;
+  };
+  const int32_t tokens = fine ? (int32_t)total.tokens : 0, pages = fine ? (int32_t)total.pages : 0;
+  const int64_t step = (int64_t)gridDim.x * threads;
+  for (int64_t v = (int64_t)blockIdx.x * threads + tid; v < a.capacity; v += step) {
+    if (v >= tokens) {
+      a.slots[v] = -1;
+      a.positions[v] = 0;
+      continue;
+    }
+    const int i = owner(token_start, (int32_t)v);
+    const int32_t have = a.lens[i];
+    const int32_t pos = have + ((int32_t)v - token_start[i]);
+    const int32_t old_pages = (int32_t)(((int64_t)have + page - 1) >> a.shift), p = pos >> a.shift;
+    const int32_t number = p < old_pages ? a.table[(int64_t)i * a.width + p]
+                                         : a.free_pages[count - 1 - (page_start[i] + (p - old_pages))];
+    a.slots[v] = (int32_t)(((uint32_t)number << a.shift) + (uint32_t)(pos & (page - 1)));
+    a.positions[v] = pos;
+    if (v < pages) {  // every new page holds a new token, so pages <= tokens
+      const int j = owner(page_start, (int32_t)v);
+      const int32_t entry = (int32_t)(((int64_t)a.lens[j] + page - 1) >> a.shift) + ((int32_t)v - page_start[j]);
+      a.table[(int64_t)j * a.width + entry] = a.free_pages[count - 1 - (int32_t)v];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// element types
+
+struct Half {
+  static __device__ float to_float(uint32_t bits) { return (float)__builtin_bit_cast(_Float16, (uint16_t)bits); }
+  static __device__ uint32_t from_float(float f) { return __builtin_bit_cast(uint16_t, (_Float16)f); }
+};
+struct Bfloat {
+  static __device__ float to_float(uint32_t bits) { return __builtin_bit_cast(float, bits << 16); }
+  static __device__ uint32_t from_float(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+};
+
+template <typename T>
+__device__ inline f8_t load8(const uint16_t *p) {
+  const u4_t w = *reinterpret_cast<const u4_t *>(p);
+  f8_t x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = T::to_float(w[i] & 0xFFFFu);
+    x[2 * i + 1] = T::to_float(w[i] >> 16);
+  }
+  return x;
+}
+
+// ---------------------------------------------------------------------------
+// writing tokens
+//
+// D/8 neighbouring lanes take one (token, head): a lane quantizes 8 channels
+// (one 16-byte load), the group maximum goes across the G/8 lanes of a group.
+// For K the lane's 8 nibbles are one word of the row.  For V the four lanes
+// that hold channels 16e + 8b .. +7 (e = 0..3) of one 64-channel block
+// exchange their words (three lane exchanges), and each writes two of the
+// eight 16-bit halves.  The work is a read of 16-bit values and a write of a
+// little over a quarter of that: bound by memory.
+
+// The 8 nibbles (in channel order) and the scale of the lane's channels.
+template <int G>
+__device__ inline uint32_t quantize8(const f8_t &x, uint32_t &scale_bits) {
+  float m = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));  // fmaxf passes over a NaN
+#pragma unroll
+  for (int d = 1; d < G / 8; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+  const _Float16 h = (_Float16)fminf(m / 7.0f, kScaleMax);
+  const float s = (float)h;
+  scale_bits = __builtin_bit_cast(uint16_t, h);
+  uint32_t word = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float q = 0.0f;
+    if (s > 0.0f && x[e] == x[e]) q = fminf(fmaxf(rintf(x[e] / s), -7.0f), 7.0f);
+    word |= (uint32_t)((int)q + 8) << (4 * e);
+  }
+  return word;
+}
+
+template <typename T, int D, int G>
+__global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a, int shift) {
+  constexpr int kLanes = D / 8;
+  const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) / kLanes;
+  const int l = threadIdx.x % kLanes;
+  const int heads = a.cache.kv_heads;
+  const int64_t units = (int64_t)a.tokens * heads;
+  // all lanes of a wave stay: the exchanges below go across lanes
+  const bool has = unit < units;
+  const int64_t u = has ? unit : units - 1;
+  const int token = (int)(u / heads), head = (int)(u % heads);
+  const int32_t slot = a.slots[token];
+  const int page_size = 1 << shift;
+  const bool store = has && slot >= 0 && (slot >> shift) < a.cache.num_pages;
+
+  const f8_t xk = load8<T>(static_cast<const uint16_t *>(a.k) + token * a.k_token + head * a.k_head + 8 * l);
+  const f8_t xv = load8<T>(static_cast<const uint16_t *>(a.v) + token * a.v_token + head * a.v_head + 8 * l);
+  uint32_t sk, sv;
+  const uint32_t wk = quantize8<G>(xk, sk);
+  const uint32_t wv = quantize8<G>(xv, sv);
+
+  // K: slot k of the word takes element (0,2,4,6,1,3,5,7)[k]
+  uint32_t word = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) word |= ((wk >> (4 * e)) & 15u) << (4 * (e / 2 + 4 * (e % 2)));
+
+  // V: lane l holds block c = l / 8, e = l % 8 / 2, b = l % 2; it collects the
+  // words of the four e and makes halves x = 2e and 2e + 1 of i = 8b + x
+  const int e = l % 8 / 2, b = l % 2, c = l / 8;
+  uint32_t halves[2] = {0, 0};
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const uint32_t other = d ? __shfl_xor(wv, 2 * d) : wv;
+    const int from = e ^ d;
+    halves[0] |= ((other >> (8 * e)) & 15u) << (4 * from);
+    halves[1] |= ((other >> (8 * e + 4)) & 15u) << (4 * from);
+  }
+  if (!store) return;
+
+  const int64_t base = (int64_t)(slot >> shift) * heads + head;
+  const int off = slot & (page_size - 1);
+  uint32_t *kv = reinterpret_cast<uint32_t *>(a.cache.k_vals + (base * page_size + off) * (D / 2));
+  kv[(D / 32) * (l % 4) + l / 4] = word;
+  uint16_t *vv = reinterpret_cast<uint16_t *>(a.cache.v_vals + (base * page_size + (off & ~3)) * (D / 2));
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int half = (8 * b + 2 * e + k) * (D / 64) + c;
+    vv[(half / 2) * 8 + (off & 3) * 2 + half % 2] = (uint16_t)halves[k];
+  }
+  if (l % (G / 8) == 0) {
+    const int64_t at = (base * page_size + (off & ~3)) * (D / G) + (l / (G / 8)) * 4 + (off & 3);
+    a.cache.k_scales[at] = (uint16_t)sk;
+    a.cache.v_scales[at] = (uint16_t)sv;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// reading tokens: the same lanes the other way round
+
+template <typename T>
+__device__ inline void store8(void *p, int64_t at, const f8_t &x) {
+  u4_t w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = T::from_float(x[2 * i]) | T::from_float(x[2 * i + 1]) << 16;
+  *reinterpret_cast<u4_t *>(static_cast<uint16_t *>(p) + at) = w;
+}
+struct Float {};
+template <>
+__device__ inline void store8<Float>(void *p, int64_t at, const f8_t &x) {
+  *reinterpret_cast<f8_t *>(static_cast<float *>(p) + at) = x;
+}
+
+template <typename T, int D, int G>
+__global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs a, int shift) {
+  constexpr int kLanes = D / 8;
+  const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) / kLanes;
+  const int l = threadIdx.x % kLanes;
+  const int heads = a.cache.kv_heads;
+  const int64_t units = (int64_t)a.tokens * heads;
+  const bool has = unit < units;
+  const int64_t u = has ? unit : units - 1;
+  const int token = (int)(u / heads), head = (int)(u % heads);
+  const int32_t slot = a.slots[token];
+  const int page_size = 1 << shift;
+  const bool inside = slot >= 0 && (slot >> shift) < a.cache.num_pages;
+  const int64_t base = (int64_t)(inside ? slot >> shift : 0) * heads + head;
+  const int off = inside ? slot & (page_size - 1) : 0;
+
+  const uint32_t *kv = reinterpret_cast<const uint32_t *>(a.cache.k_vals + (base * page_size + off) * (D / 2));
+  const uint32_t word = kv[(D / 32) * (l % 4) + l / 4];
+  const uint16_t *vv = reinterpret_cast<const uint16_t *>(a.cache.v_vals + (base * page_size + (off & ~3)) * (D / 2));
+  const int e = l % 8 / 2, b = l % 2, c = l / 8;
+  uint32_t two = 0;  // halves x = 2e and 2e + 1 of i = 8b + x
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int half = (8 * b + 2 * e + k) * (D / 64) + c;
+    two |= (uint32_t)vv[(half / 2) * 8 + (off & 3) * 2 + half % 2] << (16 * k);
+  }
+  const int64_t at = (base * page_size + (off & ~3)) * (D / G) + (l / (G / 8)) * 4 + (off & 3);
+  const float sk = Half::to_float(a.cache.k_scales[at]), sv = Half::to_float(a.cache.v_scales[at]);
+  f8_t xk, xv;
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    const float q = (float)((int)((word >> (4 * (x / 2 + 4 * (x % 2)))) & 15u) - 8);
+    xk[x] = inside ? sk * q : 0.0f;
+  }
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const uint32_t other = d ? __shfl_xor(two, 2 * d) : two;
+    // the lane e ^ d holds halves 2(e^d) and 2(e^d) + 1; channel x of this lane is nibble e of half x
+    const float q0 = (float)((int)((other >> (4 * e)) & 15u) - 8), q1 = (float)((int)((other >> (16 + 4 * e)) & 15u) - 8);
+    const float v0 = inside ? sv * q0 : 0.0f, v1 = inside ? sv * q1 : 0.0f;
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+      if ((e ^ d) == f) {
+        xv[2 * f] = v0;
+        xv[2 * f + 1] = v1;
+      }
+  }
+  if (!has) return;
+  const int64_t to = u * D + 8 * l;
+  store8<T>(a.k, to, xk);
+  store8<T>(a.v, to, xv);
+}
+
+unsigned grid_of(int64_t tokens, int heads, int head_dim) {
+  return (unsigned)((tokens * heads * (head_dim / 8) + 255) / 256);
+}
+
+template <template <typename, int, int> class Launch, typename T, typename A>
+hipError_t by_shape(const A &a, hipStream_t s) {
+  const int d = a.cache.head_dim, g = a.cache.group_size;
+  if (d == 64) return g == 32 ? Launch<T, 64, 32>::go(a, s) : Launch<T, 64, 64>::go(a, s);
+  if (d == 128)
+    return g == 32 ? Launch<T, 128, 32>::go(a, s) : g == 64 ? Launch<T, 128, 64>::go(a, s) : Launch<T, 128, 128>::go(a, s);
+  return g == 32 ? Launch<T, 256, 32>::go(a, s) : g == 64 ? Launch<T, 256, 64>::go(a, s) : Launch<T, 256, 128>::go(a, s);
+}
+
+template <typename T, int D, int G>
+struct Append {
+  static hipError_t go(const AppendArgs &a, hipStream_t s) {
+    hipLaunchKernelGGL((kv_append_kernel<T, D, G>), dim3(grid_of(a.tokens, a.cache.kv_heads, D)), dim3(256), 0, s, a,
+                       page_shift(a.cache.page_size));
+    return hipGetLastError();
+  }
+};
+
+template <typename T, int D, int G>
+struct Read {
+  static hipError_t go(const ReadArgs &a, hipStream_t s) {
+    hipLaunchKernelGGL((kv_read_kernel<T, D, G>), dim3(grid_of(a.tokens, a.cache.kv_heads, D)), dim3(256), 0, s, a,
+                       page_shift(a.cache.page_size));
+    return hipGetLastError();
+  }
+};
+
+}  // namespace
+
+hipError_t launch_kv_extend(const ExtendArgs &a, hipStream_t stream) {
+  const int threads = a.n <= 256 && a.capacity <= 4096 ? 256 : 1024;
+  const int64_t blocks = clamp_to<int64_t>(((int64_t)a.capacity + threads - 1) / threads, 1, 256);
+  const size_t lds = 2 * sizeof(int32_t) * ((size_t)a.n + 1);
+  hipLaunchKernelGGL(kv_extend_kernel, dim3((unsigned)blocks), dim3(threads), lds, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_append(const AppendArgs &a, int32_t dtype, hipStream_t stream) {
+  return dtype == I4S_F16 ? by_shape<Append, Half>(a, stream) : by_shape<Append, Bfloat>(a, stream);
+}
+
+hipError_t launch_kv_read(const ReadArgs &a, int32_t dtype, hipStream_t stream) {
+  return dtype == I4S_F16    ? by_shape<Read, Half>(a, stream)
+         : dtype == I4S_BF16 ? by_shape<Read, Bfloat>(a, stream)
+                             : by_shape<Read, Float>(a, stream);
+}
+
+}  // namespace i4s
