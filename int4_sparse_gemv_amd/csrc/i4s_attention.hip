@@ -69,32 +69,46 @@ struct BF16 {
 constexpr float kOffset = 24.0f;   // 16 of the widening + 8 of the nibble
 constexpr float kLowest = -1e38f;  // exponent offset of a row that has seen no key
 
-// (a & m) | c, one v_and_or_b32.  Left to the compiler here: it does not see
-// which registers an instruction in inline asm writes when it places the
-// waits that a VALU write to a matrix instruction's registers needs.
+// (a & m) | c.  In one v_and_or_b32 if the constants are in registers (the
+// instruction takes no literal): masks and magic numbers are made once, hidden
+// from the optimizer.  The instruction itself is left to the compiler: it does
+// not see which registers inline asm writes when it places the waits that a
+// VALU write to a matrix instruction's registers needs.
 __device__ inline uint32_t mask_or(uint32_t a, uint32_t m, uint32_t c) { return (a & m) | c; }
+__device__ inline uint32_t in_sgpr(uint32_t v) {
+  asm("" : "+s"(v));
+  return v;
+}
+__device__ inline uint32_t in_vgpr(uint32_t v) {
+  asm("" : "+v"(v));
+  return v;
+}
+
+struct Constants {
+  uint32_t k_mask, k_sixteen, v_low, v_high, v_magic;
+};
 
 // Nibbles p and p + 4 of w, p = 0..3, as exact fp16 pairs u - 8: the nibble
 // goes into the mantissa of 1024 at its place 0..3 or 4..7.
-__device__ inline void widen_v(uint32_t w, h2_t q[4]) {
-  const uint32_t magic = 0x64006400u, t = w >> 8;
+__device__ inline void widen_v(uint32_t w, const Constants &k, h2_t q[4]) {
+  const uint32_t t = w >> 8;
   const h2_t bias = {(_Float16)-1032.0f, (_Float16)-1032.0f};
   const h2_t sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
   const h2_t bias16 = {(_Float16)-72.0f, (_Float16)-72.0f};
-  q[0] = as_h2(mask_or(w, 0x000F000Fu, magic)) + bias;
-  q[2] = as_h2(mask_or(t, 0x000F000Fu, magic)) + bias;
-  q[1] = __builtin_elementwise_fma(as_h2(mask_or(w, 0x00F000F0u, magic)), sixteenth, bias16);
-  q[3] = __builtin_elementwise_fma(as_h2(mask_or(t, 0x00F000F0u, magic)), sixteenth, bias16);
+  q[0] = as_h2(mask_or(w, k.v_low, k.v_magic)) + bias;
+  q[2] = as_h2(mask_or(t, k.v_low, k.v_magic)) + bias;
+  q[1] = __builtin_elementwise_fma(as_h2(mask_or(w, k.v_high, k.v_magic)), sixteenth, bias16);
+  q[3] = __builtin_elementwise_fma(as_h2(mask_or(t, k.v_high, k.v_magic)), sixteenth, bias16);
 }
 
 // The eight channels of a K word as 16 + u.
 template <typename T>
-__device__ inline typename T::vec widen_k(uint32_t w) {
+__device__ inline typename T::vec widen_k(uint32_t w, const Constants &k) {
   w4_t r;
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     const int s = T::kShift - 4 * p;
-    r[p] = mask_or(s >= 0 ? w << (s & 31) : w >> (-s & 31), T::kMask, T::kSixteen);
+    r[p] = mask_or(s >= 0 ? w << (s & 31) : w >> (-s & 31), k.k_mask, k.k_sixteen);
   }
   return __builtin_bit_cast(typename T::vec, r);
 }
@@ -167,10 +181,16 @@ __device__ inline void load_words(uint32_t *to, const void *from) {
   }
 }
 
+// Waves a SIMD should hold (512 registers between them).
+template <int D, int RT>
+constexpr int waves_per_simd() {
+  return D * RT <= 64 ? 4 : (D * RT <= 128 ? 3 : (D * RT <= 256 ? 2 : 1));
+}
+
 template <typename T, int D, int G, int RT>
-__global__ __launch_bounds__(256) void attention_kernel(AttentionKernelArgs a) {
+__global__ __launch_bounds__(256, (waves_per_simd<D, RT>())) void attention_kernel(AttentionKernelArgs a) {
   constexpr int NG = D / G, KJ = D / 32, NC = D / 64;
-  constexpr bool kBiasInSum = NG * RT <= 8;  // else the registers are needed elsewhere
+  constexpr bool kBiasInSum = NG * RT <= (D == 256 ? 4 : 8);  // else the registers are needed elsewhere
   constexpr int kRowStride = D + 4;          // floats; the 16 rows of a store fall in distinct banks
   extern __shared__ float lds[];
   const int waves = blockDim.x / 64;
@@ -234,35 +254,44 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionKernelArgs a) {
   const int step1 = (key1 + kStepKeys - 1) / kStepKeys;
   const int last_tile = (w.len - 1) >> 4;
   const int tile_shift = a.shift - 4;
+  const Constants constants = {in_sgpr(T::kMask), in_vgpr(T::kSixteen), in_sgpr(0x000F000Fu), in_sgpr(0x00F000F0u),
+                               in_vgpr(0x64006400u)};
   const int32_t *row_of_table = a.table + (int64_t)seq * a.width;
 
   const auto page_of = [&](int s, int t) {
     const int tile = min(2 * s + t, last_tile);
     return row_of_table[tile >> tile_shift];
   };
-  const auto load = [&](Step<D, G> &st, int s, const int32_t(&page)[2]) {
+  // where tile t of step s begins, in tokens of one head
+  const auto token_of = [&](int s, int t, int32_t page) {
+    const int tile = min(2 * s + t, last_tile);
+    const int64_t number = clamp_to(page, 0, a.num_pages - 1);
+    return ((number * a.kv_heads + head) << a.shift) + ((tile & ((1 << tile_shift) - 1)) << 4);
+  };
+  Step<D, G> st;
+  const auto load_k = [&](const int64_t(&token)[2]) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int tile = min(2 * s + t, last_tile);
-      const int64_t number = clamp_to(page[t], 0, a.num_pages - 1);
-      const int64_t token = ((number * a.kv_heads + head) << a.shift) + ((tile & ((1 << tile_shift) - 1)) << 4);
-      load_words<KJ>(st.k[t], a.k_vals + token * (D / 2) + (li * (D / 2) + la * (D / 8)));
-      load_words<Step<D, G>::kVWords>(st.v[t], a.v_vals + token * (D / 2) + la * (2 * D) +
+      load_words<KJ>(st.k[t], a.k_vals + token[t] * (D / 2) + (li * (D / 2) + la * (D / 8)));
+      load_words<2 * NG>(&st.ks[t][0][0], a.k_scales + token[t] * NG + la * (4 * NG));
+    }
+  };
+  const auto load_v = [&](const int64_t(&token)[2]) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      load_words<Step<D, G>::kVWords>(st.v[t], a.v_vals + token[t] * (D / 2) + la * (2 * D) +
                                                    (D == 64 ? (li / 2) * 16 : li * (D / 8)));
-      load_words<2 * NG>(&st.ks[t][0][0], a.k_scales + token * NG + la * (4 * NG));
-      load_words<2 * NG>(&st.vs[t][0][0], a.v_scales + token * NG + la * (4 * NG));
+      load_words<2 * NG>(&st.vs[t][0][0], a.v_scales + token[t] * NG + la * (4 * NG));
     }
   };
 
-  const auto compute = [&](Step<D, G> &st, int s) {
-    const int key = s * kStepKeys;
-    const bool edge = key + kStepKeys > w.ctx;  // some key is not seen by every row
-    f4_t sc[RT][2];
+  f4_t sc[RT][2];
+  const auto scores = [&]() {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       typename T::vec kf[KJ];
 #pragma unroll
-      for (int j = 0; j < KJ; ++j) kf[j] = widen_k<T>(st.k[t][j]);
+      for (int j = 0; j < KJ; ++j) kf[j] = widen_k<T>(st.k[t][j], constants);
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         f4_t sum = {0, 0, 0, 0};
@@ -281,6 +310,10 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionKernelArgs a) {
         sc[r][t] = sum;
       }
     }
+  };
+  const auto values = [&](int s) {
+    const int key = s * kStepKeys;
+    const bool edge = key + kStepKeys > w.ctx;  // some key is not seen by every row
     if (edge) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -365,8 +398,8 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionKernelArgs a) {
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            p[r][g][4 * t + x] =
-                (_Float16)(e[t][x] * fp16_bits_to_float((st.vs[t][g][x / 2] >> (16 * (x % 2))) & 0xFFFFu));
+            p[r][g][4 * t + x] =  // one v_fma_mixlo/hi_f16: rounded once
+                (_Float16)fmaf(e[t][x], fp16_bits_to_float((st.vs[t][g][x / 2] >> (16 * (x % 2))) & 0xFFFFu), 0.0f);
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -377,7 +410,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionKernelArgs a) {
         for (int x = 0; x < 2; ++x) {
           const uint32_t w0 = st.v[t][4 * (c / 2) + 2 * x], w1 = st.v[t][4 * (c / 2) + 2 * x + 1];
           const uint32_t upper = D == 64 ? (uint32_t)(li & 1) : (uint32_t)(c & 1);
-          widen_v(__builtin_amdgcn_perm(w1, w0, upper ? 0x07060302u : 0x05040100u), vq[t][x]);
+          widen_v(__builtin_amdgcn_perm(w1, w0, upper ? 0x07060302u : 0x05040100u), constants, vq[t][x]);
         }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -391,31 +424,31 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionKernelArgs a) {
     }
   };
 
-  // Two sets of registers: one step loads while the other computes.  Loads
-  // past the wave's last step read that step again (unconditional loads: with
-  // a branch around them every wait would be for all of them).
+  // The keys of the next step load while this one's values are computed, its
+  // values while the next one's scores are: one set of registers.  Loads past
+  // the wave's last step read that step again (unconditional loads: with a
+  // branch around them every wait would be for all of them).
   const int first = key0 / kStepKeys + wave;
   if (first < step1) {
     const int final_step = first + (step1 - 1 - first) / waves * waves;
-    const auto clip = [&](int s) { return min(s, final_step); };
-    Step<D, G> even, odd;
     int32_t page[2] = {page_of(first, 0), page_of(first, 1)};
-    load(even, first, page);
-    int32_t next[2] = {page_of(clip(first + waves), 0), page_of(clip(first + waves), 1)};
-    int s = first;
-    while (true) {
-      load(odd, clip(s + waves), next);
-      page[0] = page_of(clip(s + 2 * waves), 0), page[1] = page_of(clip(s + 2 * waves), 1);
+    int64_t token[2] = {token_of(first, 0, page[0]), token_of(first, 1, page[1])};
+    load_k(token);
+    load_v(token);
+    int next = min(first + waves, final_step);
+    page[0] = page_of(next, 0), page[1] = page_of(next, 1);
+    for (int s = first; s < step1; s += waves) {
+      scores();
+      token[0] = token_of(next, 0, page[0]), token[1] = token_of(next, 1, page[1]);
       issue_fence();
-      compute(even, s);
-      s += waves;
-      if (s >= step1) break;
-      load(even, clip(s + waves), page);
-      next[0] = page_of(clip(s + 2 * waves), 0), next[1] = page_of(clip(s + 2 * waves), 1);
+      load_k(token);
+      next = min(s + 2 * waves, final_step);
+      page[0] = page_of(next, 0), page[1] = page_of(next, 1);
       issue_fence();
-      compute(odd, s);
-      s += waves;
-      if (s >= step1) break;
+      values(s);
+      issue_fence();
+      load_v(token);
+      issue_fence();
     }
   }
 
@@ -482,31 +515,43 @@ template <typename T, int D>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionKernelArgs a) {
   constexpr int kGroups = 1024 / D;
   __shared__ f4_t part[256];
-  __shared__ float sums[kGroups];
+  __shared__ float weight[kMaxSplits], wave_m[4], wave_l[4];
   const int q_heads = a.kv_heads * a.share;
   const Work w = work_of(a, blockIdx.y);
   const int t = blockIdx.x / q_heads;
   if (t >= min(w.q_len, a.max_q) || w.used == 1) return;
   const int64_t rows = (int64_t)a.num_tokens * q_heads;
   const int64_t row = (int64_t)(w.q0 + t) * q_heads + blockIdx.x % q_heads;
+  const int tid = threadIdx.x;
   float m = kLowest;
-  for (int s = 0; s < w.used; ++s) m = fmaxf(m, a.part_ml[2 * (s * rows + row)]);
-  const int group = threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
-  f4_t v = {0, 0, 0, 0};
-  float sum = 0.0f;
-  for (int s = group; s < w.used; s += kGroups) {
-    const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * (s * rows + row)] - m);
-    sum = fmaf(a.part_ml[2 * (s * rows + row) + 1], f, sum);
-    v += *reinterpret_cast<const f4_t *>(a.part_o + (s * rows + row) * D + d) * f;
+  for (int s = tid; s < w.used; s += 256) {
+    const float e = a.part_ml[2 * (s * rows + row)];
+    weight[s] = e;
+    m = fmaxf(m, e);
   }
-  part[threadIdx.x] = v;
-  if (d == 0) sums[group] = sum;
+  for (int d = 32; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+  if (tid % 64 == 0) wave_m[tid / 64] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(wave_m[0], wave_m[1]), fmaxf(wave_m[2], wave_m[3]));
+  float sum = 0.0f;
+  for (int s = tid; s < w.used; s += 256) {
+    const float f = __builtin_amdgcn_exp2f(weight[s] - m);
+    weight[s] = f;
+    sum = fmaf(a.part_ml[2 * (s * rows + row) + 1], f, sum);
+  }
+  for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+  if (tid % 64 == 0) wave_l[tid / 64] = sum;
+  __syncthreads();
+  sum = (wave_l[0] + wave_l[1]) + (wave_l[2] + wave_l[3]);
+  const int group = tid / (D / 4), d = tid % (D / 4) * 4;
+  f4_t v = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int s = group; s < w.used; s += kGroups)
+    v += *reinterpret_cast<const f4_t *>(a.part_o + (s * rows + row) * D + d) * weight[s];
+  part[tid] = v;
   __syncthreads();
   if (group) return;
-  for (int g = 1; g < kGroups; ++g) {
-    v += part[g * (D / 4) + threadIdx.x];
-    sum += sums[g];
-  }
+  for (int g = 1; g < kGroups; ++g) v += part[g * (D / 4) + tid];
   v *= sum == 0.0f ? 0.0f : 1.0f / sum;
   const w2_t bits = {T::from_float(v[0]) | T::from_float(v[1]) << 16, T::from_float(v[2]) | T::from_float(v[3]) << 16};
   *reinterpret_cast<w2_t *>(static_cast<uint16_t *>(a.out) + row * D + d) = bits;

@@ -156,10 +156,10 @@ AttentionPlan attention_plan(const i4s_attention_args &a) {
   const int64_t units = (int64_t)p.row_blocks * c.kv_heads * (a.num_seqs > 0 ? a.num_seqs : 1);
   const int64_t step = kStepKeys * p.waves;
   const int64_t steps = (len + step - 1) / step;
-  const int64_t want = clamp_to<int64_t>((768 + units - 1) / units, 1, 4096);
+  const int64_t want = clamp_to<int64_t>((768 + units - 1) / units, 1, kMaxSplits);
   const int64_t per = clamp_to<int64_t>((steps + want - 1) / want, 1, steps > 0 ? steps : 1);
   p.chunk = (int)(per * step);
-  p.splits = (int)clamp_to<int64_t>((steps + per - 1) / per, 1, 4096);
+  p.splits = (int)clamp_to<int64_t>((steps + per - 1) / per, 1, kMaxSplits);
   if (p.splits > 1)
     p.workspace_bytes = (uint64_t)p.splits * a.num_tokens * a.q_heads * (c.head_dim + 4) * sizeof(float);
   return p;

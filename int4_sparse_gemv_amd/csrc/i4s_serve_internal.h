@@ -61,6 +61,8 @@ struct AttentionPlan {
 };
 AttentionPlan attention_plan(const i4s_attention_args &a);
 
+constexpr int kMaxSplits = 4096;
+
 // Keys of one step of a wave.
 constexpr int kStepKeys = 32;
 
