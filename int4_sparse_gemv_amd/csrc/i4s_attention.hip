@@ -159,23 +159,48 @@ __device__ inline Work work_of(const AttentionKernelArgs &a, int seq) {
   return w;
 }
 
-// The registers of one step of 32 keys (two tiles of 16) for one lane.
+// One step of 32 keys (two tiles of 16) of a wave in LDS.  The loads go there
+// directly (global_load_lds, 16 bytes a lane, lane after lane), so a step on
+// its way costs no registers.  Where a lane's share of a tile is 16 bytes or
+// more its 16-byte pieces lie at [piece][lane]; for D = 64 the tile lies as in
+// the cache.
 template <int D, int G>
-struct Step {
-  static constexpr int kVWords = D == 256 ? 8 : 4;
-  uint32_t k[2][D / 32], v[2][kVWords];
-  uint32_t ks[2][D / G][2], vs[2][D / G][2];  // fp16 scales of four keys
+struct Stage {
+  static constexpr int NG = D / G;
+  static constexpr int kTile = 8 * D;               // bytes of K, and of V, of 16 keys
+  static constexpr int kScales = 32 * NG;           // bytes of K's scales, and of V's, of 16 keys
+  static constexpr int kV = 2 * kTile, kKs = 4 * kTile, kVs = kKs + 2 * kScales;
+  static constexpr int kBytes = kVs + 2 * kScales;  // 32 D + 128 NG
+  static constexpr int kLoads = (D == 64 ? 2 : D / 32) + 1;  // load instructions of a step
+  static constexpr int kVWords = D == 256 ? 8 : 4;  // V words of a lane and tile
 };
+constexpr int kStages = 2;
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) const void global_void;
+typedef const __attribute__((address_space(4))) int32_t scalar_int32;  // read with scalar loads
+
+__device__ inline void copy16(const void *from, char *to) {
+  __builtin_amdgcn_global_load_lds((global_void *)from, (lds_void *)to, 16, 0, 0);
+}
+
+// Waits until at most N vector loads are on their way (s_waitcnt vmcnt).
+template <int N>
+__device__ inline void wait_loads() {
+  issue_fence();
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4 << 14));
+  issue_fence();
+}
 
 template <int N>
-__device__ inline void load_words(uint32_t *to, const void *from) {
+__device__ inline void read_words(uint32_t *to, const char *from) {
   if constexpr (N == 2) {
-    const w2_t x = *static_cast<const w2_t *>(from);
+    const w2_t x = *reinterpret_cast<const w2_t *>(from);
     to[0] = x.x, to[1] = x.y;
   } else {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-      const w4_t x = static_cast<const w4_t *>(from)[i];
+      const w4_t x = reinterpret_cast<const w4_t *>(from)[i];
       to[4 * i] = x.x, to[4 * i + 1] = x.y, to[4 * i + 2] = x.z, to[4 * i + 3] = x.w;
     }
   }
@@ -187,12 +212,17 @@ constexpr int waves_per_simd() {
   return D * RT <= 64 ? 4 : (D * RT <= 128 ? 3 : (D * RT <= 256 ? 2 : 1));
 }
 
+template <int D, int RT>
+constexpr int most_threads() {
+  return D * RT <= 128 ? 512 : 256;
+}
+
 template <typename T, int D, int G, int RT>
-__global__ __launch_bounds__(256, (waves_per_simd<D, RT>())) void attention_kernel(AttentionKernelArgs a) {
+__global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>())) void attention_kernel(AttentionKernelArgs a) {
   constexpr int NG = D / G, KJ = D / 32, NC = D / 64;
   constexpr bool kBiasInSum = NG * RT <= (D == 256 ? 4 : 8);  // else the registers are needed elsewhere
   constexpr int kRowStride = D + 4;          // floats; the 16 rows of a store fall in distinct banks
-  extern __shared__ float lds[];
+  extern __shared__ __align__(16) float lds[];
   const int waves = blockDim.x / 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int lane = threadIdx.x % 64, li = lane % 16, la = lane / 16;
@@ -256,32 +286,62 @@ __global__ __launch_bounds__(256, (waves_per_simd<D, RT>())) void attention_kern
   const int tile_shift = a.shift - 4;
   const Constants constants = {in_sgpr(T::kMask), in_vgpr(T::kSixteen), in_sgpr(0x000F000Fu), in_sgpr(0x00F000F0u),
                                in_vgpr(0x64006400u)};
-  const int32_t *row_of_table = a.table + (int64_t)seq * a.width;
+  scalar_int32 *row_of_table = (scalar_int32 *)(uintptr_t)(a.table + (int64_t)seq * a.width);
 
-  const auto page_of = [&](int s, int t) {
+  typedef Stage<D, G> St;
+  char *stages = reinterpret_cast<char *>(lds) + wave * (kStages * St::kBytes);
+  // first token of tile t of step s in the cache's arrays of one head
+  const auto token_of = [&](int s, int t) {
     const int tile = min(2 * s + t, last_tile);
-    return row_of_table[tile >> tile_shift];
-  };
-  // where tile t of step s begins, in tokens of one head
-  const auto token_of = [&](int s, int t, int32_t page) {
-    const int tile = min(2 * s + t, last_tile);
-    const int64_t number = clamp_to(page, 0, a.num_pages - 1);
+    const int64_t number = clamp_to(row_of_table[tile >> tile_shift], 0, a.num_pages - 1);
     return ((number * a.kv_heads + head) << a.shift) + ((tile & ((1 << tile_shift) - 1)) << 4);
   };
-  Step<D, G> st;
-  const auto load_k = [&](const int64_t(&token)[2]) {
+  // this lane's piece of the 8 NG pieces of scales: array, tile, place
+  const uint16_t *my_scales = lane / (4 * NG) ? a.v_scales : a.k_scales;
+  const bool my_tile = lane / (2 * NG) % 2;
+  const int my_piece = lane % (2 * NG) * 8;
+  const auto load = [&](int s, char *to) {
+    const int64_t token[2] = {token_of(s, 0), token_of(s, 1)};
+    if constexpr (D == 64) {
+      const int64_t mine = (lane / 32 ? token[1] : token[0]) * (D / 2) + lane % 32 * 16;
+      copy16(a.k_vals + mine, to);
+      copy16(a.v_vals + mine, to + St::kV);
+    } else {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int h = 0; h < D / 128; ++h) {
+          copy16(a.k_vals + token[t] * (D / 2) + (li * (D / 2) + la * (D / 8) + 16 * h), to + t * St::kTile + 1024 * h);
+          copy16(a.v_vals + token[t] * (D / 2) + (la * (2 * D) + li * (D / 8) + 16 * h), to + St::kV + t * St::kTile + 1024 * h);
+        }
+    }
+    if (lane < 8 * NG) copy16(my_scales + (my_tile ? token[1] : token[0]) * NG + my_piece, to + St::kKs);
+  };
+  struct {
+    uint32_t k[2][KJ], v[2][St::kVWords];
+    uint32_t ks[2][NG][2], vs[2][NG][2];  // fp16 scales of four keys
+  } st;
+  const auto read_k = [&](const char *from) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      load_words<KJ>(st.k[t], a.k_vals + token[t] * (D / 2) + (li * (D / 2) + la * (D / 8)));
-      load_words<2 * NG>(&st.ks[t][0][0], a.k_scales + token[t] * NG + la * (4 * NG));
+      const char *p = from + t * St::kTile;
+      if constexpr (D == 64) {
+        read_words<2>(st.k[t], p + li * 32 + la * 8);
+      } else {
+#pragma unroll
+        for (int h = 0; h < D / 128; ++h) read_words<4>(st.k[t] + 4 * h, p + 1024 * h + lane * 16);
+      }
+      read_words<2 * NG>(&st.ks[t][0][0], from + St::kKs + t * St::kScales + la * (8 * NG));
     }
   };
-  const auto load_v = [&](const int64_t(&token)[2]) {
+  const auto read_v = [&](const char *from) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      load_words<Step<D, G>::kVWords>(st.v[t], a.v_vals + token[t] * (D / 2) + la * (2 * D) +
-                                                   (D == 64 ? (li / 2) * 16 : li * (D / 8)));
-      load_words<2 * NG>(&st.vs[t][0][0], a.v_scales + token[t] * NG + la * (4 * NG));
+      const char *p = from + St::kV + t * St::kTile;
+#pragma unroll
+      for (int h = 0; h < (D + 127) / 128; ++h)
+        read_words<4>(st.v[t] + 4 * h, p + 1024 * h + (D == 64 ? la * 128 + li / 2 * 16 : lane * 16));
+      read_words<2 * NG>(&st.vs[t][0][0], from + St::kVs + t * St::kScales + la * (8 * NG));
     }
   };
 
@@ -424,33 +484,30 @@ __global__ __launch_bounds__(256, (waves_per_simd<D, RT>())) void attention_kern
     }
   };
 
-  // The keys of the next step load while this one's values are computed, its
-  // values while the next one's scores are: one set of registers.  Loads past
-  // the wave's last step read that step again (unconditional loads: with a
-  // branch around them every wait would be for all of them).
+  // Two steps are on their way or in use at any time; the last ones are not
+  // followed by others, so there the wait is for everything.
   const int first = key0 / kStepKeys + wave;
   if (first < step1) {
-    const int final_step = first + (step1 - 1 - first) / waves * waves;
-    int32_t page[2] = {page_of(first, 0), page_of(first, 1)};
-    int64_t token[2] = {token_of(first, 0, page[0]), token_of(first, 1, page[1])};
-    load_k(token);
-    load_v(token);
-    int next = min(first + waves, final_step);
-    page[0] = page_of(next, 0), page[1] = page_of(next, 1);
+    load(first, stages);
+    if (first + waves < step1) load(first + waves, stages + St::kBytes);
+    int at = 0;
     for (int s = first; s < step1; s += waves) {
+      char *stage = stages + at;
+      if (s + waves < step1) wait_loads<St::kLoads>(); else wait_loads<0>();
+      read_k(stage);
       scores();
-      token[0] = token_of(next, 0, page[0]), token[1] = token_of(next, 1, page[1]);
-      issue_fence();
-      load_k(token);
-      next = min(s + 2 * waves, final_step);
-      page[0] = page_of(next, 0), page[1] = page_of(next, 1);
-      issue_fence();
+      read_v(stage);
       values(s);
       issue_fence();
-      load_v(token);
-      issue_fence();
+      if (s + 2 * waves < step1) {
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this stage is read
+        issue_fence();
+        load(s + 2 * waves, stage);
+      }
+      at = St::kBytes - at;
     }
   }
+  __syncthreads();  // the stages make room for what follows
 
   // the waves join: offsets and sums first, then the outputs of one 16-row
   // tile at a time, each scaled to the common offset
@@ -560,7 +617,9 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionKernelArgs
 
 template <typename T, int D, int G, int RT>
 hipError_t go(const AttentionKernelArgs &a, const AttentionPlan &p, hipStream_t stream) {
-  const size_t lds = sizeof(float) * p.waves * (16 * RT * 2 + 16 * (D + 4));
+  const size_t join = sizeof(float) * p.waves * (16 * RT * 2 + 16 * (D + 4));
+  const size_t stages = (size_t)p.waves * kStages * Stage<D, G>::kBytes;
+  const size_t lds = join > stages ? join : stages;
   if (lds > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(attention_kernel<T, D, G, RT>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
