@@ -29,7 +29,7 @@
 // probabilities, which are rounded to fp16 once, after that.  So that no
 // probability loses bits to fp16's range the offset of the exponent includes
 // a power of two that brings (largest probability) x (largest V scale seen so
-// far) just below 2^15.
+// far) between 2^6 and 2^15.
 //
 // Bound by: memory.  A key of one head is D + 4D/G bytes.
 
@@ -68,6 +68,10 @@ struct BF16 {
 
 constexpr float kOffset = 24.0f;   // 16 of the widening + 8 of the nibble
 constexpr float kLowest = -1e38f;  // exponent offset of a row that has seen no key
+// A row's offset follows its running maximum only when that has grown by more
+// than this (log2): with 16 rows or more a wave some row's maximum grows in
+// most steps, and every change scales all of O.
+constexpr float kSlack = 8.0f;
 
 // (a & m) | c.  In one v_and_or_b32 if the constants are in registers (the
 // instruction takes no literal): masks and magic numbers are made once, hidden
@@ -131,9 +135,12 @@ __device__ inline Two quarters_of(float v) {
   const uint32_t a = s[0], b = s[1];
   return {__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)};
 }
+// v_maximum(3)_f32: unlike fmaxf it passes a NaN on, so its operands need no
+// quieting first.
+__device__ inline float maximum(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 __device__ inline float max4(float v) {
-  const Two h = halves_of(v), q = quarters_of(fmaxf(h.a, h.b));
-  return fmaxf(q.a, q.b);
+  const Two h = halves_of(v), q = quarters_of(maximum(h.a, h.b));
+  return maximum(q.a, q.b);
 }
 __device__ inline float sum4(float v) {
   const Two h = halves_of(v), q = quarters_of(h.a + h.b);
@@ -221,6 +228,9 @@ template <typename T, int D, int G, int RT>
 __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>())) void attention_kernel(AttentionKernelArgs a) {
   constexpr int NG = D / G, KJ = D / 32, NC = D / 64;
   constexpr bool kBiasInSum = NG * RT <= (D == 256 ? 4 : 8);  // else the registers are needed elsewhere
+  // V's scales go to the probabilities where those are few (16 RT rows x NG
+  // groups), else to the values: one more rounding to fp16, of the scaled value
+  constexpr bool kScaleV = NG * RT >= 8;
   constexpr int kRowStride = D + 4;          // floats; the 16 rows of a store fall in distinct banks
   extern __shared__ __align__(16) float lds[];
   const int waves = blockDim.x / 64;
@@ -279,7 +289,7 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
       for (int e = 0; e < 4; ++e) o[r][c][e] = f4_t{0, 0, 0, 0};
   }
   uint32_t cap = 0;   // fp16 bits: no V scale so far was larger
-  float cap_log2 = 0.0f;
+  float cap_log2 = kScaleV ? 15.0f - kSlack : 0.0f;
 
   const int step1 = (key1 + kStepKeys - 1) / kStepKeys;
   const int last_tile = (w.len - 1) >> 4;
@@ -400,6 +410,7 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
     }
     // the largest V scale of this lane's keys (fp16 bits of positive numbers order like the numbers)
     uint32_t top = 0;
+    if constexpr (!kScaleV) {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -411,22 +422,24 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
                                                                        __builtin_bit_cast(us2, st.vs[t][g][x])));
         }
     top = max(top & 0xFFFFu, top >> 16);
+    }
     bool grows = top > cap;
     float m_new[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      float m = fmaxf(fmaxf(fmaxf(sc[r][0][0], sc[r][0][1]), fmaxf(sc[r][0][2], sc[r][0][3])),
-                      fmaxf(fmaxf(sc[r][1][0], sc[r][1][1]), fmaxf(sc[r][1][2], sc[r][1][3])));
+      float m = sc[r][0][0];
+#pragma unroll
+      for (int x = 1; x < 8; ++x) m = maximum(m, sc[r][x / 4][x % 4]);
       m_new[r] = fmaxf(mx[r], max4(m));
-      grows |= m_new[r] > mx[r];
+      grows |= (m_new[r] - mx[r]) * a.scale_log2 > kSlack;
     }
     if (__any(grows)) {
-      if (__any(top > cap)) {
+      if (!kScaleV && __any(top > cap)) {
         uint32_t all = cap;  // the keys of lanes i, i + 16, i + 32, i + 48
 #pragma unroll
         for (int x = 0; x < 64; x += 16) all = max(all, (uint32_t)__builtin_amdgcn_readlane(top, x));
         cap = all | 0x3FFu;
-        cap_log2 = 29.0f - (float)(cap >> 10);  // 2^15 / 2^(exponent + 1); subnormal scales count as 2^-14
+        cap_log2 = 29.0f - kSlack - (float)(cap >> 10);  // 2^(15 - slack) / 2^(exponent + 1); subnormal: 2^-14
       }
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
@@ -441,7 +454,7 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
           for (int e = 0; e < 4; ++e) o[r][c][e] *= f;
       }
     }
-    hf8_t p[RT][NG];
+    hf8_t p[RT][kScaleV ? 1 : NG];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       float e[2][4];
@@ -453,12 +466,12 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
           l[r] += e[t][x];
         }
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
+      for (int g = 0; g < (kScaleV ? 1 : NG); ++g)
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            p[r][g][4 * t + x] =  // one v_fma_mixlo/hi_f16: rounded once
+            p[r][g][4 * t + x] = kScaleV ? (_Float16)e[t][x] :  // one v_fma_mixlo/hi_f16: rounded once
                 (_Float16)fmaf(e[t][x], fp16_bits_to_float((st.vs[t][g][x / 2] >> (16 * (x % 2))) & 0xFFFFu), 0.0f);
     }
 #pragma unroll
@@ -474,11 +487,18 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
         }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
+        const int g = (64 * c + 16 * e) / G;
+        if constexpr (kScaleV) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) vq[t][y][e] *= as_h2(st.vs[t][g][y]);
+        }
         const w4_t x = {__builtin_bit_cast(uint32_t, vq[0][0][e]), __builtin_bit_cast(uint32_t, vq[0][1][e]),
                         __builtin_bit_cast(uint32_t, vq[1][0][e]), __builtin_bit_cast(uint32_t, vq[1][1][e])};
 #pragma unroll
         for (int r = 0; r < RT; ++r)
-          o[r][c][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(hf8_t, x), p[r][(64 * c + 16 * e) / G],
+          o[r][c][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(hf8_t, x), p[r][kScaleV ? 0 : g],
                                                               o[r][c][e], 0, 0, 0);
       }
     }

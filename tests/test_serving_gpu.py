@@ -10,10 +10,13 @@ products of q with 16 + u, from -24 sum q: at most D + D/G + 8 roundings, each
 at most 2^-24 of what the sum of the absolute terms is, sum |q| (|k| + 24 s);
 a score off by d moves every probability by at most a factor exp(2d).  Below
 the normal range of fp16 a rounding is off by half the smallest step instead:
-2^-25 for an fp16 output, and 2^-25 for a probability times its V scale, which
-are scaled so that the largest scale's power of two lies at 2^14 when the
-probability is 1: 2^-39 of the largest scale for every key, times a value of
-at most 7.
+2^-25 for an fp16 output, and 2^-25 for a probability times its V scale.  Those
+are scaled so that the largest scale's power of two lies at 2^6 at least when
+the probability is that of the key that set the row's offset (a maximum when
+it was set, so the sum that divides is at least its 1): 2^-31 of the largest
+scale for every key, times a value of at most 7.  Where the values carry V's
+scale instead (wide blocks of rows) each is rounded once to fp16 too: another
+2^-11 of sum p |v|.
 """
 
 import itertools
@@ -262,6 +265,8 @@ def check_attention(i4s, rng, c, d, lens, q_lens, share, dtype, tree=False, scal
     i4s.kv_attention(d, q_dev, i32(table), i32(lens), out=out, lse=lse, **args)
     assert torch.equal(first, out), "two calls differ"
     got, got_lse = f64(out[:total]), f64(lse[:total])
+    rows = max(max(q_lens), 1) * share
+    wide = (1 if rows <= 16 else 2 if rows <= 32 or dim == 256 else 4) * (dim // c.group) >= 8
     for i, (l, n_q) in enumerate(zip(lens, q_lens)):
         slots = [int(table[i, j // page]) * page + j % page for j in range(l)]
         k, v = c.read(slots)
@@ -273,9 +278,9 @@ def check_attention(i4s, rng, c, d, lens, q_lens, share, dtype, tree=False, scal
         for h in range(heads * share if l else 0):
             terms[:, h] = (np.abs(qi[:, h]) @ (np.abs(k[:, h // share]) + 24 * s[:, h // share]).T).max(1)
         d_score = scale * terms * (dim + dim // c.group + 8) * 2.0**-24
-        weight = np.expm1(2 * d_score) + 2.0**-11 + (l + 64) * 2.0**-24
+        weight = np.expm1(2 * d_score) + (2 if wide else 1) * 2.0**-11 + (l + 64) * 2.0**-24
         v_top = 0.0 if not l else float(c.v_scales[table[i, :-(-l // page)]].max())
-        tol = half_step(dtype) * np.abs(want) + 1.01 * weight[..., None] * spread + l * 7 * 2.0**-39 * v_top
+        tol = half_step(dtype) * np.abs(want) + 1.01 * weight[..., None] * spread + l * 7 * 2.0**-31 * v_top
         tol += 2.0**-25 if dtype == F16 else 2.0**-134
         bad = np.abs(got[a:b] - want) > tol
         assert not bad.any(), (i, np.argwhere(bad)[:3], np.abs(got[a:b] - want)[bad][:3], tol[bad][:3])
