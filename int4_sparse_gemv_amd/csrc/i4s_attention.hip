@@ -237,16 +237,68 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int lane = threadIdx.x % 64, li = lane % 16, la = lane / 16;
 
-  const int rb = blockIdx.x % a.row_blocks;
-  const int head = (blockIdx.x / a.row_blocks) % a.kv_heads;
-  const int seq = blockIdx.x / a.row_blocks / a.kv_heads;
-  const int split = blockIdx.y;
+  // pieces of the same number first: all sequences have the first ones, only
+  // long ones the last, so what runs at the end is what fills gaps
+  const int seq = blockIdx.y, split = blockIdx.z;
+  int rb = 0, head = blockIdx.x;
+  if (a.row_blocks > 1) {
+    rb = head % a.row_blocks;
+    head /= a.row_blocks;
+  }
+  const int key0 = split * a.chunk;
+  const int tile_shift = a.shift - 4;
+  // The first step's page numbers come along with the lengths: whatever the
+  // length is, the row of the table has an entry there (of any value behind
+  // the sequence's end).
+  scalar_int32 *row_of_table = (scalar_int32 *)(uintptr_t)(a.table + (int64_t)seq * a.width);
+  const int first = key0 / kStepKeys + wave;
+  const int32_t early[2] = {row_of_table[min(2 * first >> tile_shift, a.width - 1)],
+                            row_of_table[min(2 * first + 1 >> tile_shift, a.width - 1)]};
   const Work w = work_of(a, seq);
   const int rows = min(w.q_len, a.max_q) * a.share;
   const int row0 = rb * 16 * RT;
   if (row0 >= rows || split >= w.used) return;
-  const int key0 = split * a.chunk;
   const int key1 = split == a.splits - 1 ? w.len : min(w.len, key0 + a.chunk);
+
+  const int step1 = (key1 + kStepKeys - 1) / kStepKeys;
+  const int last_tile = (w.len - 1) >> 4;
+
+  typedef Stage<D, G> St;
+  char *stages = reinterpret_cast<char *>(lds) + wave * (kStages * St::kBytes);
+  // first token of a tile in the cache's arrays of one head
+  const auto token_of = [&](int tile, int32_t page) {
+    const int64_t number = clamp_to(page, 0, a.num_pages - 1);
+    return ((number * a.kv_heads + head) << a.shift) + ((tile & ((1 << tile_shift) - 1)) << 4);
+  };
+  // this lane's piece of the 8 NG pieces of scales: array, tile, place
+  const uint16_t *my_scales = lane / (4 * NG) ? a.v_scales : a.k_scales;
+  const bool my_tile = lane / (2 * NG) % 2;
+  const int my_piece = lane % (2 * NG) * 8;
+  const auto load = [&](int64_t token0, int64_t token1, char *to) {
+    if constexpr (D == 64) {
+      const int64_t mine = (lane / 32 ? token1 : token0) * (D / 2) + lane % 32 * 16;
+      copy16(a.k_vals + mine, to);
+      copy16(a.v_vals + mine, to + St::kV);
+    } else {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int h = 0; h < D / 128; ++h) {
+          const int64_t token = t ? token1 : token0;
+          copy16(a.k_vals + token * (D / 2) + (li * (D / 2) + la * (D / 8) + 16 * h), to + t * St::kTile + 1024 * h);
+          copy16(a.v_vals + token * (D / 2) + (la * (2 * D) + li * (D / 8) + 16 * h), to + St::kV + t * St::kTile + 1024 * h);
+        }
+    }
+    if (lane < 8 * NG) copy16(my_scales + (my_tile ? token1 : token0) * NG + my_piece, to + St::kKs);
+  };
+  const auto load_step = [&](int s, char *to) {
+    const int tile0 = min(2 * s, last_tile), tile1 = min(2 * s + 1, last_tile);
+    load(token_of(tile0, row_of_table[tile0 >> tile_shift]), token_of(tile1, row_of_table[tile1 >> tile_shift]), to);
+  };
+  if (first < step1) {
+    load(token_of(2 * first, early[0]), token_of(2 * first + 1, early[1]), stages);
+    if (first + waves < step1) load_step(first + waves, stages + St::kBytes);
+  }
 
   // the query rows: lane (i, a) holds channels 32j + 8a .. +7 of row i
   typename T::vec q[RT][KJ];
@@ -291,42 +343,8 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
   uint32_t cap = 0;   // fp16 bits: no V scale so far was larger
   float cap_log2 = kScaleV ? 15.0f - kSlack : 0.0f;
 
-  const int step1 = (key1 + kStepKeys - 1) / kStepKeys;
-  const int last_tile = (w.len - 1) >> 4;
-  const int tile_shift = a.shift - 4;
   const Constants constants = {in_sgpr(T::kMask), in_vgpr(T::kSixteen), in_sgpr(0x000F000Fu), in_sgpr(0x00F000F0u),
                                in_vgpr(0x64006400u)};
-  scalar_int32 *row_of_table = (scalar_int32 *)(uintptr_t)(a.table + (int64_t)seq * a.width);
-
-  typedef Stage<D, G> St;
-  char *stages = reinterpret_cast<char *>(lds) + wave * (kStages * St::kBytes);
-  // first token of tile t of step s in the cache's arrays of one head
-  const auto token_of = [&](int s, int t) {
-    const int tile = min(2 * s + t, last_tile);
-    const int64_t number = clamp_to(row_of_table[tile >> tile_shift], 0, a.num_pages - 1);
-    return ((number * a.kv_heads + head) << a.shift) + ((tile & ((1 << tile_shift) - 1)) << 4);
-  };
-  // this lane's piece of the 8 NG pieces of scales: array, tile, place
-  const uint16_t *my_scales = lane / (4 * NG) ? a.v_scales : a.k_scales;
-  const bool my_tile = lane / (2 * NG) % 2;
-  const int my_piece = lane % (2 * NG) * 8;
-  const auto load = [&](int s, char *to) {
-    const int64_t token[2] = {token_of(s, 0), token_of(s, 1)};
-    if constexpr (D == 64) {
-      const int64_t mine = (lane / 32 ? token[1] : token[0]) * (D / 2) + lane % 32 * 16;
-      copy16(a.k_vals + mine, to);
-      copy16(a.v_vals + mine, to + St::kV);
-    } else {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int h = 0; h < D / 128; ++h) {
-          copy16(a.k_vals + token[t] * (D / 2) + (li * (D / 2) + la * (D / 8) + 16 * h), to + t * St::kTile + 1024 * h);
-          copy16(a.v_vals + token[t] * (D / 2) + (la * (2 * D) + li * (D / 8) + 16 * h), to + St::kV + t * St::kTile + 1024 * h);
-        }
-    }
-    if (lane < 8 * NG) copy16(my_scales + (my_tile ? token[1] : token[0]) * NG + my_piece, to + St::kKs);
-  };
   struct {
     uint32_t k[2][KJ], v[2][St::kVWords];
     uint32_t ks[2][NG][2], vs[2][NG][2];  // fp16 scales of four keys
@@ -506,26 +524,21 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
 
   // Two steps are on their way or in use at any time; the last ones are not
   // followed by others, so there the wait is for everything.
-  const int first = key0 / kStepKeys + wave;
-  if (first < step1) {
-    load(first, stages);
-    if (first + waves < step1) load(first + waves, stages + St::kBytes);
-    int at = 0;
-    for (int s = first; s < step1; s += waves) {
-      char *stage = stages + at;
-      if (s + waves < step1) wait_loads<St::kLoads>(); else wait_loads<0>();
-      read_k(stage);
-      scores();
-      read_v(stage);
-      values(s);
+  int at = 0;
+  for (int s = first; s < step1; s += waves) {
+    char *stage = stages + at;
+    if (s + waves < step1) wait_loads<St::kLoads>(); else wait_loads<0>();
+    read_k(stage);
+    scores();
+    read_v(stage);
+    values(s);
+    issue_fence();
+    if (s + 2 * waves < step1) {
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this stage is read
       issue_fence();
-      if (s + 2 * waves < step1) {
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this stage is read
-        issue_fence();
-        load(s + 2 * waves, stage);
-      }
-      at = St::kBytes - at;
+      load_step(s + 2 * waves, stage);
     }
+    at = St::kBytes - at;
   }
   __syncthreads();  // the stages make room for what follows
 
@@ -645,8 +658,8 @@ hipError_t go(const AttentionKernelArgs &a, const AttentionPlan &p, hipStream_t 
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  const unsigned blocks = (unsigned)a.row_blocks * a.kv_heads * a.num_seqs;
-  hipLaunchKernelGGL((attention_kernel<T, D, G, RT>), dim3(blocks, p.splits), dim3(64 * p.waves), lds, stream, a);
+  hipLaunchKernelGGL((attention_kernel<T, D, G, RT>), dim3((unsigned)a.row_blocks * a.kv_heads, a.num_seqs, p.splits),
+                     dim3(64 * p.waves), lds, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3((unsigned)a.max_q * a.kv_heads * a.share, a.num_seqs), dim3(256),

@@ -148,18 +148,31 @@ AttentionPlan attention_plan(const i4s_attention_args &a) {
   // as few rows as hold them all: the softmax is paid per 16 rows
   p.row_tiles = rows <= 16 ? 1 : (rows <= 32 || c.head_dim == 256 ? 2 : 4);
   p.row_blocks = (int)((rows + 16 * p.row_tiles - 1) / (16 * p.row_tiles));
-  p.waves = 4;
+  // eight waves a block where their registers fit a compute unit: twice the
+  // keys before a second launch has to join pieces
+  p.waves = p.row_tiles == 1 && c.head_dim <= 128 ? 8 : 4;
   const int64_t capacity = (int64_t)a.table_width * c.page_size;
   const int64_t len = a.max_len > 0 && a.max_len < capacity ? a.max_len : capacity;
-  // the keys in pieces, so that about three blocks per compute unit (256)
-  // run, each of at least one step of every wave
+  // The keys in pieces.  Measured in graphs, us, one query token of fp16, D =
+  // 128, unless said otherwise (units = sequences x KV heads x row blocks):
+  //   about one block for each of the 256 compute units: 8 units x 131071
+  //     keys in 32 / 64 pieces 35 / 41, in 16: 53; 64 x 8000 (8 rows) in 4 / 8
+  //     / 2: 22.0 / 23.2 / 30.5; 40 x 2047 (16 rows) in 4 / 8 / 1: 13.6 / 15.2
+  //     / 16.7; four waves, 40 x 4000 (64 rows) in 4 / 8 / 2: 40 / 53 / 54;
+  //   with as many units as that one piece (512 x 4095: 40, in 2 / 4: 48 /
+  //     50), but none longer than 4096 keys, so that sequences of different
+  //     lengths fill the chip to the end (512 x 16384, 32 rows, in 4 / 2 / 1:
+  //     211 / 221 / 226);
+  //   a step or four of every wave are not worth a second launch on the host
+  //     (32 x 1023: 10.9 in one launch, 10.0 in two).
   const int64_t units = (int64_t)p.row_blocks * c.kv_heads * (a.num_seqs > 0 ? a.num_seqs : 1);
   const int64_t step = kStepKeys * p.waves;
-  const int64_t steps = (len + step - 1) / step;
-  const int64_t want = clamp_to<int64_t>((768 + units - 1) / units, 1, kMaxSplits);
-  const int64_t per = clamp_to<int64_t>((steps + want - 1) / want, 1, steps > 0 ? steps : 1);
+  int64_t want = 256 / units;
+  if (want < (len + 4095) / 4096) want = (len + 4095) / 4096;
+  want = len <= 4 * step ? 1 : clamp_to<int64_t>(want, 1, kMaxSplits);
+  const int64_t per = clamp_to<int64_t>((len + want * step - 1) / (want * step), 1, (1 << 30) / step);
   p.chunk = (int)(per * step);
-  p.splits = (int)clamp_to<int64_t>((steps + per - 1) / per, 1, kMaxSplits);
+  p.splits = (int)clamp_to<int64_t>((len + p.chunk - 1) / p.chunk, 1, kMaxSplits);
   if (p.splits > 1)
     p.workspace_bytes = (uint64_t)p.splits * a.num_tokens * a.q_heads * (c.head_dim + 4) * sizeof(float);
   return p;
