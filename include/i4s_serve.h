@@ -50,6 +50,7 @@ extern "C" {
 #define I4S_KV_FORMAT_VERSION 1
 #define I4S_KV_MAX_REQUESTS 4096 /* requests of one i4s_kv_extend call */
 #define I4S_MAX_TOP_K 32         /* alternatives of one i4s_token_logprobs row */
+#define I4S_MAX_VOCAB (1 << 23)  /* columns of one i4s_token_logprobs row */
 #define I4S_MAX_TREE 64          /* candidate tokens a tree mask can name */
 
 /* Element types of activations and logits. */
@@ -207,9 +208,9 @@ i4s_status i4s_attention(const i4s_attention_args *a /* host */, void *stream);
  *   entropy[r]  = ln l - sum_j (x_j - m) exp(x_j - m) / l   (fp32, nats)
  *   top_ids[r][i], top_logprobs[r][i], i < top_k: the largest logits in
  *                 falling order, among equal ones the lower index first (-0
- *                 equals 0, a NaN comes before everything), int32 and fp32.
+ *                 equals 0, a NaN counts as +inf), int32 and fp32.
  *   logits  : dtype I4S_F16, I4S_BF16 or I4S_F32, aligned to its element;
- *             stride >= vocab.
+ *             stride >= vocab; vocab 1 .. I4S_MAX_VOCAB.
  *   tokens  : int64 [rows], 8-byte aligned; one outside [0, vocab) gives NaN.
  *   top_k   : 0 .. min(I4S_MAX_TOP_K, vocab); top_ids and top_logprobs may be
  *             NULL when it is 0.

@@ -131,7 +131,8 @@ i4s_status check_logprobs(int32_t dtype, int32_t rows, int32_t vocab, int32_t to
   if (dtype != I4S_F16 && dtype != I4S_BF16 && dtype != I4S_F32)
     return fail(I4S_ERR_INVALID_ARGUMENT, "dtype=%d must be I4S_F16, I4S_BF16 or I4S_F32", dtype);
   if (rows < 0) return fail(I4S_ERR_INVALID_ARGUMENT, "rows=%d must be 0 or more", rows);
-  if (vocab < 1 || vocab > 1 << 30) return fail(I4S_ERR_INVALID_ARGUMENT, "vocab=%d must be in [1, 2^30]", vocab);
+  if (vocab < 1 || vocab > I4S_MAX_VOCAB)
+    return fail(I4S_ERR_INVALID_ARGUMENT, "vocab=%d must be in [1, %d]", vocab, I4S_MAX_VOCAB);
   if (top_k < 0 || top_k > I4S_MAX_TOP_K || top_k > vocab)
     return fail(I4S_ERR_INVALID_ARGUMENT, "top_k=%d must be in [0, %d] and at most vocab=%d", top_k, I4S_MAX_TOP_K, vocab);
   return I4S_OK;
@@ -179,14 +180,17 @@ AttentionPlan attention_plan(const i4s_attention_args &a) {
 }
 
 LogprobsPlan logprobs_plan(int32_t dtype, int32_t rows, int32_t vocab, int32_t top_k) {
-  constexpr int kSlice = 8192;
   LogprobsPlan p{};
   const int vec = 16 / dtype_size(dtype);
-  const int slices = (int)(((int64_t)vocab + vec - 1 + kSlice - 1) / kSlice);
-  const int want = rows > 0 ? clamp_to((768 + rows - 1) / rows, 1, 64) : 1;
-  const int per = (slices + want - 1) / want;
-  p.splits = (slices + per - 1) / per;
-  p.chunk = per * kSlice;
+  // Pieces for about two blocks a compute unit, where that pays a second
+  // launch.  Measured in graphs, us, in one / several pieces: 1 x 150000 fp16
+  // 25 / 13 (16), 16 x 151643 fp32 35 / 17.5 (16), 64 x 50257 bf16 20 / 17
+  // (8), 200 x 151643 37 / 32 (2); but 16 x 32000 11 / 13 (2), 200 x 32000 15
+  // / 19 (2), 600 x 50257 31 / 35 (2).
+  const int all = (vocab + vec - 1 + kSegment - 1) / kSegment;
+  const int want = rows < 1 || rows > 256 || vocab <= 32768 ? 1 : clamp_to(512 / rows, 1, 16);
+  p.segments = clamp_to((all + want - 1) / want, 1, kMaxSegments);
+  p.splits = (all + p.segments - 1) / p.segments;
   if (p.splits > 1)
     p.workspace_bytes = (uint64_t)rows * p.splits * (4 * sizeof(float) + top_k * sizeof(uint64_t));
   return p;

@@ -90,9 +90,14 @@ hipError_t launch_attention(const AttentionKernelArgs &a, const AttentionPlan &p
 // ---------------------------------------------------------------------------
 // token scores (i4s_logprobs.hip)
 
+// Launch shape of a call: blocks of 256 threads, each over a piece of
+// `segments` segments (32 values a thread) of a row, `splits` pieces a row (1:
+// one launch).
+constexpr int kMaxLogprobsSplits = 64;  // the lanes of a wave join them
+constexpr int kSegment = 256 * 32;
+constexpr int kMaxSegments = 32;        // 1 KB of LDS each
 struct LogprobsPlan {
-  int splits;  // pieces of a row (1: one launch)
-  int chunk;   // columns of a piece
+  int splits, segments;
   uint64_t workspace_bytes;
 };
 LogprobsPlan logprobs_plan(int32_t dtype, int32_t rows, int32_t vocab, int32_t top_k);
@@ -106,7 +111,7 @@ struct LogprobsArgs {
   float *logprobs, *entropy;
   int32_t *top_ids;
   float *top_logprobs;
-  float *part_stats;    // [rows][splits][4]: max, sum, weighted sum, unused
+  float *part_stats;    // [rows][splits][4]: max, reference, sum, weighted sum
   uint64_t *part_keys;  // [rows][splits][top_k]
 };
 hipError_t launch_token_logprobs(const LogprobsArgs &a, const LogprobsPlan &p, int32_t dtype, hipStream_t stream);

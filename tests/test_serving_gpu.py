@@ -486,7 +486,7 @@ def test_logprobs_ties_and_masks(i4s, vocab):
     say("logprobs ties", vocab)
     inf, nan = float("inf"), float("nan")
     g = torch.Generator().manual_seed(vocab)
-    x = torch.zeros(14, vocab)
+    x = torch.zeros(17, vocab)
     x[1] = -inf                                                    # nothing left
     x[2] = -inf
     x[2, torch.randperm(vocab, generator=g)[:5]] = torch.tensor([1.0, 2.0, 2.0, 2.0, -3.0])  # a few tokens left
@@ -503,10 +503,15 @@ def test_logprobs_ties_and_masks(i4s, vocab):
     x[11] = torch.randn(vocab, generator=g)
     x[12, :33] = 5.0
     x[13, -33:] = 5.0
-    tokens = torch.tensor([vocab - 1, 0, 1, 2, 3, 4, 5, 6, 7, vocab - 1, 3, -1, vocab, 2**40])
-    for dtype in (F16, F32):
+    tokens = torch.tensor([vocab - 1, 0, 1, 2, 3, 4, 5, 6, 7, vocab - 1, 3, -1, vocab, 2**40, 5, 6, 7])
+    for dtype in (F16, BF16, F32):
+        y = x.to(dtype)
+        y[14] = torch.finfo(dtype).min                             # masked with the type's lowest value, all
+        y[15] = torch.finfo(dtype).min
+        y[15, 6:9] = torch.tensor([1.0, 3.0, 1.0]).to(dtype)       # or all but three
+        y[16, ::3] = torch.finfo(dtype).max
         for k in (0, 1, 8, 32):
-            check_logprobs(i4s, x.to(dtype), tokens, k)
+            check_logprobs(i4s, y, tokens, k)
 
 
 def test_logprobs_rows_at_any_address(i4s):
