@@ -128,8 +128,9 @@ __device__ inline void write_top(const LogprobsArgs &a, int row, int i, uint64_t
   a.top_logprobs[at] = logprob_of(s, value_of((uint32_t)(key >> 32)));
 }
 
-// A row as 16-byte vectors from the aligned address at or below its start:
-// value e of vector q is column q * kVec + e - pad.
+// A row as 16-byte vectors, from the start of the 128-byte line that holds its
+// first value (a wave's loads then cover whole lines): value e of vector q is
+// column q * kVec + e - pad.
 template <typename T>
 struct Row {
   static constexpr int kVec = 16 / T::kSize;
@@ -137,10 +138,12 @@ struct Row {
   int pad, vocab;
   __device__ Row(const LogprobsArgs &a, int row)
       : base(static_cast<const char *>(a.logits) + (int64_t)row * a.stride * T::kSize),
-        pad((int)((reinterpret_cast<uintptr_t>(base) & 15) / T::kSize)),
+        pad((int)((reinterpret_cast<uintptr_t>(base) & 127) / T::kSize)),
         vocab(a.vocab) {}
   __device__ int vectors() const { return (vocab + pad + kVec - 1) / kVec; }
   __device__ int column(int q) const { return q * kVec - pad; }
+  __device__ int first_whole() const { return (pad + kVec - 1) / kVec; }
+  __device__ int last_whole() const { return (vocab + pad) / kVec - 1; }
   __device__ bool whole(int q) const { return column(q) >= 0 && column(q) + kVec <= vocab; }
   __device__ w4_t vector(int q) const {
     return __builtin_nontemporal_load(reinterpret_cast<const w4_t *>(base + (int64_t)column(q) * T::kSize));
@@ -280,32 +283,34 @@ __global__ __launch_bounds__(NT) void logprobs_kernel(LogprobsArgs a, int splits
   const bool valid = token >= 0 && token < a.vocab;
   const float token_x = valid ? T::one(r.base, token) : 0.0f;
 
-  // the next segment's vectors load while this one is added up
-  const auto plain = [&](int q) { return q < q1 && r.whole(q) && r.whole(q + NT * kVecs - 1); };
-  w4_t v[kVecs];
+  // The next segment's vectors load while this one is added up.  Vectors that
+  // are not whole are replaced afterwards; the loads themselves have no branch.
+  const int first_whole = r.first_whole(), last_whole = r.last_whole();
+  const bool any_whole = first_whole <= last_whole;
+  w4_t v[kVecs] = {};
   const auto fetch = [&](int q) {
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) v[j] = r.vector(q + j * NT + tid);
+    for (int j = 0; j < kVecs; ++j) v[j] = r.vector(clamp_to(q + j * NT + tid, first_whole, last_whole));
   };
   Stats s = kNothing;
-  if (plain(q0)) fetch(q0);
+  if (any_whole) fetch(q0);
   for (int seg = 0, q = q0; q < q1; ++seg, q += NT * kVecs) {
     float x[kValues];
-    if (plain(q)) {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) x[j * kVec + e] = T::get(v[j], e);
+    if (q < first_whole || q + NT * kVecs - 1 > last_whole) {
 #pragma unroll
       for (int j = 0; j < kVecs; ++j)
+        if (!r.whole(q + j * NT + tid)) {
+          float y[kVec];
+          r.load(q + j * NT + tid, y);
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) x[j * kVec + e] = T::get(v[j], e);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kVecs; ++j) {
-        float y[kVec];
-        r.load(q + j * NT + tid, y);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) x[j * kVec + e] = y[e];
-      }
+          for (int e = 0; e < kVec; ++e) x[j * kVec + e] = y[e];
+        }
     }
-    if (plain(q + NT * kVecs)) fetch(q + NT * kVecs);
+    if (any_whole && q + NT * kVecs < q1) fetch(q + NT * kVecs);
     float top = x[0];
 #pragma unroll
     for (int e = 1; e < kValues; ++e) top = fmaxf(top, x[e]);  // passes over NaN

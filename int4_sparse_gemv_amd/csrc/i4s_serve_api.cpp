@@ -181,13 +181,12 @@ AttentionPlan attention_plan(const i4s_attention_args &a) {
 
 LogprobsPlan logprobs_plan(int32_t dtype, int32_t rows, int32_t vocab, int32_t top_k) {
   LogprobsPlan p{};
-  const int vec = 16 / dtype_size(dtype);
   // Pieces for about two blocks a compute unit, where that pays a second
   // launch.  Measured in graphs, us, in one / several pieces: 1 x 150000 fp16
   // 25 / 13 (16), 16 x 151643 fp32 35 / 17.5 (16), 64 x 50257 bf16 20 / 17
   // (8), 200 x 151643 37 / 32 (2); but 16 x 32000 11 / 13 (2), 200 x 32000 15
   // / 19 (2), 600 x 50257 31 / 35 (2).
-  const int all = (vocab + vec - 1 + kSegment - 1) / kSegment;
+  const int all = (vocab + 128 / dtype_size(dtype) - 1 + kSegment - 1) / kSegment;  // rows begin inside a line
   const int want = rows < 1 || rows > 256 || vocab <= 32768 ? 1 : clamp_to(512 / rows, 1, 16);
   p.segments = clamp_to((all + want - 1) / want, 1, kMaxSegments);
   p.splits = (all + p.segments - 1) / p.segments;
