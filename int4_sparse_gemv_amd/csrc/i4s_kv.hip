@@ -169,50 +169,83 @@ __device__ inline f8_t load8(const uint16_t *p) {
 // ---------------------------------------------------------------------------
 // writing tokens
 //
-// D/8 neighbouring lanes take one (token, head): a lane quantizes 8 channels
-// (one 16-byte load), the group maximum goes across the G/8 lanes of a group.
-// For K the lane's 8 nibbles are one word of the row.  For V the four lanes
-// that hold channels 16e + 8b .. +7 (e = 0..3) of one 64-channel block
-// exchange their words (three lane exchanges), and each writes two of the
-// eight 16-bit halves.  The work is a read of 16-bit values and a write of a
-// little over a quarter of that: bound by memory.
+// A block takes 256 / (D/8) neighbouring tokens of one head, D/8 neighbouring
+// lanes a token: a lane quantizes 8 channels (one 16-byte load), the group
+// maximum goes across the G/8 lanes of a group with DPP.  Neighbouring tokens
+// mostly lie in one page, where their K rows, the V words of four tokens and
+// their scales lie next to each other, so stores fill whole lines.  For K the
+// lane's 8 nibbles are one word of the row.  For V the four lanes that hold
+// channels 16e + 8b .. +7 (e = 0..3) of one 64-channel block exchange their
+// words, and each writes two of the eight 16-bit halves.
+//
+// Bound by: memory, 2 bytes read and a little over half a byte written a
+// value.
+
+template <int CTRL>
+__device__ inline uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kXor3 = 0x1B, kXor7 = 0x141, kXor15 = 0x140;  // of the lane number
 
 // The 8 nibbles (in channel order) and the scale of the lane's channels.
+// The quotient x / s is one multiplication by the (correctly rounded)
+// reciprocal and one correction with the exact remainder: a quotient that is a
+// whole number and a half comes out exactly, and the others lie further than
+// 2^-12 from one, so rint gives what it gives for the correctly rounded
+// quotient.
 template <int G>
-__device__ inline uint32_t quantize8(const f8_t &x, uint32_t &scale_bits) {
+__device__ inline uint32_t quantize8(f8_t x, uint32_t &scale_bits) {
   float m = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));  // fmaxf passes over a NaN
+  for (int e = 0; e < 8; ++e) m = __builtin_elementwise_maximum(m, fabsf(x[e]));  // passes a NaN on
+  if (__any(m != m)) {
+    m = 0.0f;
 #pragma unroll
-  for (int d = 1; d < G / 8; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+    for (int e = 0; e < 8; ++e) {
+      x[e] = x[e] == x[e] ? x[e] : 0.0f;
+      m = fmaxf(m, fabsf(x[e]));
+    }
+  }
+  const auto with = [&](uint32_t o) { m = fmaxf(m, __builtin_bit_cast(float, o)); };
+  with(dpp<kXor1>(__builtin_bit_cast(uint32_t, m)));
+  with(dpp<kXor2>(__builtin_bit_cast(uint32_t, m)));
+  if constexpr (G > 32) with(dpp<kXor7>(__builtin_bit_cast(uint32_t, m)));  // the other four lanes of eight
+  if constexpr (G > 64) with(dpp<kXor15>(__builtin_bit_cast(uint32_t, m)));  // the other eight of sixteen
   const _Float16 h = (_Float16)fminf(m / 7.0f, kScaleMax);
-  const float s = (float)h;
+  const float s = (float)h, r = s > 0.0f ? 1.0f / s : 0.0f, most = 7.0f * s;
   scale_bits = __builtin_bit_cast(uint16_t, h);
   uint32_t word = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    float q = 0.0f;
-    if (s > 0.0f && x[e] == x[e]) q = fminf(fmaxf(rintf(x[e] / s), -7.0f), 7.0f);
-    word |= (uint32_t)((int)q + 8) << (4 * e);
+    const float y = fminf(fmaxf(x[e], -most), most), q = y * r;
+    const int n = (int)rintf(fmaf(fmaf(-q, s, y), r, q));
+    word |= (uint32_t)(n + 8) << (4 * e);
   }
   return word;
 }
 
+// Where a thread works: a token (clamped, all lanes of a wave stay for the
+// exchanges) and its slot.
+template <int D>
+struct Place {
+  static constexpr int kLanes = D / 8, kTokens = 256 / kLanes;
+  int token, l, head, slot;
+  bool has, inside;
+  __device__ Place(const i4s_kv_cache &c, const int32_t *slots, int tokens, int shift) {
+    const int64_t t = (int64_t)blockIdx.x * kTokens + threadIdx.x / kLanes;
+    has = t < tokens;
+    token = has ? (int)t : tokens - 1;
+    l = threadIdx.x % kLanes;
+    head = blockIdx.y;
+    slot = slots[token];
+    inside = slot >= 0 && (slot >> shift) < c.num_pages;
+  }
+};
+
 template <typename T, int D, int G>
 __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a, int shift) {
-  constexpr int kLanes = D / 8;
-  const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) / kLanes;
-  const int l = threadIdx.x % kLanes;
-  const int heads = a.cache.kv_heads;
-  const int64_t units = (int64_t)a.tokens * heads;
-  // all lanes of a wave stay: the exchanges below go across lanes
-  const bool has = unit < units;
-  const int64_t u = has ? unit : units - 1;
-  const int token = (int)(u / heads), head = (int)(u % heads);
-  const int32_t slot = a.slots[token];
-  const int page_size = 1 << shift;
-  const bool store = has && slot >= 0 && (slot >> shift) < a.cache.num_pages;
-
+  const Place<D> at(a.cache, a.slots, a.tokens, shift);
+  const int token = at.token, l = at.l, head = at.head, slot = at.slot, heads = a.cache.kv_heads, page_size = 1 << shift;
   const f8_t xk = load8<T>(static_cast<const uint16_t *>(a.k) + token * a.k_token + head * a.k_head + 8 * l);
   const f8_t xv = load8<T>(static_cast<const uint16_t *>(a.v) + token * a.v_token + head * a.v_head + 8 * l);
   uint32_t sk, sv;
@@ -228,14 +261,16 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a, int shift)
   // words of the four e and makes halves x = 2e and 2e + 1 of i = 8b + x
   const int e = l % 8 / 2, b = l % 2, c = l / 8;
   uint32_t halves[2] = {0, 0};
+  const uint32_t mirrored = dpp<kXor7>(wv);
+  const uint32_t words[4] = {wv, dpp<kXor2>(wv), dpp<kXor3>(mirrored), dpp<kXor1>(mirrored)};  // of lanes l ^ 2d
 #pragma unroll
   for (int d = 0; d < 4; ++d) {
-    const uint32_t other = d ? __shfl_xor(wv, 2 * d) : wv;
+    const uint32_t two = words[d] >> (8 * e);
     const int from = e ^ d;
-    halves[0] |= ((other >> (8 * e)) & 15u) << (4 * from);
-    halves[1] |= ((other >> (8 * e + 4)) & 15u) << (4 * from);
+    halves[0] |= (two & 15u) << (4 * from);
+    halves[1] |= (two >> 4 & 15u) << (4 * from);
   }
-  if (!store) return;
+  if (!at.has || !at.inside) return;
 
   const int64_t base = (int64_t)(slot >> shift) * heads + head;
   const int off = slot & (page_size - 1);
@@ -248,9 +283,9 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a, int shift)
     vv[(half / 2) * 8 + (off & 3) * 2 + half % 2] = (uint16_t)halves[k];
   }
   if (l % (G / 8) == 0) {
-    const int64_t at = (base * page_size + (off & ~3)) * (D / G) + (l / (G / 8)) * 4 + (off & 3);
-    a.cache.k_scales[at] = (uint16_t)sk;
-    a.cache.v_scales[at] = (uint16_t)sv;
+    const int64_t to = (base * page_size + (off & ~3)) * (D / G) + (l / (G / 8)) * 4 + (off & 3);
+    a.cache.k_scales[to] = (uint16_t)sk;
+    a.cache.v_scales[to] = (uint16_t)sv;
   }
 }
 
@@ -272,17 +307,10 @@ __device__ inline void store8<Float>(void *p, int64_t at, const f8_t &x) {
 
 template <typename T, int D, int G>
 __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs a, int shift) {
-  constexpr int kLanes = D / 8;
-  const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) / kLanes;
-  const int l = threadIdx.x % kLanes;
-  const int heads = a.cache.kv_heads;
-  const int64_t units = (int64_t)a.tokens * heads;
-  const bool has = unit < units;
-  const int64_t u = has ? unit : units - 1;
-  const int token = (int)(u / heads), head = (int)(u % heads);
-  const int32_t slot = a.slots[token];
-  const int page_size = 1 << shift;
-  const bool inside = slot >= 0 && (slot >> shift) < a.cache.num_pages;
+  const Place<D> place(a.cache, a.slots, a.tokens, shift);
+  const int token = place.token, l = place.l, head = place.head, slot = place.slot;
+  const int heads = a.cache.kv_heads, page_size = 1 << shift;
+  const bool inside = place.inside;
   const int64_t base = (int64_t)(inside ? slot >> shift : 0) * heads + head;
   const int off = inside ? slot & (page_size - 1) : 0;
 
@@ -298,6 +326,8 @@ __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs a, int shift) {
   }
   const int64_t at = (base * page_size + (off & ~3)) * (D / G) + (l / (G / 8)) * 4 + (off & 3);
   const float sk = Half::to_float(a.cache.k_scales[at]), sv = Half::to_float(a.cache.v_scales[at]);
+  const uint32_t mirrored = dpp<kXor7>(two);
+  const uint32_t words[4] = {two, dpp<kXor2>(two), dpp<kXor3>(mirrored), dpp<kXor1>(mirrored)};  // of lanes l ^ 2d
   f8_t xk, xv;
 #pragma unroll
   for (int x = 0; x < 8; ++x) {
@@ -306,7 +336,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs a, int shift) {
   }
 #pragma unroll
   for (int d = 0; d < 4; ++d) {
-    const uint32_t other = d ? __shfl_xor(two, 2 * d) : two;
+    const uint32_t other = words[d];
     // the lane e ^ d holds halves 2(e^d) and 2(e^d) + 1; channel x of this lane is nibble e of half x
     const float q0 = (float)((int)((other >> (4 * e)) & 15u) - 8), q1 = (float)((int)((other >> (16 + 4 * e)) & 15u) - 8);
     const float v0 = inside ? sv * q0 : 0.0f, v1 = inside ? sv * q1 : 0.0f;
@@ -317,14 +347,15 @@ __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs a, int shift) {
         xv[2 * f + 1] = v1;
       }
   }
-  if (!has) return;
-  const int64_t to = u * D + 8 * l;
+  if (!place.has) return;
+  const int64_t to = ((int64_t)token * heads + head) * D + 8 * l;
   store8<T>(a.k, to, xk);
   store8<T>(a.v, to, xv);
 }
 
-unsigned grid_of(int64_t tokens, int heads, int head_dim) {
-  return (unsigned)((tokens * heads * (head_dim / 8) + 255) / 256);
+dim3 grid_of(int tokens, int heads, int head_dim) {
+  const int per = 256 / (head_dim / 8);
+  return dim3((unsigned)((tokens + (int64_t)per - 1) / per), heads);
 }
 
 template <template <typename, int, int> class Launch, typename T, typename A>
@@ -339,7 +370,7 @@ hipError_t by_shape(const A &a, hipStream_t s) {
 template <typename T, int D, int G>
 struct Append {
   static hipError_t go(const AppendArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL((kv_append_kernel<T, D, G>), dim3(grid_of(a.tokens, a.cache.kv_heads, D)), dim3(256), 0, s, a,
+    hipLaunchKernelGGL((kv_append_kernel<T, D, G>), grid_of(a.tokens, a.cache.kv_heads, D), dim3(256), 0, s, a,
                        page_shift(a.cache.page_size));
     return hipGetLastError();
   }
@@ -348,7 +379,7 @@ struct Append {
 template <typename T, int D, int G>
 struct Read {
   static hipError_t go(const ReadArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL((kv_read_kernel<T, D, G>), dim3(grid_of(a.tokens, a.cache.kv_heads, D)), dim3(256), 0, s, a,
+    hipLaunchKernelGGL((kv_read_kernel<T, D, G>), grid_of(a.tokens, a.cache.kv_heads, D), dim3(256), 0, s, a,
                        page_shift(a.cache.page_size));
     return hipGetLastError();
   }

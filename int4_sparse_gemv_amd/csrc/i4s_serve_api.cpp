@@ -263,8 +263,6 @@ i4s_status i4s_kv_append(const i4s_kv_cache *cache, const void *k, const void *v
   if (!k || !aligned(k, 16) || !v || !aligned(v, 16))
     return fail(I4S_ERR_INVALID_ARGUMENT, "k or v is NULL or not 16-byte aligned");
   if (!slots || !aligned(slots, 4)) return fail(I4S_ERR_INVALID_ARGUMENT, "slots is NULL or not 4-byte aligned");
-  if ((int64_t)tokens * cache->kv_heads * (cache->head_dim / 8) / 256 >= kMaxGrid)
-    return fail(I4S_ERR_INVALID_ARGUMENT, "too many tokens (%d) for one call", tokens);
   i4s_kv_sizes sz;
   cache_sizes(*cache, &sz);
   const Span out[] = {{cache->k_vals, sz.vals, "k_vals"},
@@ -294,8 +292,6 @@ i4s_status i4s_kv_read(const i4s_kv_cache *cache, const int32_t *slots, int32_t 
   if (!k_out || !aligned(k_out, 16) || !v_out || !aligned(v_out, 16))
     return fail(I4S_ERR_INVALID_ARGUMENT, "k_out or v_out is NULL or not 16-byte aligned");
   if (!slots || !aligned(slots, 4)) return fail(I4S_ERR_INVALID_ARGUMENT, "slots is NULL or not 4-byte aligned");
-  if ((int64_t)tokens * cache->kv_heads * (cache->head_dim / 8) / 256 >= kMaxGrid)
-    return fail(I4S_ERR_INVALID_ARGUMENT, "too many tokens (%d) for one call", tokens);
   i4s_kv_sizes sz;
   cache_sizes(*cache, &sz);
   const uint64_t bytes = (uint64_t)tokens * cache->kv_heads * cache->head_dim * dtype_size(dtype);
