@@ -176,7 +176,8 @@ __device__ inline f8_t load8(const uint16_t *p) {
 // their scales lie next to each other, so stores fill whole lines.  For K the
 // lane's 8 nibbles are one word of the row.  For V the four lanes that hold
 // channels 16e + 8b .. +7 (e = 0..3) of one 64-channel block exchange their
-// words, and each writes two of the eight 16-bit halves.
+// words and make two of the eight 16-bit halves each, and pairs of lanes join
+// these into whole words.
 //
 // Bound by: memory, 2 bytes read and a little over half a byte written a
 // value.
@@ -185,7 +186,7 @@ template <int CTRL>
 __device__ inline uint32_t dpp(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
 }
-constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kXor3 = 0x1B, kXor7 = 0x141, kXor15 = 0x140;  // of the lane number
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kXor3 = 0x1B, kXor7 = 0x141, kXor8 = 0x128, kXor15 = 0x140;  // of the lane number
 
 // The 8 nibbles (in channel order) and the scale of the lane's channels.
 // The quotient x / s is one multiplication by the (correctly rounded)
@@ -232,11 +233,13 @@ struct Place {
   int token, l, head, slot;
   bool has, inside;
   __device__ Place(const i4s_kv_cache &c, const int32_t *slots, int tokens, int shift) {
-    const int64_t t = (int64_t)blockIdx.x * kTokens + threadIdx.x / kLanes;
+    // the heads of the same tokens run next to each other: they lie in the same rows of k and v
+    const int block = blockIdx.x / c.kv_heads;
+    const int64_t t = (int64_t)block * kTokens + threadIdx.x / kLanes;
     has = t < tokens;
     token = has ? (int)t : tokens - 1;
     l = threadIdx.x % kLanes;
-    head = blockIdx.y;
+    head = blockIdx.x - block * c.kv_heads;
     slot = slots[token];
     inside = slot >= 0 && (slot >> shift) < c.num_pages;
   }
@@ -270,17 +273,21 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a, int shift)
     halves[0] |= (two & 15u) << (4 * from);
     halves[1] |= (two >> 4 & 15u) << (4 * from);
   }
+  const uint32_t other[2] = {dpp<kXor8>(halves[0]), dpp<kXor8>(halves[1])};
   if (!at.has || !at.inside) return;
 
   const int64_t base = (int64_t)(slot >> shift) * heads + head;
   const int off = slot & (page_size - 1);
   uint32_t *kv = reinterpret_cast<uint32_t *>(a.cache.k_vals + (base * page_size + off) * (D / 2));
   kv[(D / 32) * (l % 4) + l / 4] = word;
-  uint16_t *vv = reinterpret_cast<uint16_t *>(a.cache.v_vals + (base * page_size + (off & ~3)) * (D / 2));
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int half = (8 * b + 2 * e + k) * (D / 64) + c;
-    vv[(half / 2) * 8 + (off & 3) * 2 + half % 2] = (uint16_t)halves[k];
+  uint32_t *vv = reinterpret_cast<uint32_t *>(a.cache.v_vals + (base * page_size + (off & ~3)) * (D / 2)) + (off & 3);
+  if constexpr (D == 64) {
+    vv[4 * (4 * b + e)] = halves[0] | halves[1] << 16;
+  } else {
+    // the lane of the other 64-channel block of a pair has the words' other halves: one word each
+    const bool upper = c & 1;
+    const uint32_t word_v = upper ? other[1] | halves[1] << 16 : halves[0] | other[0] << 16;
+    vv[4 * (((8 * b + 2 * e + upper) * (D / 64) + c) / 2)] = word_v;
   }
   if (l % (G / 8) == 0) {
     const int64_t to = (base * page_size + (off & ~3)) * (D / G) + (l / (G / 8)) * 4 + (off & 3);
@@ -355,7 +362,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs a, int shift) {
 
 dim3 grid_of(int tokens, int heads, int head_dim) {
   const int per = 256 / (head_dim / 8);
-  return dim3((unsigned)((tokens + (int64_t)per - 1) / per), heads);
+  return dim3((unsigned)((tokens + (int64_t)per - 1) / per * heads));
 }
 
 template <template <typename, int, int> class Launch, typename T, typename A>

@@ -254,7 +254,8 @@ i4s_status i4s_kv_append(const i4s_kv_cache *cache, const void *k, const void *v
   if (st != I4S_OK) return st;
   if (dtype != I4S_F16 && dtype != I4S_BF16)
     return fail(I4S_ERR_INVALID_ARGUMENT, "dtype=%d must be I4S_F16 or I4S_BF16", dtype);
-  if (tokens < 0) return fail(I4S_ERR_INVALID_ARGUMENT, "tokens=%d must be 0 or more", tokens);
+  if (tokens < 0 || ((int64_t)tokens * cache->head_dim / 2048 + 1) * cache->kv_heads > kMaxGrid)
+    return fail(I4S_ERR_INVALID_ARGUMENT, "tokens=%d must be 0 or more, and kv_heads * head_dim * tokens less than 2^42", tokens);
   st = check_strides(k_token_stride, k_head_stride, "k");
   if (st != I4S_OK) return st;
   st = check_strides(v_token_stride, v_head_stride, "v");
@@ -287,7 +288,8 @@ i4s_status i4s_kv_read(const i4s_kv_cache *cache, const int32_t *slots, int32_t 
   if (st != I4S_OK) return st;
   if (dtype != I4S_F16 && dtype != I4S_BF16 && dtype != I4S_F32)
     return fail(I4S_ERR_INVALID_ARGUMENT, "dtype=%d must be I4S_F16, I4S_BF16 or I4S_F32", dtype);
-  if (tokens < 0) return fail(I4S_ERR_INVALID_ARGUMENT, "tokens=%d must be 0 or more", tokens);
+  if (tokens < 0 || ((int64_t)tokens * cache->head_dim / 2048 + 1) * cache->kv_heads > kMaxGrid)
+    return fail(I4S_ERR_INVALID_ARGUMENT, "tokens=%d must be 0 or more, and kv_heads * head_dim * tokens less than 2^42", tokens);
   if (tokens == 0) return I4S_OK;
   if (!k_out || !aligned(k_out, 16) || !v_out || !aligned(v_out, 16))
     return fail(I4S_ERR_INVALID_ARGUMENT, "k_out or v_out is NULL or not 16-byte aligned");
