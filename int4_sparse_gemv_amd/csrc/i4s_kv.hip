@@ -189,13 +189,24 @@ __device__ inline uint32_t dpp(uint32_t v) {
 constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kXor3 = 0x1B, kXor7 = 0x141, kXor8 = 0x128, kXor15 = 0x140;  // of the lane number
 
 // The 8 nibbles (in channel order) and the scale of the lane's channels.
-// The quotient x / s is one multiplication by the (correctly rounded)
-// reciprocal and one correction with the exact remainder: a quotient that is a
-// whole number and a half comes out exactly, and the others lie further than
-// 2^-12 from one, so rint gives what it gives for the correctly rounded
-// quotient.
+// Quotients are a product with an approximate reciprocal and one correction
+// with the exact remainder: a quotient that has few bits (a whole number and a
+// half, half a step of a subnormal scale) comes out exactly, and the others lie
+// further from such a border (2^-12 of a step) than the error, so rounding
+// gives what it gives for the correctly rounded quotient.
+__device__ inline float quotient(float x, float divisor, float reciprocal) {
+  const float q = x * reciprocal;
+  return fmaf(fmaf(-q, divisor, x), reciprocal, q);
+}
+
+// The low bytes of a, b, c, d.
+__device__ inline uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0C0C0400u), __builtin_amdgcn_perm(b, a, 0x0C0C0400u), 0x05040100u);
+}
+
+// n[e] of the lane's channels e = 0..7: the nibble in the low byte.
 template <int G>
-__device__ inline uint32_t quantize8(f8_t x, uint32_t &scale_bits) {
+__device__ inline void quantize8(f8_t x, uint32_t (&n)[8], uint32_t &scale_bits) {
   float m = 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) m = __builtin_elementwise_maximum(m, fabsf(x[e]));  // passes a NaN on
@@ -207,22 +218,20 @@ __device__ inline uint32_t quantize8(f8_t x, uint32_t &scale_bits) {
       m = fmaxf(m, fabsf(x[e]));
     }
   }
-  const auto with = [&](uint32_t o) { m = fmaxf(m, __builtin_bit_cast(float, o)); };
+  const auto with = [&](uint32_t o) { m = __builtin_elementwise_maximum(m, __builtin_bit_cast(float, o)); };
   with(dpp<kXor1>(__builtin_bit_cast(uint32_t, m)));
   with(dpp<kXor2>(__builtin_bit_cast(uint32_t, m)));
   if constexpr (G > 32) with(dpp<kXor7>(__builtin_bit_cast(uint32_t, m)));  // the other four lanes of eight
   if constexpr (G > 64) with(dpp<kXor15>(__builtin_bit_cast(uint32_t, m)));  // the other eight of sixteen
-  const _Float16 h = (_Float16)fminf(m / 7.0f, kScaleMax);
-  const float s = (float)h, r = s > 0.0f ? 1.0f / s : 0.0f, most = 7.0f * s;
+  const _Float16 h = (_Float16)quotient(fminf(m, 7.0f * kScaleMax), 7.0f, 1.0f / 7.0f);
+  const float s = (float)h, r = s > 0.0f ? __builtin_amdgcn_rcpf(s) : 0.0f, most = 7.0f * s;
   scale_bits = __builtin_bit_cast(uint16_t, h);
-  uint32_t word = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float y = fminf(fmaxf(x[e], -most), most), q = y * r;
-    const int n = (int)rintf(fmaf(fmaf(-q, s, y), r, q));
-    word |= (uint32_t)(n + 8) << (4 * e);
+    // adding 1.5 * 2^23 + 8 rounds to a whole number (half to even) and leaves n + 8 in the low bits
+    const float u = quotient(__builtin_amdgcn_fmed3f(x[e], -most, most), s, r) + 12582920.0f;
+    n[e] = __builtin_bit_cast(uint32_t, u);
   }
-  return word;
 }
 
 // Where a thread works: a token (clamped, all lanes of a wave stay for the
@@ -251,14 +260,12 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a, int shift)
   const int token = at.token, l = at.l, head = at.head, slot = at.slot, heads = a.cache.kv_heads, page_size = 1 << shift;
   const f8_t xk = load8<T>(static_cast<const uint16_t *>(a.k) + token * a.k_token + head * a.k_head + 8 * l);
   const f8_t xv = load8<T>(static_cast<const uint16_t *>(a.v) + token * a.v_token + head * a.v_head + 8 * l);
-  uint32_t sk, sv;
-  const uint32_t wk = quantize8<G>(xk, sk);
-  const uint32_t wv = quantize8<G>(xv, sv);
-
-  // K: slot k of the word takes element (0,2,4,6,1,3,5,7)[k]
-  uint32_t word = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) word |= ((wk >> (4 * e)) & 15u) << (4 * (e / 2 + 4 * (e % 2)));
+  uint32_t sk, sv, nk[8], nv[8];
+  quantize8<G>(xk, nk, sk);
+  quantize8<G>(xv, nv, sv);
+  // K: slot k of the word takes element (0,2,4,6,1,3,5,7)[k]; V for now in order
+  const uint32_t word = low_bytes(nk[0], nk[4], nk[1], nk[5]) | low_bytes(nk[2], nk[6], nk[3], nk[7]) << 4;
+  const uint32_t wv = low_bytes(nv[0], nv[2], nv[4], nv[6]) | low_bytes(nv[1], nv[3], nv[5], nv[7]) << 4;
 
   // V: lane l holds block c = l / 8, e = l % 8 / 2, b = l % 2; it collects the
   // words of the four e and makes halves x = 2e and 2e + 1 of i = 8b + x
