@@ -27,19 +27,24 @@ __all__ = ["KVCache", "KVStep", "TokenLogprobs", "kv_cache", "kv_extend", "kv_ap
            "token_logprobs"]
 
 _DTYPES = {torch.float16: S.I4S_F16, torch.bfloat16: S.I4S_BF16, torch.float32: S.I4S_F32}
+_HALVES = {torch.float16: S.I4S_F16, torch.bfloat16: S.I4S_BF16}
+
+# The checks of a call are part of its time (a launch takes 3 us, a call 5 to
+# 8): identity of types, devices as numbers, messages only when they are needed.
 
 
-def _call(fn, device, *args):
-    """fn(*args, stream) on the device's current stream, with the device current."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    return fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+def _call(fn, index, *args):
+    """fn(*args, stream) on the current stream of device `index`, with that device current."""
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return fn(*args, torch.cuda.current_stream(index).cuda_stream)
+    return fn(*args, torch._C._cuda_getCurrentRawStream(index))
 
 
-def _int32(t, shape, device, name) -> None:
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor on {device}")
+def _check(t, dtype, shape, index, name) -> None:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on GPU {index}, "
+                         f"not {t.dtype} {list(t.shape)} on {t.device}")
 
 
 def _strides(t, name):
@@ -47,7 +52,8 @@ def _strides(t, name):
     token, head, channel = t.stride()
     if channel != 1:
         raise ValueError(f"the channels of {name} must lie next to each other")
-    return (token if t.shape[0] > 1 else 0), (head if t.shape[1] > 1 else 0)
+    shape = t.shape
+    return (token if shape[0] > 1 else 0), (head if shape[1] > 1 else 0)
 
 
 class KVCache:
@@ -73,6 +79,7 @@ class KVCache:
         self.num_pages = pages
         self.k_vals, self.v_vals, self.k_scales, self.v_scales = k_vals, v_vals, k_scales, v_scales
         self.device = k_vals.device
+        self.index = self.device.index
         d = S.i4s_kv_cache()
         d.num_pages, d.page_size, d.kv_heads, d.head_dim, d.group_size = pages, page_size, kv_heads, head_dim, group_size
         d.k_vals, d.v_vals = k_vals.data_ptr(), v_vals.data_ptr()
@@ -115,24 +122,23 @@ def kv_extend(table, lens, new_lens, free_pages, free_count, page_size: int, cap
     are the next call's; a finished request's pages are given back by writing
     them to ``free_pages`` at ``free_count`` and raising that.
     """
-    if table.dim() != 2:
-        raise ValueError("table must be int32 [requests, width]")
-    n, width = table.shape
-    device = table.device
-    _int32(table, (n, width), device, "table")
-    _int32(lens, (n,), device, "lens")
-    _int32(new_lens, (n,), device, "new_lens")
-    _int32(free_pages, (free_pages.numel(),), device, "free_pages")
-    _int32(free_count, (1,), device, "free_count")
-    if not table.is_cuda:
-        raise ValueError("table must be on a GPU")
+    index = table.get_device()
+    if table.dim() != 2 or index < 0:
+        raise ValueError("table must be int32 [requests, width] on a GPU")
+    n, width = shape = table.shape
+    _check(table, torch.int32, shape, index, "table")
+    _check(lens, torch.int32, (n,), index, "lens")
+    _check(new_lens, torch.int32, (n,), index, "new_lens")
+    entries = free_pages.numel()
+    _check(free_pages, torch.int32, (entries,), index, "free_pages")
+    _check(free_count, torch.int32, (1,), index, "free_count")
     # one allocation: lens, q_start, count, flags, slots, positions
-    buf = torch.empty(2 * n + 3 + 2 * capacity, dtype=torch.int32, device=device)
+    buf = table.new_empty(2 * n + 3 + 2 * capacity)
     at = buf.data_ptr()
-    o_start, o_count, o_slots = n, 2 * n + 1, 2 * n + 3
-    st = _call(S.load().i4s_kv_extend, device, table.data_ptr(), n, width, page_size, lens.data_ptr(), new_lens.data_ptr(),
-               free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(), capacity, at, at + 4 * o_start,
-               at + 4 * o_slots, at + 4 * (o_slots + capacity), at + 4 * o_count, at + 4 * (o_count + 1))
+    start, count, slots = at + 4 * n, at + 8 * n + 4, at + 8 * n + 12
+    st = _call(S.load().i4s_kv_extend, index, table.data_ptr(), n, width, page_size, lens.data_ptr(), new_lens.data_ptr(),
+               free_pages.data_ptr(), entries, free_count.data_ptr(), capacity, at, start, slots, slots + 4 * capacity, count,
+               count + 4)
     if st:
         B.check(st, "i4s_kv_extend")
     new, start, count, flags, slots, positions = buf.split_with_sizes((n, n + 1, 1, 1, capacity, capacity))
@@ -142,18 +148,17 @@ def kv_extend(table, lens, new_lens, free_pages, free_count, page_size: int, cap
 def kv_append(cache: KVCache, k, v, slots) -> None:
     """Quantize k, v ([tokens, kv_heads, head_dim], fp16 or bf16) into ``slots``
     (int32 [tokens]; -1 skips a token).  Tokens and heads may be strided."""
-    shape = k.shape
-    if (len(shape) != 3 or shape != v.shape or shape[1] != cache.kv_heads or shape[2] != cache.head_dim
-            or k.dtype != v.dtype or k.dtype not in (torch.float16, torch.bfloat16)):
+    shape, dtype, index = k.shape, _HALVES.get(k.dtype), cache.index
+    if (dtype is None or len(shape) != 3 or shape[1] != cache.kv_heads or shape[2] != cache.head_dim or v.shape != shape
+            or v.dtype is not k.dtype):
         raise ValueError(f"k and v must be float16 or bfloat16 [tokens, {cache.kv_heads}, {cache.head_dim}]")
-    device = cache.device
-    if k.device != device or v.device != device:
-        raise ValueError(f"k and v must be on {device}")
+    if k.get_device() != index or v.get_device() != index:
+        raise ValueError(f"k and v must be on {cache.device}")
     tokens = shape[0]
-    _int32(slots, (tokens,), device, "slots")
+    _check(slots, torch.int32, (tokens,), index, "slots")
     ks, vs = _strides(k, "k"), _strides(v, "v")
-    st = _call(S.load().i4s_kv_append, device, cache.descriptor, k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], ks[0], ks[1],
-               vs[0], vs[1], slots.data_ptr(), tokens)
+    st = _call(S.load().i4s_kv_append, index, cache.descriptor, k.data_ptr(), v.data_ptr(), dtype, ks[0], ks[1], vs[0],
+               vs[1], slots.data_ptr(), tokens)
     if st:
         B.check(st, "i4s_kv_append")
 
@@ -161,15 +166,16 @@ def kv_append(cache: KVCache, k, v, slots) -> None:
 def kv_read(cache: KVCache, slots, dtype=torch.float16):
     """(k, v) of the tokens at ``slots``, [tokens, kv_heads, head_dim] of
     ``dtype``; a slot outside the cache gives zeros."""
-    if dtype not in _DTYPES:
+    number, shape, index = _DTYPES.get(dtype), slots.shape, cache.index
+    if number is None:
         raise ValueError("dtype must be float16, bfloat16 or float32")
-    if slots.dim() != 1:
+    if len(shape) != 1:
         raise ValueError("slots must be int32 [tokens]")
-    device, tokens = cache.device, slots.shape[0]
-    _int32(slots, (tokens,), device, "slots")
-    k, v = torch.empty((2, tokens, cache.kv_heads, cache.head_dim), dtype=dtype, device=device).unbind()
-    st = _call(S.load().i4s_kv_read, device, cache.descriptor, slots.data_ptr(), tokens, _DTYPES[dtype], k.data_ptr(),
-               v.data_ptr())
+    tokens = shape[0]
+    _check(slots, torch.int32, shape, index, "slots")
+    k = slots.new_empty((tokens, cache.kv_heads, cache.head_dim), dtype=dtype)
+    v = torch.empty_like(k)
+    st = _call(S.load().i4s_kv_read, index, cache.descriptor, slots.data_ptr(), tokens, number, k.data_ptr(), v.data_ptr())
     if st:
         B.check(st, "i4s_kv_read")
     return k, v
@@ -191,42 +197,37 @@ def kv_attention(cache: KVCache, q, table, lens, q_start=None, max_q: Optional[i
     receives the logarithm of the sum of exponentials.  Returns [tokens,
     q_heads, head_dim] like q.
     """
-    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.dtype not in (torch.float16, torch.bfloat16):
+    shape, dtype, index = q.shape, _HALVES.get(q.dtype), cache.index
+    if dtype is None or len(shape) != 3 or shape[2] != cache.head_dim:
         raise ValueError(f"q must be float16 or bfloat16 [tokens, q_heads, {cache.head_dim}]")
-    device = cache.device
-    if q.device != device:
-        raise ValueError(f"q is on {q.device}, the cache on {device}")
-    tokens, heads, dim = q.shape
+    if q.get_device() != index:
+        raise ValueError(f"q is on {q.device}, the cache on {cache.device}")
+    tokens, heads, dim = shape
     if table.dim() != 2:
         raise ValueError("table must be int32 [sequences, width]")
-    n, width = table.shape
-    _int32(table, (n, width), device, "table")
-    _int32(lens, (n,), device, "lens")
-    qs = _strides(q, "q")
-    a = S.i4s_attention_args()
+    n, width = rows = table.shape
+    _check(table, torch.int32, rows, index, "table")
+    _check(lens, torch.int32, (n,), index, "lens")
+    token_stride, head_stride = _strides(q, "q")
     if q_start is not None:
-        _int32(q_start, (n + 1,), device, "q_start")
-        a.q_start = q_start.data_ptr()
-        a.max_q = max_q if max_q is not None else max(tokens, 1)
-    else:
-        a.max_q = max_q if max_q is not None else 1
+        _check(q_start, torch.int32, (n + 1,), index, "q_start")
+        if max_q is None:
+            max_q = max(tokens, 1)
+    elif max_q is None:
+        max_q = 1
     if tree_mask is not None:
-        if tree_mask.dtype != torch.int64 or tuple(tree_mask.shape) != (tokens,) or tree_mask.device != device or not tree_mask.is_contiguous():
-            raise ValueError(f"tree_mask must be a contiguous int64 [{tokens}] tensor on {device}")
-        a.tree_mask = tree_mask.data_ptr()
+        _check(tree_mask, torch.int64, (tokens,), index, "tree_mask")
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=device)
-    elif out.dtype != q.dtype or out.shape != q.shape or out.device != device or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous {q.dtype} {list(q.shape)} tensor on {device}")
+        out = q.new_empty(shape)
+    else:
+        _check(out, q.dtype, shape, index, "out")
     if lse is not None:
-        if lse.dtype != torch.float32 or tuple(lse.shape) != (tokens, heads) or lse.device != device or not lse.is_contiguous():
-            raise ValueError(f"lse must be a contiguous float32 [{tokens}, {heads}] tensor on {device}")
-        a.lse = lse.data_ptr()
-    a.cache = ctypes.addressof(cache.descriptor)
-    a.q, a.q_token_stride, a.q_head_stride = q.data_ptr(), qs[0], qs[1]
-    a.dtype, a.q_heads, a.num_tokens, a.num_seqs = _DTYPES[q.dtype], heads, tokens, n
-    a.table, a.table_width, a.lens = table.data_ptr(), width, lens.data_ptr()
-    a.max_len, a.scale, a.out = max_len, dim ** -0.5 if scale is None else scale, out.data_ptr()
+        _check(lse, torch.float32, (tokens, heads), index, "lse")
+    a = S.i4s_attention_args(
+        ctypes.addressof(cache.descriptor), q.data_ptr(), token_stride, head_stride, dtype, heads, tokens, n, table.data_ptr(),
+        width, lens.data_ptr(), None if q_start is None else q_start.data_ptr(), max_q, max_len,
+        dim ** -0.5 if scale is None else scale, None if tree_mask is None else tree_mask.data_ptr(), out.data_ptr(),
+        None if lse is None else lse.data_ptr(), None, 0)
     lib = S.load()
     nbytes = ctypes.c_uint64()
     st = lib.i4s_attention_workspace_size(a, nbytes)
@@ -234,9 +235,9 @@ def kv_attention(cache: KVCache, q, table, lens, q_start=None, max_q: Optional[i
         B.check(st, "i4s_attention_workspace_size")
     if nbytes.value:
         # of this call alone: calls on other streams and captured graphs have their own
-        ws = torch.empty(nbytes.value, dtype=torch.uint8, device=device)
+        ws = q.new_empty(nbytes.value, dtype=torch.uint8)
         a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes.value
-    st = _call(lib.i4s_attention, device, a)
+    st = _call(lib.i4s_attention, index, a)
     if st:
         B.check(st, "i4s_attention")
     return out
@@ -260,24 +261,25 @@ def token_logprobs(logits, tokens, top_k: int = 0) -> TokenLogprobs:
     """Log probabilities of ``tokens`` (int64 [rows]) under ``logits`` ([rows,
     vocab], fp16, bf16 or fp32, rows may be strided), the entropy of every row
     and its ``top_k`` largest alternatives (equal ones: lower index first)."""
-    if logits.dim() != 2 or logits.dtype not in _DTYPES or not logits.is_cuda:
+    dtype, index = _DTYPES.get(logits.dtype), logits.get_device()
+    if dtype is None or logits.dim() != 2 or index < 0:
         raise ValueError("logits must be a float16, bfloat16 or float32 [rows, vocab] tensor on a GPU")
     rows, vocab = logits.shape
-    device = logits.device
-    if tokens.dtype != torch.int64 or tuple(tokens.shape) != (rows,) or tokens.device != device or not tokens.is_contiguous():
-        raise ValueError(f"tokens must be a contiguous int64 [{rows}] tensor on {device}")
-    if logits.stride(1) != 1 and vocab > 1:
+    _check(tokens, torch.int64, (rows,), index, "tokens")
+    stride, step = logits.stride()
+    if step != 1 and vocab > 1:
         raise ValueError("the values of a row must lie next to each other")
-    stride = logits.stride(0) if rows > 1 else vocab
-    dtype = _DTYPES[logits.dtype]
+    if rows < 2:
+        stride = vocab
     nbytes = _logprobs_workspace(dtype, rows, vocab, top_k)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-    out = torch.empty((2, rows), dtype=torch.float32, device=device)
-    top_ids = torch.empty((rows, top_k), dtype=torch.int32, device=device)
-    top = torch.empty((rows, top_k), dtype=torch.float32, device=device)
-    at = out.data_ptr()
-    st = _call(S.load().i4s_token_logprobs, device, logits.data_ptr(), dtype, rows, vocab, stride, tokens.data_ptr(), top_k,
-               at, at + 4 * rows, top_ids.data_ptr(), top.data_ptr(), ws.data_ptr() if ws is not None else None, nbytes)
+    ws = logits.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+    logprobs = logits.new_empty(rows, dtype=torch.float32)
+    entropy = torch.empty_like(logprobs)
+    top_ids = tokens.new_empty((rows, top_k), dtype=torch.int32)
+    top = logprobs.new_empty((rows, top_k))
+    st = _call(S.load().i4s_token_logprobs, index, logits.data_ptr(), dtype, rows, vocab, stride, tokens.data_ptr(), top_k,
+               logprobs.data_ptr(), entropy.data_ptr(), top_ids.data_ptr(), top.data_ptr(),
+               None if ws is None else ws.data_ptr(), nbytes)
     if st:
         B.check(st, "i4s_token_logprobs")
-    return TokenLogprobs(out[0], out[1], top_ids, top)
+    return TokenLogprobs(logprobs, entropy, top_ids, top)
