@@ -669,12 +669,9 @@ hipError_t go(const AttentionKernelArgs &a, const AttentionPlan &p, hipStream_t 
 
 template <typename T, int D, int G>
 hipError_t by_rows(const AttentionKernelArgs &a, const AttentionPlan &p, hipStream_t stream) {
-  if (p.row_tiles == 1) return go<T, D, G, 1>(a, p, stream);
-  if constexpr (D == 256) {
-    return go<T, D, G, 2>(a, p, stream);
-  } else {
-    return p.row_tiles == 2 ? go<T, D, G, 2>(a, p, stream) : go<T, D, G, 4>(a, p, stream);
-  }
+  if constexpr (D / G >= 4)
+    if (p.row_tiles == 2) return go<T, D, G, 2>(a, p, stream);
+  return go<T, D, G, 1>(a, p, stream);
 }
 
 template <typename T>

@@ -146,8 +146,12 @@ AttentionPlan attention_plan(const i4s_attention_args &a) {
   const i4s_kv_cache &c = *a.cache;
   AttentionPlan p{};
   const int64_t rows = (int64_t)a.max_q * (a.q_heads / c.kv_heads);
-  // as few rows as hold them all: the softmax is paid per 16 rows
-  p.row_tiles = rows <= 16 ? 1 : (rows <= 32 || c.head_dim == 256 ? 2 : 4);
+  // 16 rows a block, or 32 where a head has four groups or more and the work
+  // a key costs by itself (its scales) counts.  Us, 32 / 16 rows a block: 512
+  // x 16384 keys, 32 rows, D = 128, G = 32: 211 / 336; but G = 64, 512 x 4000:
+  // 67 / 67, D = 64, G = 32, 256 x 4000, 40 rows: 51 / 32, D = 128, G = 64, 32 x
+  // 2000, 128 rows: 30 / 20; 64 rows a block were slower in all of these.
+  p.row_tiles = rows > 16 && c.head_dim / c.group_size >= 4 ? 2 : 1;
   p.row_blocks = (int)((rows + 16 * p.row_tiles - 1) / (16 * p.row_tiles));
   // eight waves a block where their registers fit a compute unit: twice the
   // keys before a second launch has to join pieces
@@ -159,7 +163,7 @@ AttentionPlan attention_plan(const i4s_attention_args &a) {
   //   about one block for each of the 256 compute units: 8 units x 131071
   //     keys in 32 / 64 pieces 35 / 41, in 16: 53; 64 x 8000 (8 rows) in 4 / 8
   //     / 2: 22.0 / 23.2 / 30.5; 40 x 2047 (16 rows) in 4 / 8 / 1: 13.6 / 15.2
-  //     / 16.7; four waves, 40 x 4000 (64 rows) in 4 / 8 / 2: 40 / 53 / 54;
+  //     / 16.7; four waves, 40 x 4000 (64 rows) in 4 / 8: 31 / 39;
   //   with as many units as that one piece (512 x 4095: 40, in 2 / 4: 48 /
   //     50), but none longer than 4096 keys, so that sequences of different
   //     lengths fill the chip to the end (512 x 16384, 32 rows, in 4 / 2 / 1:
