@@ -82,6 +82,10 @@ def parse():
                     help="time this build of libi4s (e.g. one made with build --define ... --out PATH)")
     ap.add_argument("--batch-paths", action="store_true",
                     help="instead of the headline: 2:4 layers at batch 2, 3, 4 and 8, one JSON line")
+    ap.add_argument("--verify-step", type=int, default=None, metavar="TOKENS",
+                    help="time one 7B-shaped layer's verification step at this many candidate tokens (1-16): the packed "
+                         "products, the 4-bit cache and its attention, and the scores of a 32000-word vocabulary")
+    ap.add_argument("--context", type=int, default=2000, help="with --verify-step: tokens held before the candidates")
     ap.add_argument("--stack", default=None,
                     help="instead of the headline: one 7B stack (c4_stack7b or x2_mix_stack7b), per pass and per layer")
     ap.add_argument("--summarize-rocprof", nargs=2, metavar=("DIR", "OUT"), default=None,
@@ -417,6 +421,119 @@ def batch_paths(R, args):
     return {"lib": args.lib or "default", "steps": args.steps, "trials": args.trials, "rows": rows}
 
 
+class VerifyStep:
+    """One layer of a 7B-shaped decoder verifying a tree of candidate tokens
+    of one request, and the scores after it: the seven packed products around
+    the 4-bit cache, its attention and the token scores.  (Norms, rotary
+    positions, the gate's activation and the residual sums are the caller's
+    and not part of this library.)  Inputs are synthetic."""
+
+    HEADS, DIM, HIDDEN, MLP, VOCAB, PAGE = 32, 128, 4096, 11008, 32000, 16
+
+    def __init__(self, I, tokens, context, seed=0, device="cuda", hidden=None, heads=None, mlp=None, vocab=None):
+        import torch
+        self.torch, self.I, self.tokens = torch, I, tokens
+        h, n, m, v = hidden or self.HIDDEN, heads or self.HEADS, mlp or self.MLP, vocab or self.VOCAB
+        self.heads, self.dim = n, h // n
+        g = torch.Generator(device=device)
+        g.manual_seed(seed)
+
+        def layer(rows, cols):
+            return I.pack((0.02 * torch.randn(rows, cols, generator=g, device=device)).half(), 2, 128)
+        self.q, self.k, self.v, self.o = (layer(h, h) for _ in range(4))
+        self.gate, self.up, self.down = layer(m, h), layer(m, h), layer(h, m)
+        self.head = layer(v, h)
+        i32 = dict(dtype=torch.int32, device=device)
+        width = -(-(context + tokens) // self.PAGE) + 1
+        self.cache = I.kv_cache(width + 2, self.PAGE, n, self.dim, 64, device)
+        self.table = torch.full((1, width), -1, **i32)
+        self.free = torch.randperm(width + 2, generator=g, device=device, dtype=torch.int32)
+        # the context: its pages, and keys and values of random tokens
+        r = I.kv_extend(self.table, torch.zeros(1, **i32), torch.full((1,), context, **i32), self.free,
+                        torch.full((1,), width + 2, **i32), self.PAGE, context)
+        kv = torch.randn(2, context, n, self.dim, generator=g, device=device).half()
+        I.kv_append(self.cache, kv[0], kv[1], r.slots)
+        self.lens, self.count, self.max_len = r.lens, r.free_count, context + tokens
+        self.new = torch.full((1,), tokens, **i32)
+        self.x = torch.randn(tokens, h, generator=g, device=device).half()
+        self.mask = torch.tensor([sum(1 << b for b in self.path(t)) for t in range(tokens)], device=device)
+        self.given = torch.randint(v, (tokens,), generator=g, device=device)
+
+    @staticmethod
+    def path(t):
+        """The ancestors of node t of a binary tree in level order, and t."""
+        out = [t]
+        while t:
+            t = (t - 1) // 2
+            out.append(t)
+        return out
+
+    def project(self):
+        return self.I.run_multi((self.q, self.k, self.v), self.x)
+
+    def extend(self):
+        return self.I.kv_extend(self.table, self.lens, self.new, self.free, self.count, self.PAGE, self.tokens)
+
+    def append(self, k, v, r):
+        self.I.kv_append(self.cache, k.unflatten(1, (self.heads, self.dim)), v.unflatten(1, (self.heads, self.dim)), r.slots)
+
+    def attend(self, q, r):
+        return self.I.kv_attention(self.cache, q.unflatten(1, (self.heads, self.dim)), self.table, r.lens, q_start=r.q_start,
+                                   max_q=self.tokens, max_len=self.max_len, tree_mask=self.mask).flatten(1)
+
+    def mlp(self, a):
+        gate, up = self.I.run_multi((self.gate, self.up), self.I.run(self.o, a))
+        return self.I.run(self.down, gate * up)
+
+    def score(self, y):
+        return self.I.token_logprobs(self.I.run(self.head, y), self.given, top_k=8)
+
+    def run(self):
+        q, k, v = self.project()
+        r = self.extend()
+        self.append(k, v, r)
+        a = self.attend(q, r)
+        y = self.mlp(a)
+        return a, y, self.score(y)
+
+
+def verify_step(R, args):
+    """The step in a graph, whole and in its parts, us each."""
+    torch = R.torch
+    s = VerifyStep(R.I, args.verify_step, args.context)
+    q, k, v = s.project()
+    r = s.extend()
+    a = s.attend(q, r)
+    y = s.mlp(a)
+
+    def timed(f):
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            f()
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(10):
+                f()
+        best = None
+        for _ in range(args.trials):
+            b, e = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            graph.replay()
+            b.record()
+            for _ in range(10):
+                graph.replay()
+            e.record()
+            e.synchronize()
+            us = b.elapsed_time(e) * 10
+            best = us if best is None else min(best, us)
+        return round(best, 2)
+    parts = {"step": s.run, "qkv": s.project, "kv_extend": s.extend, "kv_append": lambda: s.append(k, v, r),
+             "kv_attention": lambda: s.attend(q, r), "o_gate_up_down": lambda: s.mlp(a), "head_and_scores": lambda: s.score(y)}
+    return {"workload": "verify_step_7b_layer", "tokens": args.verify_step, "context": args.context, "data": "synthetic",
+            "us": {n: timed(f) for n, f in parts.items()}}
+
+
 def summarize_rocprof(d, out, min_calls):
     """rocprofv3 CSV output (kernel traces, counter collections) -> a short text file.
 
@@ -487,6 +604,9 @@ def main():
     R = Runner(args)
     if args.batch_paths:
         print(json.dumps(batch_paths(R, args)), flush=True)
+        return
+    if args.verify_step is not None:
+        print(json.dumps(verify_step(R, args)), flush=True)
         return
     if args.stack:
         items = R.stack_items(args.stack)

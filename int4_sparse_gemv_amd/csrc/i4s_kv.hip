@@ -223,7 +223,11 @@ __device__ inline void quantize8(f8_t x, uint32_t (&n)[8], uint32_t &scale_bits)
   with(dpp<kXor2>(__builtin_bit_cast(uint32_t, m)));
   if constexpr (G > 32) with(dpp<kXor7>(__builtin_bit_cast(uint32_t, m)));  // the other four lanes of eight
   if constexpr (G > 64) with(dpp<kXor15>(__builtin_bit_cast(uint32_t, m)));  // the other eight of sixteen
-  const _Float16 h = (_Float16)quotient(fminf(m, 7.0f * kScaleMax), 7.0f, 1.0f / 7.0f);
+  float amax7 = quotient(fminf(m, 7.0f * kScaleMax), 7.0f, 1.0f / 7.0f);
+  // rounded to fp32 here: joined into one instruction with the conversion it
+  // would miss quotients half way between two subnormal scales
+  asm("" : "+v"(amax7));
+  const _Float16 h = (_Float16)amax7;
   const float s = (float)h, r = s > 0.0f ? __builtin_amdgcn_rcpf(s) : 0.0f, most = 7.0f * s;
   scale_bits = __builtin_bit_cast(uint16_t, h);
 #pragma unroll

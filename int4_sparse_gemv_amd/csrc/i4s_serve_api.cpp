@@ -165,16 +165,16 @@ AttentionPlan attention_plan(const i4s_attention_args &a) {
   //     / 2: 22.0 / 23.2 / 30.5; 40 x 2047 (16 rows) in 4 / 8 / 1: 13.6 / 15.2
   //     / 16.7; four waves, 40 x 4000 (64 rows) in 4 / 8: 31 / 39;
   //   with as many units as that one piece (512 x 4095: 40, in 2 / 4: 48 /
-  //     50), but none longer than 4096 keys, so that sequences of different
-  //     lengths fill the chip to the end (512 x 16384, 32 rows, in 4 / 2 / 1:
-  //     211 / 221 / 226);
+  //     50), but none longer than 4096 keys while that gives no more than about
+  //     2048 blocks (and partial results of 35 MB), so that sequences of
+  //     different lengths fill the chip to the end (512 x 16384, 32 rows, in 4
+  //     / 2 / 1: 211 / 221 / 226);
   //   a step or four of every wave are not worth a second launch on the host
   //     (32 x 1023: 10.9 in one launch, 10.0 in two).
   const int64_t units = (int64_t)p.row_blocks * c.kv_heads * (a.num_seqs > 0 ? a.num_seqs : 1);
   const int64_t step = kStepKeys * p.waves;
-  int64_t want = 256 / units;
-  if (want < (len + 4095) / 4096) want = (len + 4095) / 4096;
-  want = len <= 4 * step ? 1 : clamp_to<int64_t>(want, 1, kMaxSplits);
+  const int64_t even = clamp_to<int64_t>((len + 4095) / 4096, 1, 2048 / units + 1);
+  const int64_t want = len <= 4 * step ? 1 : clamp_to<int64_t>(256 / units, even, kMaxSplits);
   const int64_t per = clamp_to<int64_t>((len + want * step - 1) / (want * step), 1, (1 << 30) / step);
   p.chunk = (int)(per * step);
   p.splits = (int)clamp_to<int64_t>((len + p.chunk - 1) / p.chunk, 1, kMaxSplits);

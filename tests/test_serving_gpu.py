@@ -173,6 +173,28 @@ def test_append_is_bit_exact_and_read_returns_it(i4s, dim, group, tokens, heads,
             assert torch.equal(got.cpu(), torch.from_numpy(want).to(F32).to(out))  # 4-bit x fp16 is exact in fp32
 
 
+def test_quantizer_over_every_maximum(i4s):
+    """Every finite positive fp16 as a group's maximum, with values around the borders between two steps."""
+    say("quantizer")
+    rng = np.random.default_rng(4)
+    top = np.arange(1, 0x7C00, dtype=np.uint16).view(np.float16).astype(np.float64)
+    for dtype in (F16, BF16):
+        with np.errstate(over="ignore"):
+            x = top[:, None] * np.concatenate([np.ones((len(top), 1)), (rng.integers(-7, 7, (len(top), 31)) + 0.5) / 7
+                                               * (1 + rng.integers(-1, 2, (len(top), 31)) * 2.0**-10)], 1)
+        t = torch.from_numpy(x).to(dtype)
+        t[::3] *= 2.0**-9 if dtype == BF16 else 1  # bf16 reaches below fp16's range: scales that round to 0 or a step
+        t = torch.cat([t, t[:1].expand(-len(t) % 2, -1)]).reshape(-1, 1, 64)
+        n = len(t)
+        d = i4s.kv_cache(-(-n // 256), 256, 1, 64, 32)
+        slots = torch.arange(n, dtype=torch.int32).cuda()
+        i4s.kv_append(d, t.cuda(), t.cuda(), slots)
+        k, v = i4s.kv_read(d, slots, dtype=F32)
+        q, s = O.quantize(f64(t), 32)
+        np.testing.assert_array_equal(f64(k), q * s.repeat(32, -1))
+        np.testing.assert_array_equal(f64(v), q * s.repeat(32, -1))
+
+
 def test_append_special_values(i4s):
     say("append special values")
     tiny = float(torch.finfo(F16).smallest_normal)
@@ -637,6 +659,36 @@ def test_captured_step_replays(i4s):
         assert torch.equal(srv.table, eager.table) and torch.equal(srv.cache.v_vals, eager.cache.v_vals)
         lens.copy_(r.lens), count.copy_(r.free_count)
         torch.randn(100, device="cuda").sum()
+
+
+def test_verification_step_of_a_packed_layer(i4s):
+    """The step that ``bench.py --verify-step`` times, on a small layer: packed products, slots, 4-bit cache, tree
+    attention, scores; attention and scores against the oracle on the step's own inputs."""
+    say("verification step")
+    import bench
+    s = bench.VerifyStep(i4s, 7, 77, seed=3, hidden=256, heads=4, mlp=512, vocab=640)
+    before = (s.lens.clone(), s.count.clone())
+    a, y, r = s.run()
+    torch.cuda.synchronize()
+    q, k, v = s.project()
+    step = s.extend()
+    assert int(step.flags) == 0 and step.lens.tolist() == [84] and torch.equal(s.lens, before[0])
+    slots = [int(s.table[0, p // 16]) * 16 + p % 16 for p in range(84)]
+    assert step.slots.tolist() == slots[77:] and step.positions.tolist() == list(range(77, 84))
+    keys, values = i4s.kv_read(s.cache, torch.tensor(slots, dtype=torch.int32).cuda(), dtype=F32)
+    for got, x in ((keys, k), (values, v)):
+        n, f = O.quantize(f64(x).reshape(7, 4, 64), 64)
+        np.testing.assert_array_equal(f64(got)[77:], n * f.repeat(64, -1))
+    masks = [1, 0b11, 0b101, 0b1011, 0b10011, 0b100101, 0b1000101]
+    assert s.mask.tolist() == masks
+    want, _, spread = O.attention(f64(q).reshape(7, 4, 64), f64(keys), f64(values), 77, 64**-0.5, masks)
+    assert (np.abs(f64(a).reshape(7, 4, 64) - want) <= half_step(F16) * np.abs(want) + 2.0**-10 * spread).all()
+    logits = i4s.run(s.head, y)
+    lp, ent, ids, top = O.token_logprobs(f64(logits), s.given.cpu().numpy(), 8)
+    np.testing.assert_array_equal(r.top_ids.cpu().numpy(), ids)
+    # sums of 640 terms, a handful of roundings each
+    np.testing.assert_allclose(f64(r.logprobs), lp, rtol=2.0**-20)
+    np.testing.assert_allclose(f64(r.entropy), ent, rtol=2.0**-19)
 
 
 def test_two_streams_at_once(i4s):
