@@ -130,7 +130,8 @@ i4s_status i4s_kv_extend(int32_t *table, int32_t n, int32_t width, int32_t page_
  *            [0, num_pages * page_size) is not stored (-1 marks padding).  A
  *            slot may be named once: what is stored for a slot named twice is
  *            a mix of the two.
- * k, v and slots must not overlap the cache.  One kernel launch.
+ * k, v and slots must not overlap the cache; kv_heads * D * tokens is below
+ * 2^34.  One kernel launch.
  * Errors: I4S_ERR_INVALID_ARGUMENT, I4S_ERR_UNSUPPORTED, I4S_ERR_DEVICE. */
 i4s_status i4s_kv_append(const i4s_kv_cache *cache /* host */, const void *k, const void *v, int32_t dtype,
                          int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
@@ -169,7 +170,8 @@ typedef struct i4s_attention_args {
   const int32_t *lens;       /* [num_seqs]                                    */
   const int32_t *q_start;    /* [num_seqs+1], non-decreasing, or NULL: one    */
                              /* token each, num_tokens == num_seqs            */
-  int32_t max_q;             /* largest number of query tokens of a sequence  */
+  int32_t max_q;             /* largest number of query tokens of a sequence, */
+                             /* max_q * q_heads below 2^23                    */
   int32_t max_len;           /* largest length (0: table_width * page_size);  */
                              /* sizes the launch                              */
   float scale;               /* > 0, finite                                   */
@@ -203,7 +205,7 @@ i4s_status i4s_attention(const i4s_attention_args *a /* host */, void *stream);
 
 /* Log probabilities of given tokens, the entropy of each row's distribution
  * and its top alternatives, over logits [rows][vocab] (row r at r * stride
- * elements): with m = max_j x_j and l = sum_j exp(x_j - m),
+ * elements, rows below 2^23): with m = max_j x_j and l = sum_j exp(x_j - m),
  *   logprobs[r] = x[tokens[r]] - m - ln l            (fp32)
  *   entropy[r]  = ln l - sum_j (x_j - m) exp(x_j - m) / l   (fp32, nats)
  *   top_ids[r][i], top_logprobs[r][i], i < top_k: the largest logits in

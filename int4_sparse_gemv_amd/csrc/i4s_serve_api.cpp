@@ -17,7 +17,8 @@ using i4s::overlap;
 
 namespace {
 
-constexpr int64_t kMaxGrid = 0x7FFFFFFF;
+// blocks along one axis of a grid: threads are counted in 32 bits, up to 512 a block
+constexpr int64_t kMaxBlocks = 0x7FFFFF;
 
 struct Span {
   const void *p;
@@ -118,10 +119,8 @@ i4s_status check_attention(const i4s_attention_args *a) {
     return fail(I4S_ERR_INVALID_ARGUMENT, "scale=%g must be positive and finite", (double)a->scale);
   if (a->tree_mask && a->max_q > I4S_MAX_TREE)
     return fail(I4S_ERR_INVALID_ARGUMENT, "a tree mask needs max_q=%d at most %d", a->max_q, I4S_MAX_TREE);
-  const i4s::AttentionPlan p = i4s::attention_plan(*a);
-  if ((int64_t)p.row_blocks * c.kv_heads * a->num_seqs > kMaxGrid || (int64_t)a->max_q * a->q_heads > kMaxGrid)
-    return fail(I4S_ERR_INVALID_ARGUMENT, "too many query rows: num_seqs=%d, max_q=%d, q_heads=%d", a->num_seqs,
-                a->max_q, a->q_heads);
+  if ((int64_t)a->max_q * a->q_heads > kMaxBlocks)
+    return fail(I4S_ERR_INVALID_ARGUMENT, "max_q=%d times q_heads=%d must be below 2^23", a->max_q, a->q_heads);
   return I4S_OK;
 }
 
@@ -130,7 +129,7 @@ int dtype_size(int32_t dtype) { return dtype == I4S_F32 ? 4 : 2; }
 i4s_status check_logprobs(int32_t dtype, int32_t rows, int32_t vocab, int32_t top_k) {
   if (dtype != I4S_F16 && dtype != I4S_BF16 && dtype != I4S_F32)
     return fail(I4S_ERR_INVALID_ARGUMENT, "dtype=%d must be I4S_F16, I4S_BF16 or I4S_F32", dtype);
-  if (rows < 0) return fail(I4S_ERR_INVALID_ARGUMENT, "rows=%d must be 0 or more", rows);
+  if (rows < 0 || rows > kMaxBlocks) return fail(I4S_ERR_INVALID_ARGUMENT, "rows=%d must be in [0, 2^23)", rows);
   if (vocab < 1 || vocab > I4S_MAX_VOCAB)
     return fail(I4S_ERR_INVALID_ARGUMENT, "vocab=%d must be in [1, %d]", vocab, I4S_MAX_VOCAB);
   if (top_k < 0 || top_k > I4S_MAX_TOP_K || top_k > vocab)
@@ -258,8 +257,8 @@ i4s_status i4s_kv_append(const i4s_kv_cache *cache, const void *k, const void *v
   if (st != I4S_OK) return st;
   if (dtype != I4S_F16 && dtype != I4S_BF16)
     return fail(I4S_ERR_INVALID_ARGUMENT, "dtype=%d must be I4S_F16 or I4S_BF16", dtype);
-  if (tokens < 0 || ((int64_t)tokens * cache->head_dim / 2048 + 1) * cache->kv_heads > kMaxGrid)
-    return fail(I4S_ERR_INVALID_ARGUMENT, "tokens=%d must be 0 or more, and kv_heads * head_dim * tokens less than 2^42", tokens);
+  if (tokens < 0 || ((int64_t)tokens * cache->head_dim / 2048 + 1) * cache->kv_heads > kMaxBlocks)
+    return fail(I4S_ERR_INVALID_ARGUMENT, "tokens=%d must be 0 or more, and kv_heads * head_dim * tokens below 2^34", tokens);
   st = check_strides(k_token_stride, k_head_stride, "k");
   if (st != I4S_OK) return st;
   st = check_strides(v_token_stride, v_head_stride, "v");
@@ -292,8 +291,8 @@ i4s_status i4s_kv_read(const i4s_kv_cache *cache, const int32_t *slots, int32_t 
   if (st != I4S_OK) return st;
   if (dtype != I4S_F16 && dtype != I4S_BF16 && dtype != I4S_F32)
     return fail(I4S_ERR_INVALID_ARGUMENT, "dtype=%d must be I4S_F16, I4S_BF16 or I4S_F32", dtype);
-  if (tokens < 0 || ((int64_t)tokens * cache->head_dim / 2048 + 1) * cache->kv_heads > kMaxGrid)
-    return fail(I4S_ERR_INVALID_ARGUMENT, "tokens=%d must be 0 or more, and kv_heads * head_dim * tokens less than 2^42", tokens);
+  if (tokens < 0 || ((int64_t)tokens * cache->head_dim / 2048 + 1) * cache->kv_heads > kMaxBlocks)
+    return fail(I4S_ERR_INVALID_ARGUMENT, "tokens=%d must be 0 or more, and kv_heads * head_dim * tokens below 2^34", tokens);
   if (tokens == 0) return I4S_OK;
   if (!k_out || !aligned(k_out, 16) || !v_out || !aligned(v_out, 16))
     return fail(I4S_ERR_INVALID_ARGUMENT, "k_out or v_out is NULL or not 16-byte aligned");

@@ -96,7 +96,7 @@ APPEND = dict(k=5 * GIB, v=6 * GIB, dtype=0, kt=128, kh=64, vt=128, vh=64, slots
 
 
 @pytest.mark.parametrize("change", [dict(k=None), dict(v=6 * GIB + 8), dict(dtype=2), dict(dtype=-1), dict(kt=12), dict(vh=-8),
-                                    dict(kt=1 << 41), dict(slots=None), dict(slots=7 * GIB + 1), dict(tokens=-1),
+                                    dict(kt=1 << 41), dict(slots=None), dict(slots=7 * GIB + 1), dict(tokens=-1), dict(tokens=2**31 - 1),
                                     dict(k=GIB + 64), dict(v=4 * GIB), dict(slots=3 * GIB)])
 def test_append_refuses(lib, change):
     a = dict(APPEND, **change)
@@ -168,15 +168,16 @@ def test_attention_workspace(lib):
     assert lib.i4s_attention_workspace_size(ctypes.byref(a), None) == BAD
     assert lib.i4s_attention_workspace_size(None, ctypes.byref(n)) == BAD
     assert lib.i4s_attention(None, None) == BAD
-    big = attention(cache(), num_seqs=65535, max_q=1 << 20, tree_mask=None, q_heads=65536)
-    assert S.i4s_attention_workspace_size(big, n) == BAD
+    for q, heads in ((1 << 20, 65536), (1 << 20, 8), (1 << 7, 65536)):
+        big = attention(cache(), num_seqs=65535, max_q=q, tree_mask=None, q_heads=heads)
+        assert S.i4s_attention_workspace_size(big, n) == BAD
 
 
 LOGPROBS = dict(logits=GIB, dtype=0, rows=3, vocab=90000, stride=90000, tokens=2 * GIB, top_k=5, lp=3 * GIB, ent=4 * GIB,
                 ids=5 * GIB, top=6 * GIB, ws=7 * GIB, ws_bytes=1 << 20)
 
 
-@pytest.mark.parametrize("change", [dict(logits=None), dict(logits=GIB + 1), dict(dtype=3), dict(rows=-1), dict(vocab=0),
+@pytest.mark.parametrize("change", [dict(logits=None), dict(logits=GIB + 1), dict(dtype=3), dict(rows=-1), dict(rows=1 << 23), dict(vocab=0),
                                     dict(vocab=(1 << 30) + 1), dict(stride=89999), dict(tokens=None), dict(tokens=2 * GIB + 4),
                                     dict(top_k=-1), dict(top_k=33), dict(vocab=4), dict(lp=None), dict(ent=4 * GIB + 1),
                                     dict(ids=None), dict(top=None), dict(ids=6 * GIB), dict(lp=4 * GIB), dict(ws=None),
