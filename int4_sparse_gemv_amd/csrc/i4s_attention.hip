@@ -648,6 +648,42 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionKernelArgs
   if (d == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
 }
 
+// The same for few pieces: D/4 neighbouring threads hold a row and take its
+// pieces one after the other, 1024/D rows a block (16384 rows of 4 pieces: 20
+// us with a block a row, 9 so).
+constexpr int kFewSplits = 8;
+template <typename T, int D>
+__global__ __launch_bounds__(256) void attention_join_few_kernel(AttentionKernelArgs a) {
+  const int q_heads = a.kv_heads * a.share;
+  const Work w = work_of(a, blockIdx.y);
+  const int i = blockIdx.x * (1024 / D) + threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;  // row of the sequence
+  if (i >= min(w.q_len, a.max_q) * q_heads || w.used == 1) return;
+  const int64_t rows = (int64_t)a.num_tokens * q_heads, row = (int64_t)w.q0 * q_heads + i;
+  float mo[kFewSplits], l[kFewSplits], m = kLowest;
+  f4_t v[kFewSplits];
+#pragma unroll
+  for (int s = 0; s < kFewSplits; ++s) {
+    const int at = min(s, w.used - 1);  // loads without branches
+    mo[s] = a.part_ml[2 * (at * rows + row)];
+    l[s] = a.part_ml[2 * (at * rows + row) + 1];
+    v[s] = *reinterpret_cast<const f4_t *>(a.part_o + (at * rows + row) * D + d);
+    m = fmaxf(m, mo[s]);
+  }
+  f4_t o = {0, 0, 0, 0};
+  float sum = 0.0f;
+#pragma unroll
+  for (int s = 0; s < kFewSplits; ++s)
+    if (s < w.used) {
+      const float f = __builtin_amdgcn_exp2f(mo[s] - m);
+      sum = fmaf(l[s], f, sum);
+      o += v[s] * f;
+    }
+  o *= sum == 0.0f ? 0.0f : 1.0f / sum;
+  const w2_t bits = {T::from_float(o[0]) | T::from_float(o[1]) << 16, T::from_float(o[2]) | T::from_float(o[3]) << 16};
+  *reinterpret_cast<w2_t *>(static_cast<uint16_t *>(a.out) + row * D + d) = bits;
+  if (d == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+}
+
 template <typename T, int D, int G, int RT>
 hipError_t go(const AttentionKernelArgs &a, const AttentionPlan &p, hipStream_t stream) {
   const size_t join = sizeof(float) * p.waves * (16 * RT * 2 + 16 * (D + 4));
@@ -662,6 +698,11 @@ hipError_t go(const AttentionKernelArgs &a, const AttentionPlan &p, hipStream_t 
                      dim3(64 * p.waves), lds, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
+  if (p.splits <= kFewSplits) {
+    const unsigned rows = (unsigned)a.max_q * a.kv_heads * a.share, per = 1024 / D;
+    hipLaunchKernelGGL((attention_join_few_kernel<T, D>), dim3((rows + per - 1) / per, a.num_seqs), dim3(256), 0, stream, a);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3((unsigned)a.max_q * a.kv_heads * a.share, a.num_seqs), dim3(256),
                      0, stream, a);
   return hipGetLastError();
