@@ -291,13 +291,28 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
     }
     if (lane < 8 * NG) copy16(my_scales + (my_tile ? token1 : token0) * NG + my_piece, to + St::kKs);
   };
-  const auto load_step = [&](int s, char *to) {
-    const int tile0 = min(2 * s, last_tile), tile1 = min(2 * s + 1, last_tile);
-    load(token_of(tile0, row_of_table[tile0 >> tile_shift]), token_of(tile1, row_of_table[tile1 >> tile_shift]), to);
+  // the page numbers of a step's tiles, read one step before they are needed
+  struct Pages {
+    int tile[2];
+    int32_t page[2];
   };
+  const auto pages_of = [&](int s) {
+    Pages p;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      p.tile[t] = min(2 * s + t, last_tile);
+      p.page[t] = row_of_table[p.tile[t] >> tile_shift];
+    }
+    return p;
+  };
+  const auto load_step = [&](const Pages &p, char *to) {
+    load(token_of(p.tile[0], p.page[0]), token_of(p.tile[1], p.page[1]), to);
+  };
+  Pages ahead = {};
   if (first < step1) {
     load(token_of(2 * first, early[0]), token_of(2 * first + 1, early[1]), stages);
-    if (first + waves < step1) load_step(first + waves, stages + St::kBytes);
+    if (first + waves < step1) load_step(pages_of(first + waves), stages + St::kBytes);
+    ahead = pages_of(first + 2 * waves);
   }
 
   // the query rows: lane (i, a) holds channels 32j + 8a .. +7 of row i
@@ -536,7 +551,8 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
     if (s + 2 * waves < step1) {
       __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this stage is read
       issue_fence();
-      load_step(s + 2 * waves, stage);
+      load_step(ahead, stage);
+      ahead = pages_of(s + 3 * waves);
     }
     at = St::kBytes - at;
   }
