@@ -53,6 +53,7 @@ struct F16 {
   typedef hf8_t vec;
   static constexpr uint32_t kMask = 0x03C003C0u, kSixteen = 0x4C004C00u;
   static constexpr int kShift = 6;  // left shift of nibble 0
+  static constexpr bool kCoarse = false;
   static __device__ f4_t mfma(vec a, vec b, f4_t c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
   static __device__ float to_float(uint32_t bits) { return fp16_bits_to_float(bits); }
   static __device__ uint32_t from_float(float f) { return float_to_fp16_bits(f); }
@@ -61,6 +62,7 @@ struct BF16 {
   typedef bf8_t vec;
   static constexpr uint32_t kMask = 0x00780078u, kSixteen = 0x41804180u;
   static constexpr int kShift = 3;
+  static constexpr bool kCoarse = true;  // its rounding, next to fp16's
   static __device__ f4_t mfma(vec a, vec b, f4_t c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
   static __device__ float to_float(uint32_t bits) { return __builtin_bit_cast(float, bits << 16); }
   static __device__ uint32_t from_float(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
@@ -228,9 +230,13 @@ template <typename T, int D, int G, int RT>
 __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>())) void attention_kernel(AttentionKernelArgs a) {
   constexpr int NG = D / G, KJ = D / 32, NC = D / 64;
   constexpr bool kBiasInSum = NG * RT <= (D == 256 ? 4 : 8);  // else the registers are needed elsewhere
-  // V's scales go to the probabilities where those are few (16 RT rows x NG
-  // groups), else to the values: one more rounding to fp16, of the scaled value
-  constexpr bool kScaleV = NG * RT >= 8;
+  // V's scales go to the probabilities, which are rounded to fp16 once, after
+  // that: next to an fp16 output's own rounding that makes 1.4 of its error.
+  // Where the probabilities are many (16 RT rows x NG groups) and the output
+  // is bf16, whose rounding is eight times as coarse, they go to the values: one
+  // more rounding to fp16, of the scaled value (512 x 16384 keys, 32 rows, G =
+  // 32: 256 us with the scales on the probabilities, 222 so).
+  constexpr bool kScaleV = NG * RT >= 8 && T::kCoarse;
   constexpr int kRowStride = D + 4;          // floats; the 16 rows of a store fall in distinct banks
   extern __shared__ __align__(16) float lds[];
   const int waves = blockDim.x / 64;

@@ -15,7 +15,7 @@ are scaled so that the largest scale's power of two lies at 2^6 at least when
 the probability is that of the key that set the row's offset (a maximum when
 it was set, so the sum that divides is at least its 1): 2^-31 of the largest
 scale for every key, times a value of at most 7.  Where the values carry V's
-scale instead (wide blocks of rows) each is rounded once to fp16 too: another
+scale instead (wide blocks of rows, bf16) each is rounded once to fp16 too: another
 2^-11 of sum p |v|.
 """
 
@@ -288,7 +288,7 @@ def check_attention(i4s, rng, c, d, lens, q_lens, share, dtype, tree=False, scal
     assert torch.equal(first, out), "two calls differ"
     got, got_lse = f64(out[:total]), f64(lse[:total])
     rows = max(max(q_lens), 1) * share
-    wide = (2 if rows > 16 and dim // c.group >= 4 else 1) * (dim // c.group) >= 8
+    wide = dtype == BF16 and (2 if rows > 16 and dim // c.group >= 4 else 1) * (dim // c.group) >= 8
     for i, (l, n_q) in enumerate(zip(lens, q_lens)):
         slots = [int(table[i, j // page]) * page + j % page for j in range(l)]
         k, v = c.read(slots)
