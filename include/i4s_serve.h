@@ -101,7 +101,9 @@ i4s_status i4s_kv_cache_sizes(int32_t num_pages, int32_t page_size, int32_t kv_h
  *   lens_out  : int32 [n], lens + new_lens.
  *   q_start   : int32 [n+1], where the new tokens of each request begin.
  *   slots     : int32 [capacity], the slot of each new token in request order
- *               (table entry * page_size + position % page_size), then -1.
+ *               (table entry * page_size + position % page_size), then -1;
+ *               also -1 where the page number is negative or its slots would
+ *               pass 2^31 - 1.
  *   positions : int32 [capacity], the position of each new token in its
  *               request, then 0.
  *   free_count_out : int32, the free pages that are left.

@@ -132,7 +132,9 @@ __global__ __launch_bounds__(1024) void kv_extend_kernel(ExtendArgs a) {
     const int32_t old_pages = (int32_t)(((int64_t)have + page - 1) >> a.shift), p = pos >> a.shift;
     const int32_t number = p < old_pages ? a.table[(int64_t)i * a.width + p]
                                          : a.free_pages[count - 1 - (page_start[i] + (p - old_pages))];
-    a.slots[v] = (int32_t)(((uint32_t)number << a.shift) + (uint32_t)(pos & (page - 1)));
+    // a number that no cache can have must not come round to another page's slots
+    const bool real = number >= 0 && number <= 0x7FFFFFFF >> a.shift;
+    a.slots[v] = real ? (number << a.shift) + (pos & (page - 1)) : -1;
     a.positions[v] = pos;
     if (v < pages) {  // every new page holds a new token, so pages <= tokens
       const int j = owner(page_start, (int32_t)v);

@@ -158,7 +158,8 @@ def extend(table, lens, new, free, count, page_size, capacity):
             if pos % page_size == 0:
                 count -= 1
                 table[i, pos // page_size] = free[count]
-            slots[at] = int(table[i, pos // page_size]) * page_size + pos % page_size
+            page = int(table[i, pos // page_size])
+            slots[at] = page * page_size + pos % page_size if 0 <= page < 2**31 // page_size else -1
             positions[at] = pos
             at += 1
     starts[n] = at

@@ -119,6 +119,18 @@ def test_extend_changes_nothing_when_something_does_not_fit(i4s, what, flags):
     assert w["flags"] == flags
 
 
+@pytest.mark.parametrize("page", [16, 256])
+def test_extend_page_numbers_that_no_cache_has(i4s, page):
+    # in the table and in the free list: none comes round to another page's slots
+    say("extend bad page numbers", page)
+    shift = page.bit_length() - 1
+    most = (2**31 - 1) >> shift
+    odd = [-1, -2**31, most + 1, 2**(32 - shift) % 2**31, most, 7, 2**31 - 1, -2**31 + 3]
+    table = np.array(odd).reshape(-1, 1).repeat(2, 1)
+    w = extend_both(i4s, table, [page - 3] * len(odd), [5] * len(odd), odd[::-1], len(odd), page, 5 * len(odd))
+    assert w["flags"] == 0 and max(w["slots"]) == 2**31 - 1 and w["slots"].count(-1) == 5 * 6
+
+
 def test_extend_nothing_to_do(i4s):
     say("extend empty")
     extend_both(i4s, np.zeros((2, 3), np.int64), [5, 0], [0, 0], [1], 1, 16, 0)
