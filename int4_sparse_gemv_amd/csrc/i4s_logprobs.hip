@@ -117,8 +117,8 @@ __device__ inline float logprob_of(const Stats &s, float x) {
   return (x - s.e) - __builtin_amdgcn_logf(s.l) * kLn2;
 }
 
-__device__ inline void write_row(const LogprobsArgs &a, int row, const Stats &s, const float *x) {
-  a.logprobs[row] = x ? logprob_of(s, *x) : NAN;
+__device__ inline void write_row(const LogprobsArgs &a, int row, const Stats &s, bool valid, float x) {
+  a.logprobs[row] = valid ? logprob_of(s, x) : NAN;
   float h = 0.0f;
   if (bad(s))
     h = NAN;
@@ -404,7 +404,7 @@ __global__ __launch_bounds__(NT) void logprobs_kernel(LogprobsArgs a, int splits
     held = min(held, k);
   }
   if (splits == 1) {
-    if (tid == 0) write_row(a, row, s, valid ? &token_x : nullptr);
+    if (tid == 0) write_row(a, row, s, valid, token_x);
     if (tid < k) write_top(a, row, tid, sel.best[tid], s);
   } else {
     const int64_t part = (int64_t)row * splits + split;
@@ -439,7 +439,7 @@ __global__ __launch_bounds__(NT) void logprobs_join_kernel(LogprobsArgs a, int s
     const bool valid = token >= 0 && token < a.vocab;
     const char *base = static_cast<const char *>(a.logits) + (int64_t)row * a.stride * T::kSize;
     const float x = valid ? T::one(base, token) : 0.0f;
-    write_row(a, row, s, valid ? &x : nullptr);
+    write_row(a, row, s, valid, x);
     sel.n_cand = 0;
   }
   if (!k) return;
