@@ -33,8 +33,8 @@
 //
 // Bound by: memory while few query rows share a key (a key of one head is D +
 // 4D/G bytes; a copy of such sizes reaches 4.8 TB/s): 512 x up to 4095 keys, one
-// row, D = 128, G = 64: 170 MB in 40 us, 4.3 TB/s; 8 x 131071 keys, 4 rows: 143
-// MB in 30 us, 4.8 TB/s, and 4.7 us for the join of its 32 pieces.  With 32 rows a
+// row, D = 128, G = 64: 170 MB in 39 us, 4.3 TB/s; 8 x 131071 keys, 4 rows: 143
+// MB in 29 us, 4.9 TB/s, and 4.0 us for the join of its 32 pieces.  With 32 rows a
 // key the vector instructions count (two for each widened pair, an exponential
 // and a scaling for each score) and the two waves a SIMD that the registers
 // leave: 512 x up to 16384 keys, G = 32: 675 MB in 188 us, 3.6 TB/s, the matrix
@@ -42,6 +42,8 @@
 // 11 us.
 
 #include <float.h>
+
+#include <type_traits>
 
 #include "i4s_gemv_common.h"
 #include "i4s_serve_internal.h"
@@ -197,8 +199,13 @@ typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(1))) const void global_void;
 typedef const __attribute__((address_space(4))) int32_t scalar_int32;  // read with scalar loads
 
+// Keys that one block alone reads go past the caches (`once`), those that the
+// blocks of other query rows read too do not: 8 x 131071 keys, 4 rows: 34.7 /
+// 32.3 us without / with; 128 x 4000, 128 rows: 97 / 116.
+constexpr int kNonTemporal = 2;
+template <bool ONCE>
 __device__ inline void copy16(const void *from, char *to) {
-  __builtin_amdgcn_global_load_lds((global_void *)from, (lds_void *)to, 16, 0, 0);
+  __builtin_amdgcn_global_load_lds((global_void *)from, (lds_void *)to, 16, 0, ONCE ? kNonTemporal : 0);
 }
 
 // Waits until at most N vector loads are on their way (s_waitcnt vmcnt).
@@ -289,22 +296,30 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
   const uint16_t *my_scales = lane / (4 * NG) ? a.v_scales : a.k_scales;
   const bool my_tile = lane / (2 * NG) % 2;
   const int my_piece = lane % (2 * NG) * 8;
-  const auto load = [&](int64_t token0, int64_t token1, char *to) {
+  const auto load_as = [&](auto once, int64_t token0, int64_t token1, char *to) {
+    constexpr bool kOnce = decltype(once)::value;
     if constexpr (D == 64) {
       const int64_t mine = (lane / 32 ? token1 : token0) * (D / 2) + lane % 32 * 16;
-      copy16(a.k_vals + mine, to);
-      copy16(a.v_vals + mine, to + St::kV);
+      copy16<kOnce>(a.k_vals + mine, to);
+      copy16<kOnce>(a.v_vals + mine, to + St::kV);
     } else {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int h = 0; h < D / 128; ++h) {
           const int64_t token = t ? token1 : token0;
-          copy16(a.k_vals + token * (D / 2) + (li * (D / 2) + la * (D / 8) + 16 * h), to + t * St::kTile + 1024 * h);
-          copy16(a.v_vals + token * (D / 2) + (la * (2 * D) + li * (D / 8) + 16 * h), to + St::kV + t * St::kTile + 1024 * h);
+          copy16<kOnce>(a.k_vals + token * (D / 2) + (li * (D / 2) + la * (D / 8) + 16 * h), to + t * St::kTile + 1024 * h);
+          copy16<kOnce>(a.v_vals + token * (D / 2) + (la * (2 * D) + li * (D / 8) + 16 * h), to + St::kV + t * St::kTile + 1024 * h);
         }
     }
-    if (lane < 8 * NG) copy16(my_scales + (my_tile ? token1 : token0) * NG + my_piece, to + St::kKs);
+    if (lane < 8 * NG) copy16<kOnce>(my_scales + (my_tile ? token1 : token0) * NG + my_piece, to + St::kKs);
+  };
+  const bool alone = a.row_blocks == 1;
+  const auto load = [&](int64_t token0, int64_t token1, char *to) {
+    if (alone)
+      load_as(std::true_type(), token0, token1, to);
+    else
+      load_as(std::false_type(), token0, token1, to);
   };
   // the page numbers of a step's tiles, read one step before they are needed
   struct Pages {

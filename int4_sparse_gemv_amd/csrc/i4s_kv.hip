@@ -186,7 +186,7 @@ __device__ inline f8_t load8(const uint16_t *p) {
 //
 // Bound by: memory, 2 bytes read and a little over half a byte written a
 // value.  8191 tokens x 40 heads of 128, bf16, G = 64, sliced out of a fused
-// product: 213 MB in 44 us, 4.8 TB/s (57 us with
+// product: 213 MB in 45 us, 4.7 TB/s (57 us with
 // ordinary loads: k and v are read once); 16 tokens x 32 heads 2.8 us.
 
 template <int CTRL>
@@ -317,15 +317,16 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a, int shift)
 // ---------------------------------------------------------------------------
 // reading tokens: the same lanes the other way round
 //
-// Bound by: memory.  The same 8191 tokens: 213 MB in 41 us, 5.2 TB/s (the cache,
-// just written, partly comes out of the last-level cache); 16 tokens 2.9 us.
+// Bound by: memory.  The same 8191 tokens: 213 MB in 34 us, 6.3 TB/s (the cache,
+// just written, comes out of the last-level cache; 41 us with ordinary stores);
+// 16 tokens 2.9 us.
 
 template <typename T>
 __device__ inline void store8(void *p, int64_t at, const f8_t &x) {
   u4_t w;
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = T::from_float(x[2 * i]) | T::from_float(x[2 * i + 1]) << 16;
-  *reinterpret_cast<u4_t *>(static_cast<uint16_t *>(p) + at) = w;
+  __builtin_nontemporal_store(w, reinterpret_cast<u4_t *>(static_cast<uint16_t *>(p) + at));
 }
 struct Float {};
 template <>
