@@ -79,10 +79,11 @@ struct BF16 {
 };
 
 constexpr float kOffset = 24.0f;   // 16 of the widening + 8 of the nibble
-constexpr float kLowest = -1e38f;  // exponent offset of a row that has seen no key
+constexpr float kLowest = -FLT_MAX;  // exponent offset of a row that has seen no key
 // A row's offset follows its running maximum only when that has grown by more
 // than this (log2): with 16 rows or more a wave some row's maximum grows in
-// most steps, and every change scales all of O.
+// most steps, and every change scales all of O.  (The maximum starts at -inf, so
+// that a row's first key sets the offset however small the scale of scores is.)
 constexpr float kSlack = 8.0f;
 
 // (a & m) | c.  In one v_and_or_b32 if the constants are in registers (the
@@ -377,7 +378,7 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
   float mx[RT], mo[RT], l[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    mx[r] = -FLT_MAX;
+    mx[r] = -INFINITY;
     mo[r] = kLowest;
     l[r] = 0.0f;
 #pragma unroll
