@@ -13,23 +13,43 @@
 //     32j + 8a .. +7, j = 0..D/32-1: neighbours in the format, so that one
 //     wide load per lane covers 16 keys without a gap.  The tile comes out
 //     with query row i and keys 4a .. 4a+3 in lane l.
-//   O^T = V^T P^T: v_mfma_f32_16x16x32_f16 with 16 channels as rows, 16 query
+//   O^T = V^T P^T: v_mfma_f32_16x16x32 with 16 channels as rows, 16 query
 //     rows as columns and 32 keys.  Its B operand wants query row i and 8
 //     keys in lane l: take the keys 4a .. 4a+3 of two tiles, and P is in
 //     place as S came out.  Its A operand wants channel i (of 16) and the
 //     same 8 keys: the format keeps the words of channel i for 4 neighbouring
 //     tokens together, and a v_perm_b32 of two tokens' words puts their
-//     halves into one dword, whose nibbles then widen to fp16 pairs (token,
-//     next token) of one channel.
+//     halves into one dword, whose nibbles then widen to pairs (token, next
+//     token) of one channel.
 // 4-bit values are widened with bit operations: for K the nibble goes into
 // the mantissa of 16.0 (16 + u, exact in fp16 and bf16), and the offset 24 =
 // 16 + 8 leaves with the sum: the products start from -24 * sum(q) of the
-// group's channels, in fp32.  For V the values become exact fp16 integers.
+// group's channels, in fp32, so that a score's rounding error follows sum |q|
+// (|k| + 24 s), s K's scale, not the score.
+//
 // Scales: K's multiply the fp32 sums of a group's channels; V's multiply the
-// probabilities, which are rounded to fp16 once, after that.  So that no
-// probability loses bits to fp16's range the offset of the exponent includes
-// a power of two that brings (largest probability) x (largest V scale seen so
-// far) between 2^6 and 2^15.
+// probabilities, in fp32, and the products go to the matrix instruction as two
+// bf16 terms, the value rounded and what that left, rounded: 2^-16 of it, at any
+// size, since bf16 has fp32's exponents.  (One fp16 term made a third more error
+// than an fp16 output's own rounding, and lost whole bits of values that lay far
+// below the largest product of probability and scale, in any group.)  V's
+// nibbles become 16 + u for even tokens and -(31 - u) for odd ones, exact in bf16
+// too: the value + 24 and - 23, two offsets that mostly cancel; what they add
+// is summed beside (`extra`, v_dot2) and leaves at the end.
+// Up to 8 rows fill half of the 16 columns only: there the other half takes the
+// second terms of the same rows (PAIR), at no cost in matrix instructions.  Us,
+// one term in fp16 / two in turn / two side by side: 16 x up to 4095 keys, 32
+// heads 40.3 / 46.9 / 41.9, 131071 keys, 8 heads x 4 rows 34.8 / 39.9 / 36.0.
+//
+// Where the probabilities are many (row tiles x groups >= 8) V's scales go to
+// V's values instead.  For fp16 outputs probabilities and scaled values are
+// two fp16 terms each (a 4-bit value times a scale is exact in two, and the
+// product of the two second terms, 2^-22, is left out); for bf16 outputs, whose
+// own rounding is eight times as coarse, one each: 2^-11 of either.  Us, 512 x up
+// to 16384 keys, 32 rows, G = 32: 197 with one term each, 240 with two, 287 with
+// V's scales of four groups on the probabilities.  The probability of the key that
+// set a row's offset is 2^7 at least and the smallest step of fp16 2^-31 of that:
+// whatever else a wave sees, a key's value loses at most half of it.
 //
 // Bound by: memory while few query rows share a key (a key of one head is D +
 // 4D/G bytes; a copy of such sizes reaches 4.8 TB/s): 512 x up to 4095 keys, one
@@ -56,6 +76,8 @@ typedef __bf16 bf8_t __attribute__((ext_vector_type(8)));
 typedef float f4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t w4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t w2_t __attribute__((ext_vector_type(2)));
+typedef float f2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
 
 // fp16 and bf16 query types: the matrix instruction, and how nibble p (and
 // p + 4, 16 bits on) of a word becomes 16 + u.
@@ -101,9 +123,24 @@ __device__ inline uint32_t in_vgpr(uint32_t v) {
   return v;
 }
 
+// Masks and magic numbers of the widening.
 struct Constants {
-  uint32_t k_mask, k_sixteen, v_low, v_high, v_magic;
+  uint32_t k_mask, k_sixteen, v_mask, v_pair, v_low, v_high, v_magic;
 };
+
+// Nibbles p and p + 4 of w, p = 0..3, as exact bf16 pairs (16 + u, -(31 - u)):
+// the values + 24 and - 23 (one v_bitop3_b32 each after the shift).
+__device__ inline void widen_v(uint32_t w, const Constants &k, uint32_t q[4]) {
+  q[0] = (w << 3 & k.v_mask) ^ k.v_pair;
+  q[1] = (w >> 1 & k.v_mask) ^ k.v_pair;
+  q[2] = (w >> 5 & k.v_mask) ^ k.v_pair;
+  q[3] = (w >> 9 & k.v_mask) ^ k.v_pair;
+}
+constexpr uint32_t kPairBias = 0xC1B841C0u;  // (24, -23) in bf16
+
+__device__ inline float dot2(bf2_t a, uint32_t b, float c) {
+  return __builtin_amdgcn_fdot2_f32_bf16(a, __builtin_bit_cast(bf2_t, b), c, false);
+}
 
 // Nibbles p and p + 4 of w, p = 0..3, as exact fp16 pairs u - 8: the nibble
 // goes into the mantissa of 1024 at its place 0..3 or 4..7.
@@ -231,11 +268,18 @@ __device__ inline void read_words(uint32_t *to, const char *from) {
   }
 }
 
+// V's scale on V's values, in fp16: see the top.
+template <int D, int G, int RT>
+constexpr bool scale_on_v() {
+  return D / G * RT >= 8;
+}
+
 // Waves a SIMD should hold: what O (4 D RT / 64 registers), Q and a step's words
-// leave of its 512 registers, without scratch.
-template <int D, int RT>
+// leave of its 512 registers, without scratch.  Blocks of eight waves put two on
+// every SIMD, so theirs are two or four.
+template <int D, int G, int RT>
 constexpr int waves_per_simd() {
-  return D * RT <= 64 ? 4 : (D * RT <= 128 ? 3 : (D * RT <= 256 ? 2 : 1));
+  return D * RT <= 64 ? 4 : (D * RT <= 128 ? (D / G <= 2 ? 4 : 2) : (D * RT <= 256 ? 2 : 1));
 }
 
 template <int D, int RT>
@@ -243,17 +287,13 @@ constexpr int most_threads() {
   return D * RT <= 128 ? 512 : 256;
 }
 
-template <typename T, int D, int G, int RT>
-__global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>())) void attention_kernel(AttentionKernelArgs a) {
+template <typename T, int D, int G, int RT, bool PAIR>
+__global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, G, RT>())) void attention_kernel(AttentionKernelArgs a) {
   constexpr int NG = D / G, KJ = D / 32, NC = D / 64;
   constexpr bool kBiasInSum = NG * RT <= (D == 256 ? 4 : 8);  // else the registers are needed elsewhere
-  // V's scales go to the probabilities, which are rounded to fp16 once, after
-  // that: next to an fp16 output's own rounding that makes 1.4 of its error.
-  // Where the probabilities are many (16 RT rows x NG groups) and the output
-  // is bf16, whose rounding is eight times as coarse, they go to the values: one
-  // more rounding to fp16, of the scaled value (512 x 16384 keys, 32 rows, G =
-  // 32: 256 us with the scales on the probabilities, 222 so).
-  constexpr bool kScaleV = NG * RT >= 8 && T::kCoarse;
+  constexpr bool kScaleV = scale_on_v<D, G, RT>();
+  static_assert(!PAIR || (RT == 1 && !kScaleV));
+  constexpr bool kTwo = !(kScaleV && T::kCoarse);  // terms of a probability, and of a scaled value
   constexpr int kRowStride = D + 4;          // floats; the 16 rows of a store fall in distinct banks
   extern __shared__ __align__(16) float lds[];
   const int waves = blockDim.x / 64;
@@ -353,7 +393,7 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
   uint64_t tree[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    const int row = row0 + 16 * r + li;
+    const int row = row0 + 16 * r + (PAIR ? li % 8 : li);
     const bool has = row < rows;
     const int token = w.q0 + (has ? row / a.share : 0), qh = head * a.share + (has ? row % a.share : 0);
     const uint16_t *p = static_cast<const uint16_t *>(a.q) + token * a.q_token + qh * a.q_head + 8 * la;
@@ -375,22 +415,27 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
   }
 
   f4_t o[RT][NC][4];
-  float mx[RT], mo[RT], l[RT];
+  float mx[RT], mo[RT], l[RT], extra[RT][kScaleV ? 1 : NG];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     mx[r] = -INFINITY;
     mo[r] = kLowest;
     l[r] = 0.0f;
 #pragma unroll
+    for (float &x : extra[r]) x = 0.0f;
+#pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[r][c][e] = f4_t{0, 0, 0, 0};
   }
-  uint32_t cap = 0;   // fp16 bits: no V scale so far was larger
-  float cap_log2 = kScaleV ? 15.0f - kSlack : 0.0f;
+  // fp16 terms use that type's range up to 2^15, bf16 terms need not
+  // (-1, 0) and (0, -1) in bf16; in registers, as the compiler takes the second
+  // for the constant -1.0 of the instruction, which is another number there
+  const uint32_t without[2] = {in_vgpr(PAIR && li < 8 ? 0u : 0x0000BF80u), in_vgpr(PAIR && li < 8 ? 0u : 0xBF800000u)};
+  constexpr float kHeadroom = kScaleV ? 15.0f - kSlack : 0.0f;
 
-  const Constants constants = {in_sgpr(T::kMask), in_vgpr(T::kSixteen), in_sgpr(0x000F000Fu), in_sgpr(0x00F000F0u),
-                               in_vgpr(0x64006400u)};
+  const Constants constants = {in_sgpr(T::kMask), in_vgpr(T::kSixteen), in_sgpr(BF16::kMask), in_vgpr(0xC1F84180u),
+                               in_sgpr(0x000F000Fu), in_sgpr(0x00F000F0u), in_vgpr(0x64006400u)};
   struct {
     uint32_t k[2][KJ], v[2][St::kVWords];
     uint32_t ks[2][NG][2], vs[2][NG][2];  // fp16 scales of four keys
@@ -472,22 +517,7 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
           }
         }
     }
-    // the largest V scale of this lane's keys (fp16 bits of positive numbers order like the numbers)
-    uint32_t top = 0;
-    if constexpr (!kScaleV) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            typedef uint16_t us2 __attribute__((ext_vector_type(2)));
-            top = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2, top),
-                                                                         __builtin_bit_cast(us2, st.vs[t][g][x])));
-          }
-      top = max(top & 0xFFFFu, top >> 16);
-    }
-    bool grows = top > cap;
+    bool grows = false;
     float m_new[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
@@ -498,49 +528,37 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
       grows |= (m_new[r] - mx[r]) * a.scale_log2 > kSlack;
     }
     if (__any(grows)) {
-      if (!kScaleV && __any(top > cap)) {
-        uint32_t all = cap;  // the keys of lanes i, i + 16, i + 32, i + 48
-#pragma unroll
-        for (int x = 0; x < 64; x += 16) all = max(all, (uint32_t)__builtin_amdgcn_readlane(top, x));
-        cap = all | 0x3FFu;
-        cap_log2 = 29.0f - kSlack - (float)(cap >> 10);  // 2^(15 - slack) / 2^(exponent + 1); subnormal: 2^-14
-      }
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         mx[r] = m_new[r];
-        const float next = fmaxf(mx[r] * a.scale_log2, kLowest) - cap_log2;
+        const float next = fmaxf(mx[r] * a.scale_log2, kLowest) - kHeadroom;
         const float f = __builtin_amdgcn_exp2f(mo[r] - next);
         mo[r] = next;
         l[r] *= f;
+#pragma unroll
+        for (float &x : extra[r]) x *= f;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[r][c][e] *= f;
       }
     }
-    hf8_t p[RT][kScaleV ? 1 : NG];
+    float p[RT][2][4];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      float e[2][4];
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          e[t][x] = __builtin_amdgcn_exp2f(fmaf(sc[r][t][x], a.scale_log2, -mo[r]));
-          l[r] += e[t][x];
+          p[r][t][x] = __builtin_amdgcn_exp2f(fmaf(sc[r][t][x], a.scale_log2, -mo[r]));
+          l[r] += p[r][t][x];
         }
-#pragma unroll
-      for (int g = 0; g < (kScaleV ? 1 : NG); ++g)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            p[r][g][4 * t + x] = kScaleV ? (_Float16)e[t][x] :  // one v_fma_mixlo/hi_f16: rounded once
-                (_Float16)fmaf(e[t][x], fp16_bits_to_float((st.vs[t][g][x / 2] >> (16 * (x % 2))) & 0xFFFFu), 0.0f);
-    }
+    // the probabilities, times V's scales of a group or not, in two terms
+    typedef typename std::conditional<kScaleV, hf8_t, bf8_t>::type term_t;
+    term_t high[RT], low[RT];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      h2_t vq[2][2][4];  // [tile][token pair][e]
+      typename std::conditional<kScaleV, h2_t, uint32_t>::type vq[2][2][4];  // [tile][token pair][e]
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -549,21 +567,78 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
           const uint32_t upper = D == 64 ? (uint32_t)(li & 1) : (uint32_t)(c & 1);
           widen_v(__builtin_amdgcn_perm(w1, w0, upper ? 0x07060302u : 0x05040100u), constants, vq[t][x]);
         }
+      constexpr int kSame = G < 64 ? G / 16 : 4;  // tiles of 16 channels of one group
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int g = (64 * c + 16 * e) / G;
+      for (int e0 = 0; e0 < 4; e0 += kSame) {
+        const int g = (64 * c + 16 * e0) / G;
+        const auto words = [&](int e) {
+          return w4_t{__builtin_bit_cast(uint32_t, vq[0][0][e]), __builtin_bit_cast(uint32_t, vq[0][1][e]),
+                      __builtin_bit_cast(uint32_t, vq[1][0][e]), __builtin_bit_cast(uint32_t, vq[1][1][e])};
+        };
         if constexpr (kScaleV) {
+          if (c == 0 && e0 == 0) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+            for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int y = 0; y < 2; ++y) vq[t][y][e] *= as_h2(st.vs[t][g][y]);
+              for (int x = 0; x < 8; x += 2) {
+                const f2_t y = {p[r][x / 4][x % 4], p[r][x / 4][x % 4 + 1]};
+                const h2_t first = __builtin_convertvector(y, h2_t);
+                high[r][x] = first.x, high[r][x + 1] = first.y;
+                if (!kTwo) continue;
+                // one v_fma_mixlo/hi_f16 each
+                low[r][x] = (_Float16)fmaf((float)first.x, -1.0f, y.x);
+                low[r][x + 1] = (_Float16)fmaf((float)first.y, -1.0f, y.y);
+              }
+          }
+#pragma unroll
+          for (int e = e0; e < e0 + kSame; ++e) {
+            h2_t rest[2][2];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const h2_t v = vq[x / 2][x % 2][e], scale = as_h2(st.vs[x / 2][g][x % 2]);
+              vq[x / 2][x % 2][e] = v * scale;
+              if (kTwo) rest[x / 2][x % 2] = __builtin_elementwise_fma(v, scale, -vq[x / 2][x % 2][e]);
+            }
+            const hf8_t first = __builtin_bit_cast(hf8_t, words(e));
+#pragma unroll
+            for (int r = 0; r < RT; ++r) o[r][c][e] = F16::mfma(first, high[r], o[r][c][e]);
+            if constexpr (kTwo) {
+              const hf8_t second = __builtin_bit_cast(hf8_t, rest);
+#pragma unroll
+              for (int r = 0; r < RT; ++r) o[r][c][e] = F16::mfma(second, high[r], o[r][c][e]);
+#pragma unroll
+              for (int r = 0; r < RT; ++r) o[r][c][e] = F16::mfma(first, low[r], o[r][c][e]);
+            }
+          }
+        } else {
+          if ((64 * c + 16 * e0) % G == 0) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+              for (int x = 0; x < 8; x += 2) {
+                const uint32_t scales = st.vs[x / 4][g][x % 4 / 2];
+                const f2_t y = {p[r][x / 4][x % 4] * fp16_bits_to_float(scales & 0xFFFFu),
+                                p[r][x / 4][x % 4 + 1] * fp16_bits_to_float(scales >> 16)};
+                bf2_t first = __builtin_convertvector(y, bf2_t);
+                const f2_t rest = {dot2(first, without[0], y.x), dot2(first, without[1], y.y)};
+                const bf2_t second = __builtin_convertvector(rest, bf2_t);
+                if (PAIR) first = second;
+                high[r][x] = first.x, high[r][x + 1] = first.y;
+                extra[r][g] = dot2(first, kPairBias, extra[r][g]);
+                if constexpr (!PAIR) {
+                  low[r][x] = second.x, low[r][x + 1] = second.y;
+                  extra[r][g] = dot2(second, kPairBias, extra[r][g]);
+                }
+              }
+          }
+#pragma unroll
+          for (int part = 0; part < (PAIR ? 1 : 2); ++part)
+#pragma unroll
+            for (int e = e0; e < e0 + kSame; ++e)
+#pragma unroll
+              for (int r = 0; r < RT; ++r)
+                o[r][c][e] = BF16::mfma(__builtin_bit_cast(bf8_t, words(e)), part ? low[r] : high[r], o[r][c][e]);
         }
-        const w4_t x = {__builtin_bit_cast(uint32_t, vq[0][0][e]), __builtin_bit_cast(uint32_t, vq[0][1][e]),
-                        __builtin_bit_cast(uint32_t, vq[1][0][e]), __builtin_bit_cast(uint32_t, vq[1][1][e])};
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-          o[r][c][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(hf8_t, x), p[r][kScaleV ? 0 : g],
-                                                              o[r][c][e], 0, 0, 0);
       }
     }
   };
@@ -596,6 +671,14 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     l[r] = sum4(l[r]);
+    if constexpr (!kScaleV) {
+#pragma unroll
+      for (float &x : extra[r]) x = sum4(x);
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[r][c][e] -= extra[r][(64 * c + 16 * e) / G];
+    }
     if (la == 0) {
       ml[(wave * 16 * RT + 16 * r + li) * 2] = mo[r];
       ml[(wave * 16 * RT + 16 * r + li) * 2 + 1] = l[r];
@@ -614,7 +697,7 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
       for (int e = 0; e < 4; ++e)
         *reinterpret_cast<f4_t *>(ob + (wave * 16 + li) * kRowStride + 64 * c + 16 * e + 4 * la) = o[r][c][e] * f;
     __syncthreads();
-    for (int at = threadIdx.x; at < 16 * (D / 4); at += blockDim.x) {
+    for (int at = threadIdx.x; at < (PAIR ? 8 : 16) * (D / 4); at += blockDim.x) {
       const int i = at / (D / 4), d = at % (D / 4) * 4, row = row0 + 16 * r + i;
       if (row >= rows) break;
       float m = kLowest, sum = 0.0f;
@@ -624,6 +707,7 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, RT>()))
         const float *e = ml + (x * 16 * RT + 16 * r + i) * 2;
         sum = fmaf(e[1], __builtin_amdgcn_exp2f(e[0] - m), sum);
         v += *reinterpret_cast<const f4_t *>(ob + (x * 16 + i) * kRowStride + d);
+        if (PAIR) v += *reinterpret_cast<const f4_t *>(ob + (x * 16 + i + 8) * kRowStride + d);
       }
       const int64_t token = w.q0 + row / a.share;
       const int64_t at_row = token * (a.kv_heads * a.share) + head * a.share + row % a.share;
@@ -731,17 +815,17 @@ __global__ __launch_bounds__(256) void attention_join_few_kernel(AttentionKernel
   if (d == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
 }
 
-template <typename T, int D, int G, int RT>
+template <typename T, int D, int G, int RT, bool PAIR>
 hipError_t go(const AttentionKernelArgs &a, const AttentionPlan &p, hipStream_t stream) {
   const size_t join = sizeof(float) * p.waves * (16 * RT * 2 + 16 * (D + 4));
   const size_t stages = (size_t)p.waves * kStages * Stage<D, G>::kBytes;
   const size_t lds = join > stages ? join : stages;
   if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(attention_kernel<T, D, G, RT>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(attention_kernel<T, D, G, RT, PAIR>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((attention_kernel<T, D, G, RT>), dim3((unsigned)a.row_blocks * a.kv_heads, a.num_seqs, p.splits),
+  hipLaunchKernelGGL((attention_kernel<T, D, G, RT, PAIR>), dim3((unsigned)a.row_blocks * a.kv_heads, a.num_seqs, p.splits),
                      dim3(64 * p.waves), lds, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
@@ -758,8 +842,10 @@ hipError_t go(const AttentionKernelArgs &a, const AttentionPlan &p, hipStream_t 
 template <typename T, int D, int G>
 hipError_t by_rows(const AttentionKernelArgs &a, const AttentionPlan &p, hipStream_t stream) {
   if constexpr (D / G >= 4)
-    if (p.row_tiles == 2) return go<T, D, G, 2>(a, p, stream);
-  return go<T, D, G, 1>(a, p, stream);
+    if (p.row_tiles == 2) return go<T, D, G, 2, false>(a, p, stream);
+  if constexpr (!scale_on_v<D, G, 1>())
+    if (a.max_q * a.share <= 8) return go<T, D, G, 1, true>(a, p, stream);
+  return go<T, D, G, 1, false>(a, p, stream);
 }
 
 template <typename T>
