@@ -21,6 +21,8 @@ from dataclasses import dataclass, field
 from typing import Dict, Optional
 
 import ctypes
+import importlib
+import importlib.util
 
 from . import _binding as B
 from ._binding import (  # noqa: F401  (the C names)
@@ -34,13 +36,24 @@ __all__ = ["PackedWeight", "pack", "run", "run_multi", "pack_sizes", "run_worksp
 
 _SERVING = ("KVCache", "KVStep", "TokenLogprobs", "kv_cache", "kv_extend", "kv_append", "kv_read", "kv_attention",
             "token_logprobs")
-__all__ += _SERVING
+
+
+def _torch_installed() -> bool:
+    try:
+        return importlib.util.find_spec("torch") is not None
+    except (ImportError, ValueError):
+        return False
+
+
+# the serving operators need torch when they are defined, packing only when it
+# is called: a star import, which resolves every name here, leaves them out
+# where there is no torch
+if _torch_installed():
+    __all__ += _SERVING
 
 
 def __getattr__(name):
-    # the serving operators need torch when they are defined, packing only when it is called
     if name in _SERVING or name == "serving":
-        import importlib
         serving = importlib.import_module(".serving", __name__)
         globals().update({n: getattr(serving, n) for n in _SERVING})
         return serving if name == "serving" else globals()[name]
