@@ -1,0 +1,51 @@
+"""The serving operators on the GPU: calls at the edges of what the header
+allows."""
+
+import numpy as np
+import pytest
+
+from oracle import serve_oracle as O
+from test_serving_gpu import BF16, F16, F32, f64, filled, say
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def i4s():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import int4_sparse_gemv_amd as I
+    return I
+
+
+def int32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32).cuda()
+
+
+# ---------------------------------------------------------------------------
+# reading tokens
+
+
+@pytest.mark.parametrize("dim,group", [(64, 32), (128, 64), (256, 128)])
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_read_into_outputs_of_16_byte_alignment(i4s, dim, group, dtype):
+    """Outputs that begin between two multiples of 32 bytes, and what lies around them stays."""
+    say("read alignment", dim, group, dtype)
+    from int4_sparse_gemv_amd import _serve_binding as S
+    rng = np.random.default_rng(dim)
+    c, d = filled(i4s, rng, 3, 16, 3, dim, group)
+    slots = int32([47, 0, 17, -1, 48, 5, 31])
+    n = 7 * 3 * dim
+    size = torch.empty(0, dtype=dtype).element_size()
+    bufs = [torch.full((n * size + 64,), 0x55, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    assert all(b.data_ptr() % 32 == 0 for b in bufs)
+    number = {F16: S.I4S_F16, BF16: S.I4S_BF16, F32: S.I4S_F32}[dtype]
+    stream = torch.cuda.current_stream().cuda_stream
+    assert S.i4s_kv_read(d.descriptor, slots.data_ptr(), 7, number, bufs[0].data_ptr() + 16, bufs[1].data_ptr() + 16, stream) == 0
+    torch.cuda.synchronize()
+    for b, want in zip(bufs, c.read(slots.cpu().numpy())):
+        got = b[16:16 + n * size].view(dtype).view(7, 3, dim)
+        assert torch.equal(got.cpu(), torch.from_numpy(want).to(dtype))
+        assert (b[:16] == 0x55).all() and (b[16 + n * size:] == 0x55).all()
