@@ -189,7 +189,11 @@ def kv_attention(cache: KVCache, q, table, lens, q_start=None, max_q: Optional[i
     ``table`` int32 [sequences, width] and ``lens`` int32 [sequences] say what
     each sequence holds, its query tokens included (append them first).
     ``q_start`` int32 [sequences + 1] bounds the query tokens of each, at most
-    ``max_q`` (default: all of them); without it every sequence has one.
+    ``max_q``; without it every sequence has one.  ``max_q`` sizes the launch;
+    its default, all of the tokens (with ``tree_mask`` the 64 that a mask can
+    name), is right but slow where sequences have few of many.  Rows of ``out``
+    that no sequence has, and tokens past a sequence's ``max_q``, are left as
+    they were: whatever the memory held where ``out`` is not given.
     ``max_len`` is the largest length, if known.  ``scale`` defaults to
     head_dim ** -0.5.  Token t sees the keys up to its own; with ``tree_mask``
     (int64 [tokens]) it sees the keys before the sequence's query tokens and
@@ -213,6 +217,8 @@ def kv_attention(cache: KVCache, q, table, lens, q_start=None, max_q: Optional[i
         _check(q_start, torch.int32, (n + 1,), index, "q_start")
         if max_q is None:
             max_q = max(tokens, 1)
+            if tree_mask is not None and tokens <= S.I4S_MAX_TREE * n:
+                max_q = min(max_q, S.I4S_MAX_TREE)
     elif max_q is None:
         max_q = 1
     if tree_mask is not None:

@@ -49,3 +49,21 @@ def test_read_into_outputs_of_16_byte_alignment(i4s, dim, group, dtype):
         got = b[16:16 + n * size].view(dtype).view(7, 3, dim)
         assert torch.equal(got.cpu(), torch.from_numpy(want).to(dtype))
         assert (b[:16] == 0x55).all() and (b[16 + n * size:] == 0x55).all()
+
+
+# ---------------------------------------------------------------------------
+# attention
+
+
+def test_tree_masks_of_many_sequences_need_no_max_q(i4s):
+    """More than 64 tokens in all, few of each sequence; more than 64 of one sequence are refused."""
+    say("tree default")
+    rng = np.random.default_rng(1)
+    c, d = filled(i4s, rng, 12, 16, 1, 64, 32)
+    q = torch.from_numpy(rng.standard_normal((100, 2, 64))).to(F16).cuda()
+    table, lens, starts = int32(rng.integers(0, 12, (5, 4))), int32([60, 20, 33, 45, 21]), int32([0, 20, 40, 60, 80, 100])
+    mask = torch.from_numpy(np.concatenate([(1 << np.arange(20)) | 1] * 5)).cuda()
+    got = i4s.kv_attention(d, q, table, lens, q_start=starts, tree_mask=mask)
+    assert torch.equal(got, i4s.kv_attention(d, q, table, lens, q_start=starts, max_q=20, tree_mask=mask))
+    with pytest.raises(i4s.I4SError):
+        i4s.kv_attention(d, q[:65], table[:1], lens[:1], q_start=int32([0, 65]), tree_mask=mask[:65])
