@@ -47,6 +47,12 @@ def _check(t, dtype, shape, index, name) -> None:
                          f"not {t.dtype} {list(t.shape)} on {t.device}")
 
 
+def _fit(*numbers) -> None:
+    """ctypes would pass the lower half of a number that 32 bits do not hold."""
+    if max(numbers) > 2147483647 or min(numbers) < -2147483648:
+        raise ValueError(f"{[n for n in numbers if not -2**31 <= n < 2**31]}: 32 bits do not hold this number")
+
+
 def _strides(t, name):
     """(token, head) strides of [tokens, heads, channels]; an axis of one counts as 0."""
     token, head, channel = t.stride()
@@ -66,6 +72,7 @@ class KVCache:
 
     def __init__(self, page_size: int, kv_heads: int, head_dim: int, group_size: int, k_vals, v_vals, k_scales, v_scales):
         pages = k_vals.shape[0]
+        _fit(pages, page_size, kv_heads, head_dim, group_size)
         sz = S.i4s_kv_sizes()
         B.check(S.i4s_kv_cache_sizes(pages, page_size, kv_heads, head_dim, group_size, sz), "i4s_kv_cache_sizes")
         values = page_size * head_dim
@@ -92,6 +99,7 @@ class KVCache:
 
 def kv_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int, group_size: int = 64, device="cuda") -> KVCache:
     """Allocate a cache (its values start as zeros)."""
+    _fit(num_pages, page_size, kv_heads, head_dim, group_size)
     sz = S.i4s_kv_sizes()
     B.check(S.i4s_kv_cache_sizes(num_pages, page_size, kv_heads, head_dim, group_size, sz), "i4s_kv_cache_sizes")
     values = page_size * head_dim
@@ -132,6 +140,7 @@ def kv_extend(table, lens, new_lens, free_pages, free_count, page_size: int, cap
     entries = free_pages.numel()
     _check(free_pages, torch.int32, (entries,), index, "free_pages")
     _check(free_count, torch.int32, (1,), index, "free_count")
+    _fit(n, width, page_size, entries, capacity)
     # one allocation: lens, q_start, count, flags, slots, positions
     buf = table.new_empty(2 * n + 3 + 2 * capacity)
     at = buf.data_ptr()
@@ -155,6 +164,7 @@ def kv_append(cache: KVCache, k, v, slots) -> None:
     if k.get_device() != index or v.get_device() != index:
         raise ValueError(f"k and v must be on {cache.device}")
     tokens = shape[0]
+    _fit(0, tokens)
     _check(slots, torch.int32, (tokens,), index, "slots")
     ks, vs = _strides(k, "k"), _strides(v, "v")
     st = _call(S.load().i4s_kv_append, index, cache.descriptor, k.data_ptr(), v.data_ptr(), dtype, ks[0], ks[1], vs[0],
@@ -172,6 +182,7 @@ def kv_read(cache: KVCache, slots, dtype=torch.float16):
     if len(shape) != 1:
         raise ValueError("slots must be int32 [tokens]")
     tokens = shape[0]
+    _fit(0, tokens)
     _check(slots, torch.int32, shape, index, "slots")
     k = slots.new_empty((tokens, cache.kv_heads, cache.head_dim), dtype=dtype)
     v = torch.empty_like(k)
@@ -221,6 +232,7 @@ def kv_attention(cache: KVCache, q, table, lens, q_start=None, max_q: Optional[i
                 max_q = min(max_q, S.I4S_MAX_TREE)
     elif max_q is None:
         max_q = 1
+    _fit(tokens, heads, n, width, max_q, max_len)
     if tree_mask is not None:
         _check(tree_mask, torch.int64, (tokens,), index, "tree_mask")
     if out is None:
@@ -258,6 +270,7 @@ class TokenLogprobs(NamedTuple):
 
 @functools.lru_cache(maxsize=4096)
 def _logprobs_workspace(dtype: int, rows: int, vocab: int, top_k: int) -> int:
+    _fit(rows, vocab, top_k)
     n = ctypes.c_uint64()
     B.check(S.i4s_token_logprobs_workspace_size(dtype, rows, vocab, top_k, n), "i4s_token_logprobs_workspace_size")
     return n.value

@@ -67,3 +67,26 @@ def test_tree_masks_of_many_sequences_need_no_max_q(i4s):
     assert torch.equal(got, i4s.kv_attention(d, q, table, lens, q_start=starts, max_q=20, tree_mask=mask))
     with pytest.raises(i4s.I4SError):
         i4s.kv_attention(d, q[:65], table[:1], lens[:1], q_start=int32([0, 65]), tree_mask=mask[:65])
+
+
+# ---------------------------------------------------------------------------
+# numbers that 32 bits do not hold
+
+
+def test_numbers_beyond_32_bits_are_refused(i4s):
+    """The C ABI takes 32-bit numbers; none is cut down to its lower half."""
+    say("32 bits")
+    big = 1 << 32
+    d = i4s.kv_cache(4, 16, 2, 64, 32)
+    t, l, one = int32([[0, 1]]), int32([20]), int32([1])
+    q = torch.zeros(2, 2, 64, dtype=F16).cuda()
+    for call in (lambda: i4s.kv_extend(t, l, one, one, one, big + 16, 1), lambda: i4s.kv_extend(t, l, one, one, one, 16, big + 1),
+                 lambda: i4s.kv_extend(t, l, one, one, one, 16, -big + 1),
+                 lambda: i4s.kv_attention(d, q, t, l, q_start=int32([0, 2]), max_q=big + 1),
+                 lambda: i4s.kv_attention(d, q, t, l, q_start=int32([0, 2]), max_len=big),
+                 lambda: i4s.kv_attention(d, q, t, l, q_start=int32([0, 2]), max_len=-big),
+                 lambda: i4s.token_logprobs(torch.zeros(1, 9).cuda(), torch.zeros(1, dtype=torch.int64).cuda(), top_k=big + 1),
+                 lambda: i4s.kv_cache(4, big + 16, 2, 64, 32), lambda: i4s.kv_cache(big + 4, 16, 2, 64, 32),
+                 lambda: i4s.KVCache(16, 2 + big, 64, 32, d.k_vals, d.v_vals, d.k_scales, d.v_scales)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
