@@ -1,5 +1,6 @@
 """ctypes binding of the serving operators of libi4s (include/i4s_serve.h),
-same names as the C ABI.  Argument marshalling only, like ``_binding``.
+same names as the C ABI.  Argument marshalling only, like ``_binding``; a
+structure is passed as it is where a function takes its address.
 """
 
 from __future__ import annotations
@@ -101,42 +102,9 @@ def load() -> ctypes.CDLL:
     return _lib
 
 
-# thin wrappers with the C names --------------------------------------------
-
-def i4s_kv_cache_sizes(num_pages, page_size, kv_heads, head_dim, group_size, out):
-    return load().i4s_kv_cache_sizes(num_pages, page_size, kv_heads, head_dim, group_size, ctypes.byref(out))
-
-
-def i4s_kv_extend(table_ptr, n, width, page_size, lens_ptr, new_lens_ptr, free_pages_ptr, free_entries, free_count_ptr,
-                  capacity, lens_out_ptr, q_start_ptr, slots_ptr, positions_ptr, free_count_out_ptr, flags_ptr, stream):
-    return load().i4s_kv_extend(table_ptr, n, width, page_size, lens_ptr, new_lens_ptr, free_pages_ptr, free_entries,
-                                free_count_ptr, capacity, lens_out_ptr, q_start_ptr, slots_ptr, positions_ptr,
-                                free_count_out_ptr, flags_ptr, stream)
-
-
-def i4s_kv_append(cache, k_ptr, v_ptr, dtype, k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots_ptr,
-                  tokens, stream):
-    return load().i4s_kv_append(ctypes.byref(cache), k_ptr, v_ptr, dtype, k_token_stride, k_head_stride, v_token_stride,
-                                v_head_stride, slots_ptr, tokens, stream)
-
-
-def i4s_kv_read(cache, slots_ptr, tokens, dtype, k_ptr, v_ptr, stream):
-    return load().i4s_kv_read(ctypes.byref(cache), slots_ptr, tokens, dtype, k_ptr, v_ptr, stream)
-
-
-def i4s_attention_workspace_size(args, out):
-    return load().i4s_attention_workspace_size(ctypes.byref(args), ctypes.byref(out))
-
-
-def i4s_attention(args, stream):
-    return load().i4s_attention(ctypes.byref(args), stream)
-
-
-def i4s_token_logprobs_workspace_size(dtype, rows, vocab, top_k, out):
-    return load().i4s_token_logprobs_workspace_size(dtype, rows, vocab, top_k, ctypes.byref(out))
-
-
-def i4s_token_logprobs(logits_ptr, dtype, rows, vocab, stride, tokens_ptr, top_k, logprobs_ptr, entropy_ptr, top_ids_ptr,
-                       top_logprobs_ptr, ws_ptr, ws_bytes, stream):
-    return load().i4s_token_logprobs(logits_ptr, dtype, rows, vocab, stride, tokens_ptr, top_k, logprobs_ptr, entropy_ptr,
-                                     top_ids_ptr, top_logprobs_ptr, ws_ptr, ws_bytes, stream)
+def __getattr__(name):
+    # the library's functions under their C names, found when they are first used
+    if name in SIGNATURES:
+        globals()[name] = fn = getattr(load(), name)
+        return fn
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -145,7 +145,7 @@ def kv_extend(table, lens, new_lens, free_pages, free_count, page_size: int, cap
     buf = table.new_empty(2 * n + 3 + 2 * capacity)
     at = buf.data_ptr()
     start, count, slots = at + 4 * n, at + 8 * n + 4, at + 8 * n + 12
-    st = _call(S.load().i4s_kv_extend, index, table.data_ptr(), n, width, page_size, lens.data_ptr(), new_lens.data_ptr(),
+    st = _call(S.i4s_kv_extend, index, table.data_ptr(), n, width, page_size, lens.data_ptr(), new_lens.data_ptr(),
                free_pages.data_ptr(), entries, free_count.data_ptr(), capacity, at, start, slots, slots + 4 * capacity, count,
                count + 4)
     if st:
@@ -167,7 +167,7 @@ def kv_append(cache: KVCache, k, v, slots) -> None:
     _fit(0, tokens)
     _check(slots, torch.int32, (tokens,), index, "slots")
     ks, vs = _strides(k, "k"), _strides(v, "v")
-    st = _call(S.load().i4s_kv_append, index, cache.descriptor, k.data_ptr(), v.data_ptr(), dtype, ks[0], ks[1], vs[0],
+    st = _call(S.i4s_kv_append, index, cache.descriptor, k.data_ptr(), v.data_ptr(), dtype, ks[0], ks[1], vs[0],
                vs[1], slots.data_ptr(), tokens)
     if st:
         B.check(st, "i4s_kv_append")
@@ -186,7 +186,7 @@ def kv_read(cache: KVCache, slots, dtype=torch.float16):
     _check(slots, torch.int32, shape, index, "slots")
     k = slots.new_empty((tokens, cache.kv_heads, cache.head_dim), dtype=dtype)
     v = torch.empty_like(k)
-    st = _call(S.load().i4s_kv_read, index, cache.descriptor, slots.data_ptr(), tokens, number, k.data_ptr(), v.data_ptr())
+    st = _call(S.i4s_kv_read, index, cache.descriptor, slots.data_ptr(), tokens, number, k.data_ptr(), v.data_ptr())
     if st:
         B.check(st, "i4s_kv_read")
     return k, v
@@ -246,16 +246,15 @@ def kv_attention(cache: KVCache, q, table, lens, q_start=None, max_q: Optional[i
         width, lens.data_ptr(), None if q_start is None else q_start.data_ptr(), max_q, max_len,
         dim ** -0.5 if scale is None else scale, None if tree_mask is None else tree_mask.data_ptr(), out.data_ptr(),
         None if lse is None else lse.data_ptr(), None, 0)
-    lib = S.load()
     nbytes = ctypes.c_uint64()
-    st = lib.i4s_attention_workspace_size(a, nbytes)
+    st = S.i4s_attention_workspace_size(a, nbytes)
     if st:
         B.check(st, "i4s_attention_workspace_size")
     if nbytes.value:
         # of this call alone: calls on other streams and captured graphs have their own
         ws = q.new_empty(nbytes.value, dtype=torch.uint8)
         a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes.value
-    st = _call(lib.i4s_attention, index, a)
+    st = _call(S.i4s_attention, index, a)
     if st:
         B.check(st, "i4s_attention")
     return out
@@ -296,7 +295,7 @@ def token_logprobs(logits, tokens, top_k: int = 0) -> TokenLogprobs:
     entropy = torch.empty_like(logprobs)
     top_ids = tokens.new_empty((rows, top_k), dtype=torch.int32)
     top = logprobs.new_empty((rows, top_k))
-    st = _call(S.load().i4s_token_logprobs, index, logits.data_ptr(), dtype, rows, vocab, stride, tokens.data_ptr(), top_k,
+    st = _call(S.i4s_token_logprobs, index, logits.data_ptr(), dtype, rows, vocab, stride, tokens.data_ptr(), top_k,
                logprobs.data_ptr(), entropy.data_ptr(), top_ids.data_ptr(), top.data_ptr(),
                None if ws is None else ws.data_ptr(), nbytes)
     if st:
