@@ -111,7 +111,8 @@ i4s_status i4s_kv_cache_sizes(int32_t num_pages, int32_t page_size, int32_t kv_h
  *               bit is set the call changes nothing: lens_out = lens,
  *               free_count_out = free_count, table unchanged, q_start all 0,
  *               slots all -1, positions all 0.
- * n is 0 .. I4S_KV_MAX_REQUESTS.  Every pointer 4-byte aligned; none may be
+ * n is 0 .. I4S_KV_MAX_REQUESTS, width 1 or more, page_size 16, 32, 64, 128 or
+ * 256, capacity and free_entries 0 or more.  Every pointer 4-byte aligned; none may be
  * NULL but table, lens, new_lens and lens_out when n is 0, slots and positions
  * when capacity is 0, and free_pages when free_entries is 0.  No output may
  * overlap an input or another output: the new lengths and the new count go
@@ -127,13 +128,13 @@ i4s_status i4s_kv_extend(int32_t *table, int32_t n, int32_t width, int32_t page_
 /* Quantizes the K and V of `tokens` tokens into their slots.
  *   k, v   : [tokens][kv_heads][D] of dtype I4S_F16 or I4S_BF16; the channels
  *            of a head lie next to each other, tokens and heads at the given
- *            strides (in elements, 0 or more, multiples of 8); 16-byte aligned.
+ *            strides (in elements, 0 .. 2^40, multiples of 8); 16-byte aligned.
  *   slots  : int32 [tokens], 4-byte aligned.  A token whose slot is outside
  *            [0, num_pages * page_size) is not stored (-1 marks padding).  A
  *            slot may be named once: what is stored for a slot named twice is
  *            a mix of the two.
- * k, v and slots must not overlap the cache; kv_heads * D * tokens is below
- * 2^34.  One kernel launch.
+ * k, v and slots must not overlap the cache; kv_heads * (D * tokens + 2048) is
+ * below 2^34.  One kernel launch.
  * Errors: I4S_ERR_INVALID_ARGUMENT, I4S_ERR_UNSUPPORTED, I4S_ERR_DEVICE. */
 i4s_status i4s_kv_append(const i4s_kv_cache *cache /* host */, const void *k, const void *v, int32_t dtype,
                          int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
@@ -142,7 +143,8 @@ i4s_status i4s_kv_append(const i4s_kv_cache *cache /* host */, const void *k, co
 /* Reads tokens back: k_out, v_out = s * q, rounded once to dtype (I4S_F16,
  * I4S_BF16 or I4S_F32), [tokens][kv_heads][D] contiguous, 16-byte aligned.  A
  * token whose slot is outside the cache gives zeros.  The outputs must not
- * overlap the cache, slots or one another.  One kernel launch.
+ * overlap the cache, slots or one another; kv_heads * (D * tokens + 2048) is
+ * below 2^34.  One kernel launch.
  * Errors: I4S_ERR_INVALID_ARGUMENT, I4S_ERR_UNSUPPORTED, I4S_ERR_DEVICE. */
 i4s_status i4s_kv_read(const i4s_kv_cache *cache /* host */, const int32_t *slots, int32_t tokens,
                        int32_t dtype, void *k_out, void *v_out, void *stream);
@@ -161,19 +163,19 @@ typedef struct i4s_attention_args {
   const i4s_kv_cache *cache; /* host                                          */
   const void *q;             /* [num_tokens][q_heads][D], channels adjacent,  */
                              /* 16-byte aligned                               */
-  int64_t q_token_stride;    /* in elements, 0 or more, multiples of 8        */
+  int64_t q_token_stride;    /* in elements, 0 .. 2^40, multiples of 8        */
   int64_t q_head_stride;
   int32_t dtype;             /* of q and out: I4S_F16 or I4S_BF16             */
-  int32_t q_heads;           /* a multiple of kv_heads                        */
+  int32_t q_heads;           /* a multiple of kv_heads, at most 65536         */
   int32_t num_tokens;        /* rows of q and out, 0 or more                  */
-  int32_t num_seqs;          /* 0 or more                                     */
+  int32_t num_seqs;          /* 0 .. 65535                                    */
   const int32_t *table;      /* [num_seqs][table_width] page numbers          */
-  int32_t table_width;
+  int32_t table_width;       /* 1 or more, times page_size at most 2^30       */
   const int32_t *lens;       /* [num_seqs]                                    */
   const int32_t *q_start;    /* [num_seqs+1], non-decreasing, or NULL: one    */
                              /* token each, num_tokens == num_seqs            */
   int32_t max_q;             /* largest number of query tokens of a sequence, */
-                             /* max_q * q_heads below 2^23                    */
+                             /* 1 .. 2^20, times q_heads below 2^23           */
   int32_t max_len;           /* largest length (0: table_width * page_size);  */
                              /* sizes the launch                              */
   float scale;               /* > 0, finite                                   */
@@ -214,7 +216,7 @@ i4s_status i4s_attention(const i4s_attention_args *a /* host */, void *stream);
  *                 falling order, among equal ones the lower index first (-0
  *                 equals 0, a NaN counts as +inf), int32 and fp32.
  *   logits  : dtype I4S_F16, I4S_BF16 or I4S_F32, aligned to its element;
- *             stride >= vocab; vocab 1 .. I4S_MAX_VOCAB.
+ *             stride vocab .. 2^40; vocab 1 .. I4S_MAX_VOCAB.
  *   tokens  : int64 [rows], 8-byte aligned; one outside [0, vocab) gives NaN.
  *   top_k   : 0 .. min(I4S_MAX_TOP_K, vocab); top_ids and top_logprobs may be
  *             NULL when it is 0.

@@ -89,6 +89,15 @@ i4s_status check_strides(int64_t token, int64_t head, const char *name) {
                 (long long)token, (long long)head);
   return I4S_OK;
 }
+
+// A block takes 2048 / D tokens of a head: fewer than kMaxBlocks + 1 blocks.
+i4s_status check_tokens(const i4s_kv_cache &c, int32_t tokens) {
+  if (tokens < 0 || c.kv_heads * ((int64_t)tokens * c.head_dim + 2048) >= (kMaxBlocks + 1) * 2048)
+    return fail(I4S_ERR_INVALID_ARGUMENT,
+                "tokens=%d must be 0 or more, and kv_heads * (head_dim * tokens + 2048) below 2^34", tokens);
+  return I4S_OK;
+}
+
 uint64_t extent(int64_t tokens, int64_t token, int64_t heads, int64_t head, int64_t dim) {
   return tokens < 1 ? 0 : 2ull * ((tokens - 1) * token + (heads - 1) * head + dim);
 }
@@ -257,8 +266,8 @@ i4s_status i4s_kv_append(const i4s_kv_cache *cache, const void *k, const void *v
   if (st != I4S_OK) return st;
   if (dtype != I4S_F16 && dtype != I4S_BF16)
     return fail(I4S_ERR_INVALID_ARGUMENT, "dtype=%d must be I4S_F16 or I4S_BF16", dtype);
-  if (tokens < 0 || ((int64_t)tokens * cache->head_dim / 2048 + 1) * cache->kv_heads > kMaxBlocks)
-    return fail(I4S_ERR_INVALID_ARGUMENT, "tokens=%d must be 0 or more, and kv_heads * head_dim * tokens below 2^34", tokens);
+  st = check_tokens(*cache, tokens);
+  if (st != I4S_OK) return st;
   st = check_strides(k_token_stride, k_head_stride, "k");
   if (st != I4S_OK) return st;
   st = check_strides(v_token_stride, v_head_stride, "v");
@@ -291,8 +300,8 @@ i4s_status i4s_kv_read(const i4s_kv_cache *cache, const int32_t *slots, int32_t 
   if (st != I4S_OK) return st;
   if (dtype != I4S_F16 && dtype != I4S_BF16 && dtype != I4S_F32)
     return fail(I4S_ERR_INVALID_ARGUMENT, "dtype=%d must be I4S_F16, I4S_BF16 or I4S_F32", dtype);
-  if (tokens < 0 || ((int64_t)tokens * cache->head_dim / 2048 + 1) * cache->kv_heads > kMaxBlocks)
-    return fail(I4S_ERR_INVALID_ARGUMENT, "tokens=%d must be 0 or more, and kv_heads * head_dim * tokens below 2^34", tokens);
+  st = check_tokens(*cache, tokens);
+  if (st != I4S_OK) return st;
   if (tokens == 0) return I4S_OK;
   if (!k_out || !aligned(k_out, 16) || !v_out || !aligned(v_out, 16))
     return fail(I4S_ERR_INVALID_ARGUMENT, "k_out or v_out is NULL or not 16-byte aligned");
