@@ -311,3 +311,62 @@ def test_outputs_are_as_near_as_their_rounding(i4s):
         # before that the 2^-16 of every key, of either sign, adds up as the keys' values themselves do, whose signs are
         # random too: 2^-16 of the output, 2^-5 of its rounding
         assert norm(out - want) <= 1.04 * norm(rounded - want)
+
+
+# ---------------------------------------------------------------------------
+# keys in pieces
+
+
+def held(i4s, rng, lens, page, heads, dim, group):
+    return filled(i4s, rng, sum(-(-l // page) for l in lens) + 1, page, heads, dim, group)
+
+
+@pytest.mark.parametrize("dim,group,heads,share,lens,q_lens,most", [
+    (128, 64, 1, 4, [2300], [1], False), (128, 64, 1, 4, [1500, 40, 1100], [1, 1, 1], True), (128, 32, 2, 1, [3000], [2], False),
+    (64, 32, 2, 8, [4100], [1], False), (64, 64, 1, 3, [1300, 9], [5, 2], True), (256, 128, 1, 4, [2000], [2], False),
+    (256, 64, 1, 1, [900], [3], True), (256, 32, 1, 2, [2100], [1], False)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_pieces_of_few_rows(i4s, dtype, dim, group, heads, share, lens, q_lens, most):
+    """Up to 16 rows: joined by rows (up to 8 pieces) and by blocks (more), every type and channel count."""
+    say("pieces", dim, group, heads, share, lens, q_lens, dtype)
+    rng = np.random.default_rng(dim + sum(lens))
+    c, d = held(i4s, rng, lens, 32, heads, dim, group)
+    attend(i4s, rng, c, d, lens, q_lens, share, dtype, pieces=lambda n: 2 <= n <= 8 if most else n > 8)
+
+
+@pytest.mark.parametrize("dim,group,lens,q_lens,most", [
+    (128, 32, [900, 130], [5, 3], True), (128, 32, [1900], [5], False), (256, 64, [800], [4], True), (256, 64, [1500], [4], False),
+    (256, 32, [700, 3], [3, 3], True), (256, 32, [1400], [6], False), (128, 64, [1800], [7], True), (64, 32, [3000], [9], False)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_pieces_of_many_rows(i4s, dtype, dim, group, lens, q_lens, most):
+    """Several row tiles and blocks of rows, with V's scales on the values and on the probabilities."""
+    say("pieces of many rows", dim, group, lens, q_lens, dtype)
+    rng = np.random.default_rng(dim + sum(lens) + 1)
+    c, d = held(i4s, rng, lens, 16, 1, dim, group)
+    attend(i4s, rng, c, d, lens, q_lens, 8, dtype, pieces=lambda n: 2 <= n <= 8 if most else n > 8)
+
+
+@pytest.mark.parametrize("dim,group,share,lens,q_lens", [
+    (128, 128, 1, [2047], [16]), (128, 64, 2, [2100, 70], [64, 64]), (64, 32, 1, [3001], [64]), (128, 32, 8, [1200], [7]),
+    (256, 64, 1, [2070, 1], [40, 1]), (128, 64, 1, [2049, 2080], [3, 64])])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_tree_masks_over_pieces(i4s, dtype, dim, group, share, lens, q_lens):
+    """The candidates lie in the last piece of the keys, or across the last two; some rows see none of a piece."""
+    say("tree over pieces", dim, group, share, lens, q_lens, dtype)
+    rng = np.random.default_rng(dim + sum(lens) + 2)
+    c, d = held(i4s, rng, lens, 32, 1, dim, group)
+    attend(i4s, rng, c, d, lens, q_lens, share, dtype, masks=random_masks(rng, q_lens), pieces=lambda n: n > 1)
+
+
+@pytest.mark.parametrize("dim,group,share,max_len", [(128, 64, 1, 1500), (128, 64, 4, 1100), (128, 32, 24, 700), (64, 32, 2, 2400),
+                                                     (256, 128, 1, 600)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_lengths_beyond_max_len(i4s, dtype, dim, group, share, max_len):
+    """Keys in pieces by a largest length that is too small: the last piece takes what is left, in any sequence."""
+    for tree in (False, True):
+        say("beyond max_len", dim, group, share, max_len, dtype, tree)
+        lens, q_lens = [2500, max_len, 5, max_len + 1, 3300], [2, 1, 2, 2, 1]
+        rng = np.random.default_rng(dim + max_len)
+        c, d = held(i4s, rng, lens, 32, 1, dim, group)
+        attend(i4s, rng, c, d, lens, q_lens, share, dtype, max_len=max_len, pieces=lambda n: n > 1,
+               masks=random_masks(rng, q_lens) if tree else None)
