@@ -91,7 +91,12 @@ def parse():
     ap.add_argument("--summarize-rocprof", nargs=2, metavar=("DIR", "OUT"), default=None,
                     help="summarize rocprofv3 CSV output under DIR into the text file OUT (no GPU needed)")
     ap.add_argument("--min-calls", type=int, default=20, help="with --summarize-rocprof")
-    return ap.parse_args()
+    args = ap.parse_args()
+    if args.verify_step is not None and not 1 <= args.verify_step <= 16:
+        ap.error("--verify-step takes 1 to 16 candidate tokens, the batches of the packed products")
+    if args.context < 0:
+        ap.error("--context takes 0 or more tokens")
+    return args
 
 
 def sha_of(paths):
@@ -497,41 +502,56 @@ class VerifyStep:
         return a, y, self.score(y)
 
 
-def verify_step(R, args):
-    """The step in a graph, whole and in its parts, us each."""
-    torch = R.torch
-    s = VerifyStep(R.I, args.verify_step, args.context)
-    q, k, v = s.project()
-    r = s.extend()
-    a = s.attend(q, r)
-    y = s.mlp(a)
+VERIFY_COPIES = 64  # of a layer: 8 GB, and over 0.5 GB of every part but extend and append, past every cache
 
-    def timed(f):
+
+def verify_step(R, args):
+    """The step in a graph, whole and in its parts, us each: hot, the same layer
+    again and again, which the last-level cache holds, and cold, as in a model of
+    many layers, where each step finds another layer's weights and cache."""
+    torch = R.torch
+    steps = [VerifyStep(R.I, args.verify_step, args.context, seed) for seed in range(VERIFY_COPIES)]
+    say(f"verify step: {len(steps)} layers made")
+    held = []
+    for s in steps:
+        q, k, v = s.project()
+        r = s.extend()
+        a = s.attend(q, r)
+        held.append((q, k, v, r, a, s.mlp(a)))
+
+    def timed(f, order):
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
-            f()
+            f(0)
         torch.cuda.current_stream().wait_stream(side)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
-            for _ in range(10):
-                f()
+            for i in order:
+                f(i)
         best = None
         for _ in range(args.trials):
             b, e = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
             graph.replay()
             b.record()
-            for _ in range(10):
+            for _ in range(5):
                 graph.replay()
             e.record()
             e.synchronize()
-            us = b.elapsed_time(e) * 10
+            us = b.elapsed_time(e) * 1e3 / 5 / len(order)
             best = us if best is None else min(best, us)
         return round(best, 2)
-    parts = {"step": s.run, "qkv": s.project, "kv_extend": s.extend, "kv_append": lambda: s.append(k, v, r),
-             "kv_attention": lambda: s.attend(q, r), "o_gate_up_down": lambda: s.mlp(a), "head_and_scores": lambda: s.score(y)}
-    return {"workload": "verify_step_7b_layer", "tokens": args.verify_step, "context": args.context, "data": "synthetic",
-            "us": {n: timed(f) for n, f in parts.items()}}
+    parts = {"step": lambda i: steps[i].run(), "qkv": lambda i: steps[i].project(), "kv_extend": lambda i: steps[i].extend(),
+             "kv_append": lambda i: steps[i].append(held[i][1], held[i][2], held[i][3]),
+             "kv_attention": lambda i: steps[i].attend(held[i][0], held[i][3]),
+             "o_gate_up_down": lambda i: steps[i].mlp(held[i][4]), "head_and_scores": lambda i: steps[i].score(held[i][5])}
+    out = {"workload": "verify_step_7b_layer", "tokens": args.verify_step, "context": args.context, "data": "synthetic",
+           "layers": len(steps), "cold_us": {}, "hot_us": {}}
+    for n, f in parts.items():
+        out["cold_us"][n] = timed(f, range(len(steps)))
+        out["hot_us"][n] = timed(f, [0] * 10)
+        say(f"verify step: {n} cold {out['cold_us'][n]} us, hot {out['hot_us'][n]} us")
+    return out
 
 
 def summarize_rocprof(d, out, min_calls):
