@@ -25,7 +25,10 @@
 // the mantissa of 16.0 (16 + u, exact in fp16 and bf16), and the offset 24 =
 // 16 + 8 leaves with the sum: the products start from -24 * sum(q) of the
 // group's channels, in fp32, so that a score's rounding error follows sum |q|
-// (|k| + 24 s), s K's scale, not the score.
+// (|k| + 24 s), s K's scale, not the score.  The sum over groups starts from minus
+// the row's reference (a score near the row's running maximum): exponents are
+// differences of scores, taken before they are scaled, and stay small however far
+// from 0 the scores lie.
 //
 // Scales: K's multiply the fp32 sums of a group's channels; V's multiply the
 // probabilities, in fp32, and the products go to the matrix instruction as two
@@ -48,7 +51,7 @@
 // own rounding is eight times as coarse, one each: 2^-11 of either.  Us, 512 x up
 // to 16384 keys, 32 rows, G = 32: 197 with one term each, 240 with two, 287 with
 // V's scales of four groups on the probabilities.  The probability of the key that
-// set a row's offset is 2^7 at least and the smallest step of fp16 2^-31 of that:
+// set a row's reference is 2^7 at least and the smallest step of fp16 2^-31 of that:
 // whatever else a wave sees, a key's value loses at most half of it.
 //
 // Bound by: memory while few query rows share a key (a key of one head is D +
@@ -101,12 +104,12 @@ struct BF16 {
 };
 
 constexpr float kOffset = 24.0f;   // 16 of the widening + 8 of the nibble
-constexpr float kLowest = -FLT_MAX;  // exponent offset of a row that has seen no key
-// A row's offset follows its running maximum only when that has grown by more
-// than this (log2): with 16 rows or more a wave some row's maximum grows in
-// most steps, and every change scales all of O.  (The maximum starts at -inf, so
-// that a row's first key sets the offset however small the scale of scores is.)
-constexpr float kSlack = 8.0f;
+// A row's reference is a score near its running maximum: its first key's step
+// sets it, and it follows the maximum only when that has grown by more than
+// kAttentionSlack (log2): with 16 rows or more a wave some row's maximum grows in most
+// steps, and every change scales all of O.
+// Below every reference: where rows without keys join others.
+constexpr float kLowest = -FLT_MAX;
 
 // (a & m) | c.  In one v_and_or_b32 if the constants are in registers (the
 // instruction takes no literal): masks and magic numbers are made once, hidden
@@ -195,6 +198,12 @@ __device__ inline float max4(float v) {
 __device__ inline float sum4(float v) {
   const Two h = halves_of(v), q = quarters_of(h.a + h.b);
   return q.a + q.b;
+}
+
+// Natural logarithm of a row's sum of exponentials, from its reference and the sum
+// relative to that; -inf for a row without keys.
+__device__ inline float lse_of(float reference, float sum, float scale_log2) {
+  return sum == 0.0f ? -INFINITY : fmaf(reference, scale_log2, __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
 }
 
 // What a block works on: its sequence's lengths, all made safe.
@@ -415,11 +424,15 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, G, RT>(
   }
 
   f4_t o[RT][NC][4];
-  float mx[RT], mo[RT], l[RT], extra[RT][kScaleV ? 1 : NG];
+  // Scores are sums that start from minus the reference, so that their distance
+  // to it is exact where it counts, however far from 0 both are.
+  float less[RT];      // minus the reference
+  uint64_t fresh[RT];  // the lanes whose row has seen no key yet
+  float l[RT], extra[RT][kScaleV ? 1 : NG];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    mx[r] = -INFINITY;
-    mo[r] = kLowest;
+    less[r] = 0.0f;
+    fresh[r] = ~uint64_t(0);
     l[r] = 0.0f;
 #pragma unroll
     for (float &x : extra[r]) x = 0.0f;
@@ -432,7 +445,7 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, G, RT>(
   // (-1, 0) and (0, -1) in bf16; in registers, as the compiler takes the second
   // for the constant -1.0 of the instruction, which is another number there
   const uint32_t without[2] = {in_vgpr(PAIR && li < 8 ? 0u : 0x0000BF80u), in_vgpr(PAIR && li < 8 ? 0u : 0xBF800000u)};
-  constexpr float kHeadroom = kScaleV ? 15.0f - kSlack : 0.0f;
+  constexpr float kHeadroom = kScaleV ? 15.0f - (float)kAttentionSlack : 0.0f;
 
   const Constants constants = {in_sgpr(T::kMask), in_vgpr(T::kSixteen), in_sgpr(BF16::kMask), in_vgpr(0xC1F84180u),
                                in_sgpr(0x000F000Fu), in_sgpr(0x00F000F0u), in_vgpr(0x64006400u)};
@@ -473,7 +486,7 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, G, RT>(
       for (int j = 0; j < KJ; ++j) kf[j] = widen_k<T>(st.k[t][j], constants);
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        f4_t sum = {0, 0, 0, 0};
+        f4_t sum = {less[r], less[r], less[r], less[r]};
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           const float b = bias[r][g];
@@ -518,22 +531,26 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, G, RT>(
         }
     }
     bool grows = false;
-    float m_new[RT];
+    float top[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       float m = sc[r][0][0];
 #pragma unroll
       for (int x = 1; x < 8; ++x) m = maximum(m, sc[r][x / 4][x % 4]);
-      m_new[r] = fmaxf(mx[r], max4(m));
-      grows |= (m_new[r] - mx[r]) * a.scale_log2 > kSlack;
+      top[r] = max4(m);
+      grows |= top[r] > a.slack;
+      if (fresh[r]) grows |= __builtin_amdgcn_inverse_ballot_w64(fresh[r]) && top[r] > -INFINITY;
     }
     if (__any(grows)) {
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        mx[r] = m_new[r];
-        const float next = fmaxf(mx[r] * a.scale_log2, kLowest) - kHeadroom;
-        const float f = __builtin_amdgcn_exp2f(mo[r] - next);
-        mo[r] = next;
+        const bool first = __builtin_amdgcn_inverse_ballot_w64(fresh[r]), seen = top[r] > -INFINITY;  // no key, or a NaN
+        const float to = less[r] - (first ? (seen ? top[r] : 0.0f) : fmaxf(top[r], 0.0f));
+        const float up = less[r] - to, f = first ? 1.0f : __builtin_amdgcn_exp2f(-up * a.scale_log2);
+        less[r] = to;
+        fresh[r] &= ~__ballot(seen);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) sc[r][x / 4][x % 4] -= up;
         l[r] *= f;
 #pragma unroll
         for (float &x : extra[r]) x *= f;
@@ -550,7 +567,7 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, G, RT>(
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          p[r][t][x] = __builtin_amdgcn_exp2f(fmaf(sc[r][t][x], a.scale_log2, -mo[r]));
+          p[r][t][x] = __builtin_amdgcn_exp2f(fmaf(sc[r][t][x], a.scale_log2, kHeadroom));
           l[r] += p[r][t][x];
         }
     // the probabilities, times V's scales of a group or not, in two terms
@@ -664,12 +681,13 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, G, RT>(
   }
   __syncthreads();  // the stages make room for what follows
 
-  // the waves join: offsets and sums first, then the outputs of one 16-row
-  // tile at a time, each scaled to the common offset
+  // the waves join: references and sums first, then the outputs of one 16-row
+  // tile at a time, each scaled to the common reference
   float *ml = lds;                         // [waves][16 * RT][2]
   float *ob = lds + waves * 16 * RT * 2;   // [waves][16][kRowStride]
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
+    less[r] = __builtin_amdgcn_inverse_ballot_w64(fresh[r]) ? -INFINITY : -less[r];  // now the reference
     l[r] = sum4(l[r]);
     if constexpr (!kScaleV) {
 #pragma unroll
@@ -680,7 +698,7 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, G, RT>(
         for (int e = 0; e < 4; ++e) o[r][c][e] -= extra[r][(64 * c + 16 * e) / G];
     }
     if (la == 0) {
-      ml[(wave * 16 * RT + 16 * r + li) * 2] = mo[r];
+      ml[(wave * 16 * RT + 16 * r + li) * 2] = less[r];
       ml[(wave * 16 * RT + 16 * r + li) * 2 + 1] = l[r];
     }
   }
@@ -690,7 +708,7 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, G, RT>(
     if (r) __syncthreads();
     float top = kLowest;
     for (int x = 0; x < waves; ++x) top = fmaxf(top, ml[(x * 16 * RT + 16 * r + li) * 2]);
-    const float f = __builtin_amdgcn_exp2f(mo[r] - top);
+    const float f = __builtin_amdgcn_exp2f(fmaf(less[r] - top, a.scale_log2, -kHeadroom));
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -705,7 +723,7 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, G, RT>(
       f4_t v = {0, 0, 0, 0};
       for (int x = 0; x < waves; ++x) {
         const float *e = ml + (x * 16 * RT + 16 * r + i) * 2;
-        sum = fmaf(e[1], __builtin_amdgcn_exp2f(e[0] - m), sum);
+        sum = fmaf(e[1], __builtin_amdgcn_exp2f(fmaf(e[0] - m, a.scale_log2, -kHeadroom)), sum);
         v += *reinterpret_cast<const f4_t *>(ob + (x * 16 + i) * kRowStride + d);
         if (PAIR) v += *reinterpret_cast<const f4_t *>(ob + (x * 16 + i + 8) * kRowStride + d);
       }
@@ -717,7 +735,7 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, G, RT>(
         const w2_t bits = {T::from_float(v[0]) | T::from_float(v[1]) << 16,
                            T::from_float(v[2]) | T::from_float(v[3]) << 16};
         *reinterpret_cast<w2_t *>(static_cast<uint16_t *>(a.out) + at_row * D + d) = bits;
-        if (d == 0 && a.lse) a.lse[at_row] = sum == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+        if (d == 0 && a.lse) a.lse[at_row] = lse_of(m, sum, a.scale_log2);
       } else {
         const int64_t part = (int64_t)split * a.num_tokens * (a.kv_heads * a.share) + at_row;
         *reinterpret_cast<f4_t *>(a.part_o + part * D + d) = v;
@@ -756,7 +774,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionKernelArgs
   m = fmaxf(fmaxf(wave_m[0], wave_m[1]), fmaxf(wave_m[2], wave_m[3]));
   float sum = 0.0f;
   for (int s = tid; s < w.used; s += 256) {
-    const float f = __builtin_amdgcn_exp2f(weight[s] - m);
+    const float f = __builtin_amdgcn_exp2f((weight[s] - m) * a.scale_log2);
     weight[s] = f;
     sum = fmaf(a.part_ml[2 * (s * rows + row) + 1], f, sum);
   }
@@ -776,7 +794,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionKernelArgs
   v *= sum == 0.0f ? 0.0f : 1.0f / sum;
   const w2_t bits = {T::from_float(v[0]) | T::from_float(v[1]) << 16, T::from_float(v[2]) | T::from_float(v[3]) << 16};
   *reinterpret_cast<w2_t *>(static_cast<uint16_t *>(a.out) + row * D + d) = bits;
-  if (d == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+  if (d == 0 && a.lse) a.lse[row] = lse_of(m, sum, a.scale_log2);
 }
 
 // The same for few pieces: D/4 neighbouring threads hold a row and take its
@@ -805,14 +823,14 @@ __global__ __launch_bounds__(256) void attention_join_few_kernel(AttentionKernel
 #pragma unroll
   for (int s = 0; s < kFewSplits; ++s)
     if (s < w.used) {
-      const float f = __builtin_amdgcn_exp2f(mo[s] - m);
+      const float f = __builtin_amdgcn_exp2f((mo[s] - m) * a.scale_log2);
       sum = fmaf(l[s], f, sum);
       o += v[s] * f;
     }
   o *= sum == 0.0f ? 0.0f : 1.0f / sum;
   const w2_t bits = {T::from_float(o[0]) | T::from_float(o[1]) << 16, T::from_float(o[2]) | T::from_float(o[3]) << 16};
   *reinterpret_cast<w2_t *>(static_cast<uint16_t *>(a.out) + row * D + d) = bits;
-  if (d == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+  if (d == 0 && a.lse) a.lse[row] = lse_of(m, sum, a.scale_log2);
 }
 
 template <typename T, int D, int G, int RT, bool PAIR>

@@ -4,6 +4,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 
 #include "i4s_serve.h"
@@ -384,6 +385,7 @@ i4s_status i4s_attention(const i4s_attention_args *a, void *stream) {
   k.table = a->table, k.width = a->table_width, k.lens = a->lens, k.q_start = a->q_start;
   k.max_q = a->max_q, k.row_blocks = p.row_blocks, k.splits = p.splits, k.chunk = p.chunk;
   k.scale_log2 = (float)((double)a->scale * 1.4426950408889634);
+  k.slack = (float)std::fmin(i4s::kAttentionSlack / ((double)a->scale * 1.4426950408889634), FLT_MAX);
   k.tree = a->tree_mask, k.out = a->out, k.lse = a->lse;
   k.part_o = static_cast<float *>(a->workspace);
   k.part_ml = p.workspace_bytes ? k.part_o + (uint64_t)p.splits * rows * c.head_dim : nullptr;

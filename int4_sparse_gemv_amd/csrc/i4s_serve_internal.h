@@ -63,6 +63,9 @@ AttentionPlan attention_plan(const i4s_attention_args &a);
 
 constexpr int kMaxSplits = 4096;
 
+// How far (log2) a row's largest probability may pass 1 before its reference follows.
+constexpr int kAttentionSlack = 8;
+
 // Keys of one step of a wave.
 constexpr int kStepKeys = 32;
 
@@ -78,11 +81,12 @@ struct AttentionKernelArgs {
   const int32_t *lens, *q_start;
   int32_t max_q, row_blocks, splits, chunk;
   float scale_log2;  // scale * log2(e)
+  float slack;       // kAttentionSlack in units of scores
   const int64_t *tree;
   void *out;
   float *lse;
   float *part_o;     // [splits][num_tokens * q_heads][D]
-  float *part_ml;    // [splits][num_tokens * q_heads][2]: offset, sum
+  float *part_ml;    // [splits][num_tokens * q_heads][2]: reference, sum
 };
 hipError_t launch_attention(const AttentionKernelArgs &a, const AttentionPlan &p, int32_t head_dim,
                             int32_t group_size, int32_t dtype, hipStream_t stream);

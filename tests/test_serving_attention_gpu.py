@@ -6,8 +6,9 @@ The outputs are held against the float64 definition to the last half step of
 their type, by its true spacing, and what the arithmetic before that loses:
 
 * key j's score is off by at most d_j = scale (D + D/G + 8) 2^-24 sum |q| (|k_j|
-  + 24 s_j) (fp32 sums of products with 16 + u that start from -24 sum q), which
-  moves its weight by expm1(d_j) of itself, and the sum that divides by at most E
+  + 24 s_j) (fp32 sums of products with 16 + u that start from -24 sum q) and, as
+  the sum over groups starts from minus the row's reference, a score too, by
+  scale (D/G + 2) 2^-24 max |q . k|, which moves its weight by expm1(d_j) of itself, and the sum that divides by at most E
   = sum p_j expm1(d_j): together (sum p_j expm1(d_j) |v_j| + |out| E) / (1 - E);
 * a probability times V's scale s is taken in two bf16 terms, of 8 bits each:
   the first leaves 2^-8 of it, the second 2^-8 of that: 2^-16;
@@ -84,7 +85,7 @@ class Definition:
             self.p_s[some, h] = p @ vs[:, h // share]
             self.sum_v[some, h] = seen[some].astype(float) @ np.abs(vh)
             d = scale * (np.abs(qh) @ (np.abs(kh) + 24 * ks[:, h // share]).T) * (dim + dim // group + 8) * 2.0**-24
-            d = np.where(seen[some], d, 0)
+            d = np.where(seen[some], d + np.abs(np.where(seen[some], x, 0)).max(1, keepdims=True) * (dim // group + 2) * 2.0**-24, 0)
             z = (p * np.expm1(d)).sum(1, keepdims=True)
             assert (z < 0.5).all()
             self.moved[some, h] = ((p * np.expm1(d)) @ np.abs(vh) + np.abs(p @ vh) * z) / (1 - z)
@@ -370,3 +371,43 @@ def test_lengths_beyond_max_len(i4s, dtype, dim, group, share, max_len):
         c, d = held(i4s, rng, lens, 32, 1, dim, group)
         attend(i4s, rng, c, d, lens, q_lens, share, dtype, max_len=max_len, pieces=lambda n: n > 1,
                masks=random_masks(rng, q_lens) if tree else None)
+
+
+# ---------------------------------------------------------------------------
+# scores far from zero
+
+
+@pytest.mark.parametrize("dim,group,share,n_q,length,page", [(64, 32, 1, 1, 40, 16), (128, 64, 4, 1, 300, 32), (128, 32, 8, 4, 2000, 32),
+                                                            (128, 64, 8, 4, 700, 16), (256, 32, 2, 3, 900, 64), (256, 128, 1, 1, 3000, 64)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_of_billions(i4s, dtype, dim, group, share, n_q, length, page, sign):
+    """Scores that are whole multiples of 2^26 or more, exact in fp32: the largest one alone has a weight, and two equal
+    ones have a half each, wherever they lie; all of them far above or far below zero."""
+    say("billions", dim, group, share, n_q, length, dtype, sign)
+    for power in ((11, 13, 15) if dtype == F16 else (12, 20, 60)):
+        rng = np.random.default_rng(dim + length + power)
+        c, _ = filled(i4s, rng, -(-length // page), page, 1, dim, group)
+        c.k_scales[:] = 8192
+        c.k_vals[:] = 0x88
+        height = rng.integers(-7, 6, length)            # channel 0 of K, in steps of the scale
+        best = sorted(rng.choice(length - n_q, 2, replace=False)) if length > 50 else [3, 3]
+        height[best] = 6
+        height += sign                                  # all of one sign at the top
+        height = np.clip(height, -7, 7)
+        if sign < 0:
+            height = np.where(np.isin(np.arange(length), best), -1, np.minimum(height, -2))
+        for at, h in enumerate(height):
+            byte = c._at(at % page)[0][0]
+            c.k_vals[at // page, 0, byte] = 0x80 | int(h + 8)  # channel 0 is the word's first nibble
+        q = np.zeros((n_q, share, dim))
+        q[:, :, 0] = 2.0**power
+        d = device_cache(i4s, c)
+        _, v = c.read(np.arange(length))
+        lse = torch.empty(n_q, share).cuda()
+        out = f64(i4s.kv_attention(d, torch.from_numpy(q).to(dtype).cuda(), int32(np.arange(-(-length // page))[None]), int32([length]),
+                                   q_start=int32([0, n_q]), max_q=n_q, scale=4.0, lse=lse))
+        want = v[best, 0].mean(0)
+        assert np.isfinite(out).all() and (np.abs(out - want) <= 2.0**-8 * np.abs(v[best, 0]).max(0)).all(), (power, best)
+        top = 4.0 * 2.0**power * 8192 * (height.max() if sign > 0 else -1)
+        assert (np.abs(f64(lse) - top) <= 2.0**-21 * abs(top)).all()
