@@ -320,8 +320,8 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a, int shift)
 //
 // Bound by: memory.  The same 8191 tokens: 213 MB in 34 us, 6.3 TB/s (the cache,
 // just written, comes out of the last-level cache; 41 us with ordinary stores);
-// as fp32 from a cold cache 382 MB in 103 us, launch included (114 us with
-// ordinary stores); 16 tokens 2.9 us.
+// as fp32 382 MB in 109 us, 3.5 TB/s (129 us with stores past the caches);
+// 16 tokens 2.9 us.
 
 template <typename T>
 __device__ inline void store8(void *p, int64_t at, const f8_t &x) {
@@ -333,12 +333,11 @@ __device__ inline void store8(void *p, int64_t at, const f8_t &x) {
 struct Float {};
 template <>
 __device__ inline void store8<Float>(void *p, int64_t at, const f8_t &x) {
-  // two vectors of 16 bytes: the outputs have that alignment
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const f4_t half = {x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]};
-    __builtin_nontemporal_store(half, reinterpret_cast<f4_t *>(static_cast<float *>(p) + at) + h);
-  }
+  // two vectors of 16 bytes: the outputs have that alignment.  Not past the caches,
+  // where each store would fill half lines only
+  f4_t *to = reinterpret_cast<f4_t *>(static_cast<float *>(p) + at);
+  to[0] = f4_t{x[0], x[1], x[2], x[3]};
+  to[1] = f4_t{x[4], x[5], x[6], x[7]};
 }
 
 template <typename T, int D, int G>
