@@ -54,15 +54,18 @@
 // set a row's reference is 2^7 at least and the smallest step of fp16 2^-31 of that:
 // whatever else a wave sees, a key's value loses at most half of it.
 //
-// Bound by: memory while few query rows share a key (a key of one head is D +
-// 4D/G bytes; a copy of such sizes reaches 4.8 TB/s): 512 x up to 4095 keys, one
-// row, D = 128, G = 64: 170 MB in 39 us, 4.3 TB/s; 8 x 131071 keys, 4 rows: 143
-// MB in 29 us, 4.9 TB/s, and 4.0 us for the join of its 32 pieces.  With 32 rows a
-// key the vector instructions count (two for each widened pair, an exponential
-// and a scaling for each score) and the two waves a SIMD that the registers
-// leave: 512 x up to 16384 keys, G = 32: 675 MB in 188 us, 3.6 TB/s, the matrix
-// units busy in 16 % of the cycles, the vector units in half.  Short contexts are latency: 32 x 1023 keys
-// 11 us.
+// Bound by: memory's latency and the vector units together while few query rows
+// share a key (a key of one head is D + 4D/G bytes; a plain read of such sizes
+// reaches 6.7 TB/s, a copy 4.8): 512 x up to 4095 keys, one row, D = 128, G = 64: 170
+// MB in 41 us, 4.2 TB/s, vector instructions in 47 % of the cycles; 8 x 131071
+// keys, 4 rows: 143 MB in 31 us, 4.6 TB/s, and 4.0 us for the join of its 32
+// pieces.  With 32 rows a key neither is full: 512 x up to 16384 keys, G = 32, bf16:
+// 675 MB in 193 us, 3.5 TB/s, vector units 49 %, matrix units 15 %, two waves a SIMD
+// (what the registers leave).  Short contexts: 6 us for any (launch, page numbers,
+// queries, joining the waves) and 1.5 us for each step of a wave, 256 keys: 32 x
+// 1 / 256 / 512 / 1023 keys 6.2 / 7.8 / 9.4 / 12.  Many query tokens: each block
+// of 16 rows reads and widens every key, also those that its rows do not see: 2048
+// causal tokens of 40 heads 0.3 ms, 8191 4.0 ms, 172 TFLOP/s of what counts.
 
 #include <float.h>
 
@@ -248,7 +251,7 @@ typedef const __attribute__((address_space(4))) int32_t scalar_int32;  // read w
 
 // Keys that one block alone reads go past the caches (`once`), those that the
 // blocks of other query rows read too do not: 8 x 131071 keys, 4 rows: 34.7 /
-// 32.3 us without / with; 128 x 4000, 128 rows: 97 / 116.
+// 32.3 us without / with; 128 x 4000, 128 rows: 104 / 122.
 constexpr int kNonTemporal = 2;
 template <bool ONCE>
 __device__ inline void copy16(const void *from, char *to) {
@@ -859,7 +862,7 @@ hipError_t go(const AttentionKernelArgs &a, const AttentionPlan &p, hipStream_t 
 
 template <typename T, int D, int G>
 hipError_t by_rows(const AttentionKernelArgs &a, const AttentionPlan &p, hipStream_t stream) {
-  if constexpr (D / G >= 4)
+  if constexpr (D <= 128 && D / G >= 4)
     if (p.row_tiles == 2) return go<T, D, G, 2, false>(a, p, stream);
   if constexpr (!scale_on_v<D, G, 1>())
     if (a.max_q * a.share <= 8) return go<T, D, G, 1, true>(a, p, stream);

@@ -155,12 +155,13 @@ AttentionPlan attention_plan(const i4s_attention_args &a) {
   const i4s_kv_cache &c = *a.cache;
   AttentionPlan p{};
   const int64_t rows = (int64_t)a.max_q * (a.q_heads / c.kv_heads);
-  // 16 rows a block, or 32 where a head has four groups or more and the work
-  // a key costs by itself (its scales) counts.  Us, 32 / 16 rows a block: 512
-  // x 16384 keys, 32 rows, D = 128, G = 32: 211 / 336; but G = 64, 512 x 4000:
-  // 67 / 67, D = 64, G = 32, 256 x 4000, 40 rows: 51 / 32, D = 128, G = 64, 32 x
-  // 2000, 128 rows: 30 / 20; 64 rows a block were slower in all of these.
-  p.row_tiles = rows > 16 && c.head_dim / c.group_size >= 4 ? 2 : 1;
+  // 16 rows a block, or 32 where four groups make a key dear by itself (its
+  // scales) and the registers hold it.  Us, 32 / 16 rows a block, fp16 unless said
+  // otherwise: D = 128, G = 32, 512 x up to 16384 keys, 32 rows: 237 / 364, bf16 199
+  // / 362; but D = 256, 64 x 4000, 32 rows, G = 32: 48 / 45, bf16 44 / 40, G = 64: 45
+  // / 40, bf16 41 / 40; D = 64, G = 32, 256 x 4000, 40 rows: 95 / 56; D = 128, G = 64,
+  // 32 x 2000, 128 rows: 27 / 21, though 512 x 4000, 32 rows: 93 / 111.
+  p.row_tiles = rows > 16 && c.head_dim <= 128 && c.head_dim / c.group_size >= 4 ? 2 : 1;
   p.row_blocks = (int)((rows + 16 * p.row_tiles - 1) / (16 * p.row_tiles));
   // eight waves a block where their registers fit a compute unit: twice the
   // keys before a second launch has to join pieces
@@ -170,16 +171,19 @@ AttentionPlan attention_plan(const i4s_attention_args &a) {
   // The keys in pieces.  Measured in graphs, us, one query token of fp16, D =
   // 128, unless said otherwise (units = sequences x KV heads x row blocks):
   //   about one block for each of the 256 compute units: 8 units x 131071
-  //     keys in 32 / 64 pieces 35 / 41, in 16: 53; 64 x 8000 (8 rows) in 4 / 8
-  //     / 2: 22.0 / 23.2 / 30.5; 40 x 2047 (16 rows) in 4 / 8 / 1: 13.6 / 15.2
-  //     / 16.7; four waves, 40 x 4000 (64 rows) in 4 / 8: 31 / 39;
-  //   with as many units as that one piece (512 x 4095: 40, in 2 / 4: 48 /
-  //     50), but none longer than 4096 keys while that gives no more than about
+  //     keys in 32 / 64 / 16 pieces 35 / 33 / 54; 64 x 8000 (8 rows) in 4 / 8 / 2:
+  //     22.4 / 22.3 / 31.4; 40 x 2047 (16 rows) in 4 / 8 / 1: 13.5 / 14.8 / 18.8;
+  //     160 x 4000 (16 rows) in 1 / 4 / 8: 33 / 33 / 35;
+  //   with as many units as that one piece (512 x 4095, in 1 / 2 / 4: 59 / 58 /
+  //     63), but none longer than 4096 keys while that gives no more than about
   //     2048 blocks (and partial results of 35 MB), so that sequences of
-  //     different lengths fill the chip to the end (512 x 16384, 32 rows, in 4
-  //     / 2 / 1: 211 / 221 / 226);
-  //   a step or four of every wave are not worth a second launch on the host
-  //     (32 x 1023: 10.9 in one launch, 10.0 in two).
+  //     different lengths fill the chip to the end (512 x up to 16384, 32 rows,
+  //     in 4 / 2 / 1: 197 / 209 / 224);
+  //   a step or four of every wave are not worth a second launch (32 x 1023:
+  //     11.9 in one launch, 12.1 in two, and that costs the host 3).
+  // The pieces follow max_len, or the table's width where that is 0: a length far
+  // below it uses few of them (8 x 16384 keys, 4 rows: 14 with the length, 31
+  // with a table for 131072 tokens; 512 x up to 4095: 42 / 42).
   const int64_t units = (int64_t)p.row_blocks * c.kv_heads * (a.num_seqs > 0 ? a.num_seqs : 1);
   const int64_t step = kStepKeys * p.waves;
   const int64_t even = clamp_to<int64_t>((len + 4095) / 4096, 1, 2048 / units + 1);
@@ -196,8 +200,8 @@ LogprobsPlan logprobs_plan(int32_t dtype, int32_t rows, int32_t vocab, int32_t t
   LogprobsPlan p{};
   // Pieces for about two blocks a compute unit, where that pays a second
   // launch.  Measured in graphs, us, in one / several pieces: 1 x 150000 fp16
-  // 25 / 13 (16), 16 x 151643 fp32 35 / 17.5 (16), 64 x 50257 bf16 20 / 17
-  // (8), 200 x 151643 37 / 32 (2); but 16 x 32000 11 / 13 (2), 200 x 32000 15
+  // 25 / 13 (10), 16 x 151643 fp32 35 / 17.5 (10), 64 x 50257 bf16 20 / 17
+  // (7), 200 x 151643 37 / 32 (2); but 16 x 32000 11 / 13 (2), 200 x 32000 15
   // / 19 (2), 600 x 50257 31 / 35 (2).
   const int all = (vocab + 128 / dtype_size(dtype) - 1 + kSegment - 1) / kSegment;  // rows begin inside a line
   const int want = rows < 1 || rows > 256 || vocab <= 32768 ? 1 : clamp_to(512 / rows, 1, 16);

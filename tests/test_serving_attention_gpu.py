@@ -119,7 +119,7 @@ def pieces_of(d, tokens, q_heads, n, width, max_q, max_len):
 
 def scales_v(c, rows):
     groups = c.dim // c.group
-    return (2 if rows > 16 and groups >= 4 else 1) * groups >= 8
+    return (2 if rows > 16 and groups >= 4 and c.dim <= 128 else 1) * groups >= 8
 
 
 def attend(i4s, rng, c, d, lens, q_lens, share, dtype, q=None, masks=None, scale=None, max_len=0, pieces=None, table=None):
