@@ -159,11 +159,11 @@ i4s_status i4s_kv_read(const i4s_kv_cache *cache /* host */, const int32_t *slot
  * A token that sees no key gets out = 0 and lse = -inf.  Query head h reads
  * KV head h / (q_heads / kv_heads).  Scores, softmax statistics and sums are
  * held in fp32; a score is off by about 2^-24 scale sum |q| (|k| + 24 s), s K's
- * scales.  A probability times V's scale keeps 2^-16 of itself.  Many rows and
- * groups at once (D/G >= 8, or D = 128, G = 32 and more than 16 query rows of a
- * KV head): fp16 outputs keep 2^-21 of a probability times a value, bf16 ones
- * 2^-10, and a value whose probability is below 2^-21 of the largest loses up to
- * 2^-32 of itself. */
+ * scales.  A probability times V's scale is exact to 2^-16 of itself.  With many
+ * rows and groups (D/G >= 8, or D = 128, G = 32 and more than 16 query rows of a
+ * KV head) a probability times a value is exact to 2^-21 for fp16 and 2^-10 for
+ * bf16 outputs, and where the probability is below 2^-21 of the row's largest it
+ * is off by up to 2^-32 of that largest one instead. */
 typedef struct i4s_attention_args {
   const i4s_kv_cache *cache; /* host                                          */
   const void *q;             /* [num_tokens][q_heads][D], channels adjacent,  */

@@ -548,9 +548,10 @@ __global__ __launch_bounds__((most_threads<D, RT>()), (waves_per_simd<D, G, RT>(
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         const bool first = __builtin_amdgcn_inverse_ballot_w64(fresh[r]), seen = top[r] > -INFINITY;  // no key, or a NaN
-        const float to = less[r] - (first ? (seen ? top[r] : 0.0f) : fmaxf(top[r], 0.0f));
-        const float up = less[r] - to, f = first ? 1.0f : __builtin_amdgcn_exp2f(-up * a.scale_log2);
-        less[r] = to;
+        // up by the step's largest exactly: its distance is 0 now, whatever a last place of the score may be worth
+        const float up = first ? (seen ? top[r] : 0.0f) : fmaxf(top[r], 0.0f);
+        const float f = first ? 1.0f : __builtin_amdgcn_exp2f(-up * a.scale_log2);
+        less[r] -= up;
         fresh[r] &= ~__ballot(seen);
 #pragma unroll
         for (int x = 0; x < 8; ++x) sc[r][x / 4][x % 4] -= up;

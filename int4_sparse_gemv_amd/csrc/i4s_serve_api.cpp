@@ -388,8 +388,9 @@ i4s_status i4s_attention(const i4s_attention_args *a, void *stream) {
   k.num_tokens = a->num_tokens, k.num_seqs = a->num_seqs;
   k.table = a->table, k.width = a->table_width, k.lens = a->lens, k.q_start = a->q_start;
   k.max_q = a->max_q, k.row_blocks = p.row_blocks, k.splits = p.splits, k.chunk = p.chunk;
-  k.scale_log2 = (float)((double)a->scale * 1.4426950408889634);
-  k.slack = (float)std::fmin(i4s::kAttentionSlack / ((double)a->scale * 1.4426950408889634), FLT_MAX);
+  const double scale_log2 = (double)a->scale * 1.4426950408889634;
+  k.scale_log2 = (float)std::fmin(scale_log2, FLT_MAX);
+  k.slack = (float)std::fmin(i4s::kAttentionSlack / scale_log2, FLT_MAX);
   k.tree = a->tree_mask, k.out = a->out, k.lse = a->lse;
   k.part_o = static_cast<float *>(a->workspace);
   k.part_ml = p.workspace_bytes ? k.part_o + (uint64_t)p.splits * rows * c.head_dim : nullptr;

@@ -411,3 +411,26 @@ def test_scores_of_billions(i4s, dtype, dim, group, share, n_q, length, page, si
         assert np.isfinite(out).all() and (np.abs(out - want) <= 2.0**-8 * np.abs(v[best, 0]).max(0)).all(), (power, best)
         top = 4.0 * 2.0**power * 8192 * (height.max() if sign > 0 else -1)
         assert (np.abs(f64(lse) - top) <= 2.0**-21 * abs(top)).all()
+
+
+@pytest.mark.parametrize("dim,group,share,length", [(64, 64, 1, 300), (128, 64, 4, 2000), (128, 32, 24, 300), (256, 32, 1, 900)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_any_finite_scale(i4s, dim, group, share, length, dtype):
+    """A scale so large that the largest score alone has a weight."""
+    for scale in (1e30, 2.3e38, 3.4e38):
+        say("large scale", dim, group, share, length, dtype, scale)
+        rng = np.random.default_rng(dim + share + length)
+        pages = -(-length // 32)
+        c, d = filled(i4s, rng, pages, 32, 1, dim, group)
+        k, v = c.read(np.arange(length))
+        q = torch.from_numpy(rng.standard_normal((1, share, dim))).to(dtype)
+        x = f64(q)[0] @ k[:, 0].T
+        two = np.sort(x, 1)[:, -2:]
+        assert (two[:, 1] - two[:, 0] > 1e-3).all()  # fp32 tells them apart
+        out = f64(i4s.kv_attention(d, q.cuda(), int32(np.arange(pages)[None]), int32([length]), scale=scale))
+        best = x.argmax(1)
+        want, scales = v[best, 0], scales_of(c, best)[1][:, 0]
+        # the output's rounding, half a step of at most 2^-8, and 2^-10 for a probability and a scaled value of one term
+        # each; the offsets' additions (see the top) leave something of a value of 0 too
+        tol = (2.0**-8 + 2.0**-10) * np.abs(want) + (62 + 96) * 2.0**-23 * (length / 256 + 1) * scales
+        assert (np.abs(out[0] - want) <= tol).all(), scale
