@@ -12,7 +12,10 @@ Parallel Verification", sections 3.2 and 3.3.
 The rest of a decode or verification step is in ``serving``: a 4-bit paged KV
 cache (``kv_cache``, ``kv_extend``, ``kv_append``, ``kv_read``), attention
 over it (``kv_attention``) and token scores (``token_logprobs``), declared in
-``include/i4s_serve.h``.
+``include/i4s_serve.h``.  A prompt's step is in ``prompt``: products of any
+number of tokens in microscaled 4-bit floating point (``mx_quantize``,
+``mx_read``, ``mx_product``) and attention of whole prompts
+(``prompt_attention``), declared in ``include/i4s_prompt.h``.
 """
 
 from __future__ import annotations
@@ -36,6 +39,7 @@ __all__ = ["PackedWeight", "pack", "run", "run_multi", "pack_sizes", "run_worksp
 
 _SERVING = ("KVCache", "KVStep", "TokenLogprobs", "kv_cache", "kv_extend", "kv_append", "kv_read", "kv_attention",
             "token_logprobs")
+_PROMPT = ("MXTensor", "mx_quantize", "mx_read", "mx_product", "prompt_attention")
 
 
 def _torch_installed() -> bool:
@@ -45,18 +49,19 @@ def _torch_installed() -> bool:
         return False
 
 
-# the serving operators need torch when they are defined, packing only when it
+# the operators of these modules need torch when they are defined, packing only when it
 # is called: a star import, which resolves every name here, leaves them out
 # where there is no torch
 if _torch_installed():
-    __all__ += _SERVING
+    __all__ += _SERVING + _PROMPT
 
 
 def __getattr__(name):
-    if name in _SERVING or name == "serving":
-        serving = importlib.import_module(".serving", __name__)
-        globals().update({n: getattr(serving, n) for n in _SERVING})
-        return serving if name == "serving" else globals()[name]
+    for module, names in (("serving", _SERVING), ("prompt", _PROMPT)):
+        if name in names or name == module:
+            m = importlib.import_module("." + module, __name__)
+            globals().update({n: getattr(m, n) for n in names})
+            return m if name == module else globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

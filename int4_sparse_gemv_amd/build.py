@@ -29,7 +29,8 @@ LIB = os.path.join(PKG, "libi4s.so")
 FLOOR_LIB = os.path.join(PKG, "libi4s_floor.so")
 
 SOURCES = ("i4s_api.cpp", "i4s_plan.cpp", "i4s_pack.hip", "i4s_gemv_b1.hip", "i4s_gemv_b2.hip", "i4s_gemv_batch.hip",
-           "i4s_noalloc.hip", "i4s_serve_api.cpp", "i4s_kv.hip", "i4s_attention.hip", "i4s_logprobs.hip")
+           "i4s_noalloc.hip", "i4s_serve_api.cpp", "i4s_kv.hip", "i4s_attention.hip", "i4s_logprobs.hip",
+           "i4s_prompt_api.cpp", "i4s_mx.hip", "i4s_mx_product.hip", "i4s_prompt_attention.hip")
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

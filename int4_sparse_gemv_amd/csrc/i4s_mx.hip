@@ -1,0 +1,149 @@
+// Quantization to the microscaled 4-bit format and reading it back (format:
+// include/i4s_prompt.h), for gfx950.
+//
+// A wave takes 16 rows x 512 columns: the scales of a tile group.  Sixteen
+// neighbouring lanes hold 128 neighbouring columns of a row, eight each (16
+// bytes), so four lanes hold a block, whose largest magnitude two DPP steps
+// find as whole-number bits.  A lane's eight codes are four bytes of the
+// block's sixteen, and the rows 4i .. 4i+3 of a load lie next to each other in
+// the tile: every store covers whole 64-byte pieces.
+//
+// Bound by memory: 2 bytes read and 0.53 written a value.
+
+#include "i4s_mx_common.h"
+
+namespace i4s {
+namespace {
+
+constexpr int kMxThreads = 256;
+constexpr int kMxWavesPerBlock = kMxThreads / 64;
+
+// Largest of the four lanes of a quad.
+__device__ inline uint32_t quad_max(uint32_t v) {
+  v = max_halves(v, __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, false));  // lanes 1 0 3 2
+  return max_halves(v, __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, false));  // lanes 2 3 0 1
+}
+
+template <typename X>
+__global__ __launch_bounds__(kMxThreads) void mx_quantize_kernel(MxQuantizeArgs a) {
+  const int groups = mx_groups(a.cols), steps = mx_steps(a.cols);
+  const int64_t unit = (int64_t)blockIdx.x * kMxWavesPerBlock + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int64_t tile = unit / groups;
+  const int group = (int)(unit - tile * groups);
+  if (tile >= mx_row_tiles(a.rows)) return;
+  const int lane = threadIdx.x & 63, col = lane % 16 * 8, sub = lane / 16, quad = lane % 4, block = lane % 16 / 4;
+  const int left = steps - 4 * group < 4 ? steps - 4 * group : 4;  // tiles of this group
+  const uint16_t *x = static_cast<const uint16_t *>(a.x);
+  u4_t v[4][4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t row = tile * kMxRows + 4 * i + sub;
+      const int at = group * kMxGroup + c * kMxStep + col;
+      v[c][i] = u4_t{0, 0, 0, 0};
+      if (row < a.rows && at < a.cols)
+        v[c][i] = *reinterpret_cast<const u4_t *>(x + row * a.stride + at);
+    }
+  uint32_t scales[4] = {0, 0, 0, 0};
+  uint8_t *vals = a.vals + (tile * steps + 4 * group) * kMxTileBytes + block * 256 + quad * 4;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t pair = quad_max(top_bits(v[c][i]));
+      const uint32_t top = (pair & 0xFFFFu) > pair >> 16 ? pair & 0xFFFFu : pair >> 16;
+      const uint32_t byte = scale_byte<X>(top);
+      scales[i] |= byte << (8 * c);
+      const uint32_t word = byte == kMxNaN ? 0u : codes<X>(v[c][i], scale_value(byte));
+      if (c < left && tile * kMxRows + 4 * i + sub < a.rows)
+        *reinterpret_cast<uint32_t *>(vals + c * kMxTileBytes + (4 * i + sub) * 16) = word;
+    }
+  // the quad's lanes hold the same four scale words: each stores one
+  const uint32_t word = quad < 2 ? (quad ? scales[1] : scales[0]) : (quad == 3 ? scales[3] : scales[2]);
+  const int row = 4 * quad + sub;
+  if (tile * kMxRows + row < a.rows)
+    *reinterpret_cast<uint32_t *>(a.scales + (tile * groups + group) * kMxGroupBytes + (block * 16 + row) * 4) = word;
+}
+
+// Values 2i and 2i + 1 of a word of codes.
+typedef float f2_t __attribute__((ext_vector_type(2)));
+template <int B>
+__device__ inline f2_t two_values(uint32_t word) {
+  return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.0f, B);
+}
+
+struct AsHalf {
+  typedef uint16_t type;
+  static __device__ uint16_t of(float f) { return (uint16_t)float_to_fp16_bits(f); }
+};
+struct AsBrain {
+  typedef uint16_t type;
+  static __device__ uint16_t of(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+};
+struct AsFloat {
+  typedef float type;
+  static __device__ float of(float f) { return f; }
+};
+
+template <typename Y>
+__global__ __launch_bounds__(kMxThreads) void mx_read_kernel(MxReadArgs a) {
+  typedef typename Y::type T;
+  const int groups = mx_groups(a.cols), steps = mx_steps(a.cols);
+  const int64_t unit = (int64_t)blockIdx.x * kMxWavesPerBlock + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int64_t tile = unit / groups;
+  const int group = (int)(unit - tile * groups);
+  if (tile >= mx_row_tiles(a.rows)) return;
+  const int lane = threadIdx.x & 63, col = lane % 16 * 8, sub = lane / 16, quad = lane % 4, block = lane % 16 / 4;
+  const uint8_t *vals = a.vals + (tile * steps + 4 * group) * kMxTileBytes + block * 256 + quad * 4;
+  const uint8_t *scales = a.scales + (tile * groups + group) * kMxGroupBytes + block * 64;
+  T *out = static_cast<T *>(a.out);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = tile * kMxRows + 4 * i + sub;
+    if (row >= a.rows) continue;
+    const uint32_t four = *reinterpret_cast<const uint32_t *>(scales + (4 * i + sub) * 4);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int at = group * kMxGroup + c * kMxStep + col;
+      if (at >= a.cols) continue;
+      const uint32_t word = *reinterpret_cast<const uint32_t *>(vals + c * kMxTileBytes + (4 * i + sub) * 16);
+      const uint32_t byte = four >> (8 * c) & 255u;
+      const float scale = byte == kMxNaN ? __builtin_nanf("") : scale_value(byte);
+      const f2_t p[4] = {two_values<0>(word), two_values<1>(word), two_values<2>(word), two_values<3>(word)};
+      typedef T vec __attribute__((ext_vector_type(8)));
+      vec y;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = Y::of(p[e / 2][e % 2] * scale);
+      *reinterpret_cast<vec *>(out + row * a.cols + at) = y;
+    }
+  }
+}
+
+}  // namespace
+
+static int64_t mx_blocks(int32_t rows, int32_t cols) {
+  return ((int64_t)mx_row_tiles(rows) * mx_groups(cols) + kMxWavesPerBlock - 1) / kMxWavesPerBlock;
+}
+
+hipError_t launch_mx_quantize(const MxQuantizeArgs &a, int32_t dtype, hipStream_t stream) {
+  const dim3 grid((unsigned)mx_blocks(a.rows, a.cols));
+  if (dtype == I4S_F16)
+    hipLaunchKernelGGL(mx_quantize_kernel<HalfX>, grid, dim3(kMxThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL(mx_quantize_kernel<BrainX>, grid, dim3(kMxThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_read(const MxReadArgs &a, int32_t dtype, hipStream_t stream) {
+  const dim3 grid((unsigned)mx_blocks(a.rows, a.cols));
+  if (dtype == I4S_F16)
+    hipLaunchKernelGGL(mx_read_kernel<AsHalf>, grid, dim3(kMxThreads), 0, stream, a);
+  else if (dtype == I4S_BF16)
+    hipLaunchKernelGGL(mx_read_kernel<AsBrain>, grid, dim3(kMxThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL(mx_read_kernel<AsFloat>, grid, dim3(kMxThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace i4s

@@ -1,0 +1,384 @@
+// Products y = X W^T of matrices in the microscaled 4-bit format (format:
+// include/i4s_prompt.h), for gfx950.
+//
+// v_mfma_scale_f32_16x16x128_f8f6f4 multiplies 16 weight rows by 16 tokens
+// over 128 columns, 65536 operations in 16 cycles of a SIMD: lane 16 b + r
+// brings row (token) r's columns 32 b .. 32 b + 31, 16 bytes, and their scale,
+// one byte of a register that an immediate picks.  The format keeps both in that
+// order: a tile's values are one 16-byte load per lane, its scales for four
+// tiles one 4-byte load.  Lane 16 a + n of the result holds token n, rows 4 a
+// .. 4 a + 3.  Sums are fp32 from first to last; a product of two codes and
+// two powers of two is exact.
+
+#include <type_traits>
+
+#include "i4s_mx_common.h"
+
+namespace i4s {
+namespace {
+
+typedef int i8_t __attribute__((ext_vector_type(8)));
+typedef float f4_t __attribute__((ext_vector_type(4)));
+
+// One matrix instruction: scale byte C of sa and sb.  Format 4 is e2m1, which
+// takes half of the registers.
+template <int C>
+__device__ inline f4_t mx_mfma(u4_t a, uint32_t sa, u4_t b, uint32_t sb, f4_t c) {
+  const i8_t wa = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  const i8_t wb = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, wb, c, 4, 4, C, (int)sa, C, (int)sb);
+}
+
+__device__ inline u4_t load16(const void *p) { return *static_cast<const u4_t *>(p); }
+__device__ inline uint32_t load4(const void *p) { return *static_cast<const uint32_t *>(p); }
+
+template <typename Y>
+struct OutOf {};
+struct YHalf {
+  typedef uint16_t type;
+  static __device__ uint16_t of(float f) { return (uint16_t)float_to_fp16_bits(f); }
+};
+struct YBrain {
+  typedef uint16_t type;
+  static __device__ uint16_t of(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+};
+struct YFloat {
+  typedef float type;
+  static __device__ float of(float f) { return f; }
+};
+
+// ---------------------------------------------------------------------------
+// few tokens: the weight's bytes are the time
+//
+// A block takes RT weight tiles and up to 16 * NT tokens; its waves take the
+// groups of 512 columns in turn and join their sums in LDS.
+
+constexpr int kFewWaves = 8;
+
+struct NoX {};  // tokens in the format
+
+// One group's operands in registers.
+template <int N>
+struct Operand {
+  u4_t v[N][4];
+  uint32_t s[N];
+};
+
+template <int N>
+__device__ inline void load_operand(Operand<N> &o, const uint8_t *vals, const uint8_t *scales, int first, int tiles, int steps,
+                                    int groups, int group, int left, int lane) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int64_t tile = first + i < tiles ? first + i : tiles - 1;
+    o.s[i] = load4(scales + (tile * groups + group) * kMxGroupBytes + lane * 4);
+    const uint8_t *p = vals + (tile * steps + 4 * group) * kMxTileBytes + lane * 16;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o.v[i][c] = c < left ? load16(p + c * kMxTileBytes) : u4_t{0, 0, 0, 0};
+  }
+}
+
+// A lane's block of a 16-bit token: 32 values quantized.
+template <typename X>
+__device__ inline uint32_t quantize_block(const u4_t v[4], u4_t &out) {
+  uint32_t m = top_bits(v[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) m = max_halves(m, top_bits(v[i]));
+  const uint32_t top = (m & 0xFFFFu) > m >> 16 ? m & 0xFFFFu : m >> 16;
+  const uint32_t byte = scale_byte<X>(top);
+  const float scale = scale_value(byte);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[i] = byte == kMxNaN ? 0u : codes<X>(v[i], scale);
+  return byte;
+}
+
+template <typename X, typename Y, int RT, int NT>
+__global__ __launch_bounds__(kFewWaves * 64) void mx_few_kernel(MxProductKernelArgs a) {
+  constexpr bool kFused = !std::is_same<X, NoX>::value;
+  __shared__ float sums[kFewWaves][RT * NT][64][4];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
+  const int steps = mx_steps(a.cols), groups = mx_groups(a.cols), tiles = mx_row_tiles(a.rows);
+  const int first = blockIdx.x * RT;
+  f4_t acc[RT][NT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[r][n] = f4_t{0, 0, 0, 0};
+  for (int g = wave; g < groups; g += kFewWaves) {
+    const int left = steps - 4 * g < 4 ? steps - 4 * g : 4;
+    Operand<RT> w;
+    load_operand<RT>(w, a.w_vals, a.w_scales, first, tiles, steps, groups, g, left, lane);
+    Operand<NT> x;
+    if constexpr (kFused) {
+      const int token = lane % 16 < a.tokens ? lane % 16 : a.tokens - 1;
+      const uint16_t *p = static_cast<const uint16_t *>(a.x) + token * a.x_stride;
+      u4_t raw[4][4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int at = g * kMxGroup + c * kMxStep + lane / 16 * 32;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) raw[c][i] = at < a.cols ? load16(p + at + 8 * i) : u4_t{0, 0, 0, 0};
+      }
+      x.s[0] = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x.s[0] |= quantize_block<X>(raw[c], x.v[0][c]) << (8 * c);
+    } else {
+      load_operand<NT>(x, a.x_vals, a.x_scales, 0, mx_row_tiles(a.tokens), steps, groups, g, left, lane);
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        acc[r][n] = mx_mfma<0>(w.v[r][0], w.s[r], x.v[n][0], x.s[n], acc[r][n]);
+        acc[r][n] = mx_mfma<1>(w.v[r][1], w.s[r], x.v[n][1], x.s[n], acc[r][n]);
+        if (left == 4) {
+          acc[r][n] = mx_mfma<2>(w.v[r][2], w.s[r], x.v[n][2], x.s[n], acc[r][n]);
+          acc[r][n] = mx_mfma<3>(w.v[r][3], w.s[r], x.v[n][3], x.s[n], acc[r][n]);
+        }
+      }
+  }
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) *reinterpret_cast<f4_t *>(sums[wave][r * NT + n][lane]) = acc[r][n];
+  __syncthreads();
+  // 16 neighbouring rows of a token go out together
+  typename Y::type *y = static_cast<typename Y::type *>(a.y);
+  for (int at = threadIdx.x; at < RT * NT * 256; at += kFewWaves * 64) {
+    const int row = at % 16, token = at / 16 % 16, part = at / 256;
+    const int r = part % RT, n = part / RT, from = row / 4 * 16 + token;
+    float s = 0;
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) s += sums[w][r * NT + n][from][row % 4];
+    const int64_t t = 16 * n + token, out = (int64_t)(first + r) * 16 + row;
+    if (t < a.tokens && out < a.rows) y[t * a.y_stride + out] = Y::of(s);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// many tokens: the matrix instructions are the time
+//
+// A block of WR x WC waves takes WR*RT weight tiles x WC*NT token tiles; a
+// wave RT x NT of them.  Tiles go to LDS directly (global_load_lds), a step of
+// 128 columns at a time, into a ring of kRing steps; scales a group of four
+// steps at a time, into two areas.  One barrier a step: behind it every wave
+// has its step's tiles, and no wave reads the step before any more, whose place
+// the next load takes.
+
+constexpr int kRing = 4;
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) const void global_void;
+__device__ inline void copy16(const void *from, char *to) {
+  __builtin_amdgcn_global_load_lds((global_void *)from, (lds_void *)to, 16, 0, 0);
+}
+template <int N>
+__device__ inline void wait_loads() {
+  issue_fence();
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4 << 14));
+  issue_fence();
+}
+// Waves meet; LDS reads before it are done (their values are in use), direct
+// loads have been waited for.
+__device__ inline void meet() {
+  issue_fence();
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  issue_fence();
+}
+
+template <int RT, int NT, int WR, int WC>
+struct TileShape {
+  static constexpr int kWaves = WR * WC, kThreads = 64 * kWaves;
+  static constexpr int kA = WR * RT, kB = WC * NT;          // weight and token tiles of a block
+  static constexpr int kStep = (kA + kB) * kMxTileBytes;    // LDS bytes of a step
+  static constexpr int kScales = (kA + kB) * kMxGroupBytes; // LDS bytes of a group's scales
+  static constexpr int kLds = kRing * kStep + 2 * kScales;
+  static constexpr int kLoads = (kA + kB) / kWaves;         // load instructions of a wave and step
+  static_assert((kA + kB) % kWaves == 0, "tiles of a step are dealt evenly");
+  static constexpr int kScaleLoads = (kScales / 1024 + kWaves - 1) / kWaves;
+};
+
+// The block's place: consecutive blocks go to the eight XCDs in turn; each XCD
+// takes a contiguous range of places, ordered in bands of kBand weight tiles, so
+// that blocks that run together share what its L2 holds.
+constexpr int kBand = 8;
+struct Place {
+  int row, token;
+};
+__device__ inline Place place_of(int id, int rows, int tokens) {
+  const int n = rows * tokens, per = n / 8, more = n % 8, xcd = id % 8;
+  const int at = id / 8 + xcd * per + (xcd < more ? xcd : more);
+  const int band = at / (kBand * tokens), in = at - band * kBand * tokens;
+  const int wide = rows - band * kBand < kBand ? rows - band * kBand : kBand;
+  return {band * kBand + in % wide, in / wide};
+}
+
+template <typename Y, int RT, int NT, int WR, int WC, bool SPLIT>
+__global__ __launch_bounds__(64 * WR *WC) void mx_tile_kernel(MxProductKernelArgs a) {
+  typedef TileShape<RT, NT, WR, WC> S;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
+  const int all = mx_steps(a.cols), groups_all = mx_groups(a.cols);
+  const int row_tiles = mx_row_tiles(a.rows), token_tiles = mx_row_tiles(a.tokens);
+  const Place place = place_of(blockIdx.x, (row_tiles + S::kA - 1) / S::kA, (token_tiles + S::kB - 1) / S::kB);
+  const int row0 = place.row * S::kA, token0 = place.token * S::kB;
+  // this block's groups
+  const int g0 = SPLIT ? (int)((int64_t)groups_all * blockIdx.y / gridDim.y) : 0;
+  const int g1 = SPLIT ? (int)((int64_t)groups_all * (blockIdx.y + 1) / gridDim.y) : groups_all;
+  const int last = all - 1;
+
+  // the tiles that this wave brings
+  const uint8_t *from[S::kLoads];
+#pragma unroll
+  for (int i = 0; i < S::kLoads; ++i) {
+    const int t = wave * S::kLoads + i;
+    if (t < S::kA) {
+      const int64_t tile = row0 + t < row_tiles ? row0 + t : row_tiles - 1;
+      from[i] = a.w_vals + tile * all * kMxTileBytes + lane * 16;
+    } else {
+      const int64_t tile = token0 + t - S::kA < token_tiles ? token0 + t - S::kA : token_tiles - 1;
+      from[i] = a.x_vals + tile * all * kMxTileBytes + lane * 16;
+    }
+  }
+  // and the scales: 16 lanes a tile
+  const uint8_t *scales_from[S::kScaleLoads];
+#pragma unroll
+  for (int i = 0; i < S::kScaleLoads; ++i) {
+    int t = (wave * S::kScaleLoads + i) * 4 + lane / 16;
+    if (t >= S::kA + S::kB) t = S::kA + S::kB - 1;
+    if (t < S::kA) {
+      const int64_t tile = row0 + t < row_tiles ? row0 + t : row_tiles - 1;
+      scales_from[i] = a.w_scales + tile * groups_all * kMxGroupBytes + lane % 16 * 16;
+    } else {
+      const int64_t tile = token0 + t - S::kA < token_tiles ? token0 + t - S::kA : token_tiles - 1;
+      scales_from[i] = a.x_scales + tile * groups_all * kMxGroupBytes + lane % 16 * 16;
+    }
+  }
+  char *const ring = lds;
+  char *const scale_area = lds + kRing * S::kStep;
+  auto load_step = [&](int step) {
+    const int64_t at = (int64_t)(step < last ? step : last) * kMxTileBytes;
+#pragma unroll
+    for (int i = 0; i < S::kLoads; ++i)
+      copy16(from[i] + at, ring + (step & (kRing - 1)) * S::kStep + (wave * S::kLoads + i) * kMxTileBytes);
+  };
+  auto load_scales = [&](int group) {
+    const int64_t at = (int64_t)(group < groups_all ? group : groups_all - 1) * kMxGroupBytes;
+#pragma unroll
+    for (int i = 0; i < S::kScaleLoads; ++i) {
+      const int piece = wave * S::kScaleLoads + i;
+      if (S::kScales / 1024 == S::kWaves * S::kScaleLoads || piece < S::kScales / 1024)
+        copy16(scales_from[i] + at, scale_area + (group & 1) * S::kScales + piece * 1024);
+    }
+  };
+
+  const int wr = wave / WC, wc = wave % WC;
+  f4_t acc[RT][NT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[r][n] = f4_t{0, 0, 0, 0};
+
+  load_scales(g0);
+  load_step(4 * g0);
+  load_step(4 * g0 + 1);
+  load_step(4 * g0 + 2);
+  uint32_t sa[RT], sb[NT];
+  auto step = [&](int s, auto C) {
+    constexpr int c = decltype(C)::value;
+    // on their way behind this step's tiles: two more steps (and scales)
+    wait_loads<2 * S::kLoads>();
+    meet();
+    if (c == 0) load_scales(s / 4 + 1);
+    load_step(s + 3);
+    const char *base = ring + (s & (kRing - 1)) * S::kStep + lane * 16;
+    if (c == 0) {
+      const char *p = scale_area + (s / 4 & 1) * S::kScales + lane * 4;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) sa[r] = load4(p + (wr * RT + r) * kMxGroupBytes);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) sb[n] = load4(p + (S::kA + wc * NT + n) * kMxGroupBytes);
+    }
+    u4_t va[RT], vb[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) vb[n] = load16(base + (S::kA + wc * NT + n) * kMxTileBytes);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) va[r] = load16(base + (wr * RT + r) * kMxTileBytes);
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[r][n] = mx_mfma<c>(va[r], sa[r], vb[n], sb[n], acc[r][n]);
+  };
+  for (int g = g0; g < g1; ++g) {
+    step(4 * g, std::integral_constant<int, 0>());
+    step(4 * g + 1, std::integral_constant<int, 1>());
+    if (4 * g + 2 < all) {
+      step(4 * g + 2, std::integral_constant<int, 2>());
+      step(4 * g + 3, std::integral_constant<int, 3>());
+    }
+  }
+  wait_loads<0>();
+
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int64_t token = (int64_t)(token0 + wc * NT + n) * 16 + lane % 16;
+    if (token >= a.tokens) continue;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const int64_t row = (int64_t)(row0 + wr * RT + r) * 16 + lane / 16 * 4;
+      if constexpr (SPLIT) {
+        float *to = a.partial + ((int64_t)blockIdx.y * a.tokens + token) * a.rows + row;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (row + i < a.rows) to[i] = acc[r][n][i];
+      } else {
+        typename Y::type *to = static_cast<typename Y::type *>(a.y) + token * a.y_stride + row;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (row + i < a.rows) to[i] = Y::of(acc[r][n][i]);
+      }
+    }
+  }
+}
+
+template <typename Y>
+hipError_t launch_few(const MxProductKernelArgs &a, const MxProductPlan &p, hipStream_t stream) {
+  const dim3 grid((mx_row_tiles(a.rows) + p.row_tiles - 1) / p.row_tiles), block(kFewWaves * 64);
+#define I4S_FEW(X, RT, NT) hipLaunchKernelGGL((mx_few_kernel<X, Y, RT, NT>), grid, block, 0, stream, a)
+  if (a.x) {
+    if (a.x_dtype == I4S_F16) I4S_FEW(HalfX, 1, 1); else I4S_FEW(BrainX, 1, 1);
+  } else if (p.token_tiles == 1) {
+    I4S_FEW(NoX, 1, 1);
+  } else if (p.token_tiles == 2) {
+    I4S_FEW(NoX, 1, 2);
+  } else {
+    I4S_FEW(NoX, 1, 4);
+  }
+#undef I4S_FEW
+  return hipGetLastError();
+}
+
+template <typename Y, int RT, int NT, int WR, int WC>
+hipError_t launch_tiles(const MxProductKernelArgs &a, hipStream_t stream) {
+  typedef TileShape<RT, NT, WR, WC> S;
+  const int64_t blocks = (int64_t)((mx_row_tiles(a.rows) + S::kA - 1) / S::kA) * ((mx_row_tiles(a.tokens) + S::kB - 1) / S::kB);
+  hipLaunchKernelGGL((mx_tile_kernel<Y, RT, NT, WR, WC, false>), dim3((unsigned)blocks), dim3(S::kThreads), S::kLds, stream, a);
+  return hipGetLastError();
+}
+
+template <typename Y>
+hipError_t launch_product(const MxProductKernelArgs &a, const MxProductPlan &p, hipStream_t stream) {
+  if (p.few) return launch_few<Y>(a, p, stream);
+  if (p.tile == 256) return launch_tiles<Y, 8, 4, 2, 4>(a, stream);
+  return launch_tiles<Y, 4, 4, 2, 2>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_mx_product(const MxProductKernelArgs &a, const MxProductPlan &p, int32_t y_dtype, hipStream_t stream) {
+  if (y_dtype == I4S_F16) return launch_product<YHalf>(a, p, stream);
+  if (y_dtype == I4S_BF16) return launch_product<YBrain>(a, p, stream);
+  return launch_product<YFloat>(a, p, stream);
+}
+
+}  // namespace i4s

@@ -1,0 +1,455 @@
+// Attention of packed sequences over their own 16-bit keys and values
+// (include/i4s_prompt.h), for gfx950.
+//
+// A block takes the query rows (tokens x query heads) of one sequence that
+// read one KV head, 32 a wave; its waves share tiles of keys and values in
+// LDS, filled with direct 16-byte loads one step ahead of their use.  Scores
+// and outputs are computed transposed, so that no value moves between lanes
+// on the way:
+//   S^T = K Q^T: v_mfma_f32_32x32x16 with 32 keys as rows, 32 query rows as
+//     columns and 16 channels.  Lane l = i + 32 h holds query row i and the
+//     keys 8 x + 4 h + 0..3, x = 0..3, of a tile: its softmax is a loop over
+//     registers and one exchange with lane l ^ 32.
+//   O^T = V^T P^T: 32 channels as rows, 32 query rows as columns, 16 keys.  Its
+//     B operand wants query row i and 8 keys in lane l: P's registers as they
+//     are, for the keys 4 h + 0..3 and 8 + 4 h + 0..3.  Its A operand wants
+//     channel i and the same keys: ds_read_b64_tr_b16 hands 4 keys x 16
+//     channels of a row-major tile to 16 lanes, transposed.
+// Scores are summed from minus the row's reference on (a score near its
+// running maximum): exponents are exact differences however far from 0 the
+// scores lie, and the reference follows the maximum only when that has grown
+// by 8 powers of two, so O is scaled rarely.
+
+#include <float.h>
+
+#include <type_traits>
+
+#include "i4s_gemv_common.h"
+#include "i4s_prompt_internal.h"
+
+namespace i4s {
+namespace {
+
+typedef float f16_t __attribute__((ext_vector_type(16)));
+typedef float f4_t __attribute__((ext_vector_type(4)));
+typedef float f2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
+typedef short s4_t __attribute__((ext_vector_type(4)));
+typedef __bf16 b2_t __attribute__((ext_vector_type(2)));
+
+struct Half {
+  typedef _Float16 vec __attribute__((ext_vector_type(8)));
+  typedef h2_t pair;
+  static constexpr float kHeadroom = 7.0f;  // log2 of a probability's factor: 2^15 with the slack is finite
+  static constexpr uint32_t kInf = 0x7C00u, kOne = 0x3C00u;
+  static __device__ f16_t mfma(u4_t a, u4_t b, f16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(vec, a), __builtin_bit_cast(vec, b), c, 0, 0, 0);
+  }
+  static __device__ float dot(uint32_t a, uint32_t b, float c) {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(h2_t, a), __builtin_bit_cast(h2_t, b), c, false);
+  }
+};
+struct Brain {
+  typedef __bf16 vec __attribute__((ext_vector_type(8)));
+  typedef b2_t pair;
+  static constexpr float kHeadroom = 0.0f;  // fp32's exponents
+  static constexpr uint32_t kInf = 0x7F80u, kOne = 0x3F80u;
+  static __device__ f16_t mfma(u4_t a, u4_t b, f16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(vec, a), __builtin_bit_cast(vec, b), c, 0, 0, 0);
+  }
+  static __device__ float dot(uint32_t a, uint32_t b, float c) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2_t, a), __builtin_bit_cast(b2_t, b), c, false);
+  }
+};
+
+// Two values rounded to nearest even, the first in the low half.
+template <typename T>
+__device__ inline uint32_t two(float a, float b) {
+  const f2_t f = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, typename T::pair));
+}
+
+// The value of the other lane that holds the same query row.
+__device__ inline float other_half(float v, int lane) {
+  const uint32_t x = __builtin_bit_cast(uint32_t, v);
+  const auto s = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  const uint32_t a = s[0], b = s[1];
+  return __builtin_bit_cast(float, lane < 32 ? b : a);
+}
+
+__device__ inline float lse_of(float reference, float sum, float scale_log2, float headroom) {
+  return sum == 0.0f ? -INFINITY
+                     : fmaf(reference, scale_log2, __builtin_amdgcn_logf(sum) - headroom) * 0.6931471805599453f;
+}
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) const void global_void;
+__device__ inline void copy16(const void *from, char *to) {
+  __builtin_amdgcn_global_load_lds((global_void *)from, (lds_void *)to, 16, 0, 0);
+}
+template <int N>
+__device__ inline void wait_loads() {
+  issue_fence();
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4 << 14));
+  issue_fence();
+}
+// Waves meet: their LDS reads are done, their direct loads waited for.
+__device__ inline void meet() {
+  issue_fence();
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  issue_fence();
+}
+
+// What a block works on, all made safe.
+struct Sequence {
+  int q0, nq, k0, nk;
+};
+__device__ inline Sequence sequence_of(const PromptKernelArgs &a, int seq) {
+  Sequence s;
+  s.q0 = clamp_to(a.q_start[seq], 0, a.num_tokens);
+  s.nq = clamp_to(a.q_start[seq + 1], s.q0, a.num_tokens) - s.q0;
+  s.k0 = clamp_to(a.k_start[seq], 0, a.num_keys);
+  s.nk = clamp_to(a.k_start[seq + 1], s.k0, a.num_keys) - s.k0;
+  return s;
+}
+// How many keys query token t sees.
+__device__ inline int keys_seen(const PromptKernelArgs &a, const Sequence &s, int t) {
+  return a.causal ? clamp_to(s.nk - s.nq + t + 1, 0, s.nk) : s.nk;
+}
+
+// Tiles of K and V in LDS: rows of 2 D bytes, the 16-byte pieces of a row
+// exchanged by the row's number so that the rows that an instruction reads
+// together lie in different banks: for K (16 bytes of 32 rows) by the row, for
+// V (32 bytes of 8 rows) by twice the row.
+template <int D>
+struct Tile {
+  static constexpr int kPieces = D / 8;  // of a row
+  static constexpr int kKeys = D == 256 ? 32 : 64;
+  static constexpr int kBytes = kKeys * D * 2;
+  static __device__ int k_piece(int row, int piece) { return piece ^ (row & 7); }
+  static __device__ int v_piece(int row, int piece) { return piece ^ ((row & 7) << 1 & (kPieces - 1)); }
+};
+
+constexpr float kSlack = 8.0f;  // log2: how far a probability may pass 2^kHeadroom
+
+template <typename T, int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt_kernel(PromptKernelArgs a) {
+  typedef Tile<D> L;
+  constexpr int NK = L::kKeys / 32, NC = D / 32, NQ = D / 16;
+  constexpr int kLoads = 2 * L::kBytes / 1024 / WAVES;  // load instructions of a wave and step, half of them K's
+  constexpr int kRowsPerLoad = 64 / L::kPieces;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
+  const int li = lane & 31, lh = lane >> 5;
+
+  // long rows first; where the pairs of sequence and head are a multiple of
+  // eight each XCD takes its own ones, one after the other
+  const int pairs = a.num_seqs * a.kv_heads;
+  int pair, rb;
+  if (pairs % 8 == 0) {
+    const int j = blockIdx.x / 8;
+    pair = j / a.row_blocks * 8 + blockIdx.x % 8, rb = a.row_blocks - 1 - j % a.row_blocks;
+  } else {
+    pair = blockIdx.x % pairs, rb = a.row_blocks - 1 - blockIdx.x / pairs;
+  }
+  const int seq = pair / a.kv_heads, head = pair % a.kv_heads;
+  const Sequence s = sequence_of(a, seq);
+  const int tokens = s.nq < a.max_q ? s.nq : a.max_q;
+  const int rows = tokens * a.share, block_row = rb * WAVES * kPromptRows;
+  if (block_row >= rows) return;
+
+  // keys of this piece that any row of the block sees
+  const int last_row = block_row + WAVES * kPromptRows < rows ? block_row + WAVES * kPromptRows - 1 : rows - 1;
+  const int most = keys_seen(a, s, last_row / a.share);
+  const int piece0 = blockIdx.y * a.chunk;
+  const int piece1 = (int)blockIdx.y + 1 < a.splits && most - piece0 > a.chunk ? piece0 + a.chunk : most;
+  if (blockIdx.y && piece0 >= most) return;
+
+  const int row = block_row + wave * kPromptRows + li;
+  const int safe = row < rows ? row : rows - 1;
+  const int t = safe / a.share, q_head = head * a.share + (safe - t * a.share);
+  const int seen = keys_seen(a, s, t) < piece1 ? keys_seen(a, s, t) : piece1;  // this lane's row sees the keys below
+  const int wave_row = block_row + wave * kPromptRows < rows ? block_row + wave * kPromptRows : rows - 1;
+  const int all_see = keys_seen(a, s, wave_row / a.share);  // every row of the wave sees these
+  const int wave_last = wave_row + kPromptRows - 1 < rows ? wave_row + kPromptRows - 1 : rows - 1;
+  const int any_sees = keys_seen(a, s, wave_last / a.share);
+
+  u4_t q[NQ];
+  {
+    const uint16_t *p = static_cast<const uint16_t *>(a.q) + (int64_t)(s.q0 + t) * a.q_token + q_head * a.q_head + lh * 8;
+#pragma unroll
+    for (int c = 0; c < NQ; ++c) q[c] = *reinterpret_cast<const u4_t *>(p + 16 * c);
+  }
+
+  const char *kb = static_cast<const char *>(a.k) + 2 * (s.k0 * a.k_token + head * a.k_head);
+  const char *vb = static_cast<const char *>(a.v) + 2 * (s.k0 * a.v_token + head * a.v_head);
+  const uint32_t k_step = 2 * (uint32_t)a.k_token, v_step = 2 * (uint32_t)a.v_token;
+  // each wave brings kLoads / 2 pieces of 1024 bytes of K and of V
+  auto load_step = [&](int key, int stage) {
+    char *to = lds + stage * 2 * L::kBytes;
+    const char *k0 = kb + (int64_t)key * k_step, *v0 = vb + (int64_t)key * v_step;
+    const int left = s.nk - 1 - key;  // rows past it repeat the last: their scores are masked
+#pragma unroll
+    for (int i = 0; i < kLoads / 2; ++i) {
+      const int at = wave * (kLoads / 2) + i, r = at * kRowsPerLoad + lane / L::kPieces, p = lane % L::kPieces;
+      const int from = r < left ? r : left;
+      copy16(k0 + (uint32_t)(from * k_step + L::k_piece(r, p) * 16), to + at * 1024);
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads / 2; ++i) {
+      const int at = wave * (kLoads / 2) + i, r = at * kRowsPerLoad + lane / L::kPieces, p = lane % L::kPieces;
+      const int from = r < left ? r : left;
+      copy16(v0 + (uint32_t)(from * v_step + L::v_piece(r, p) * 16), to + L::kBytes + at * 1024);
+    }
+  };
+
+  f16_t o[NC], less;  // less: minus the row's reference, in every register
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[c][e] = 0;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) less[e] = 0;
+  float sum = 0;
+  bool fresh = true;
+
+  // V's operand: channels 32 c + li of the keys 16 x + 4 lh + 0..3 and + 8
+  const int tr_row = (lane & 15) / 4 + 4 * lh, tr_piece = (lane >> 4 & 1) * 2 + (lane & 3) / 2;
+  auto read_v = [&](const char *tile, int c, int x) {
+    u4_t r;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int key = 16 * x + 8 * y + tr_row;
+      const char *p = tile + key * 2 * D + L::v_piece(tr_row, 4 * c + tr_piece) * 16 + (lane & 1) * 8;
+      const u2_t w = __builtin_bit_cast(
+          u2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4_t *)p));
+      r[2 * y] = w.x, r[2 * y + 1] = w.y;
+    }
+    return r;
+  };
+
+  auto step = [&](int key, const char *stage) {
+    f16_t p[NK];
+#pragma unroll
+    for (int n = 0; n < NK; ++n) {
+      const char *tile = stage + (32 * n + li) * 2 * D;
+      u4_t k = *reinterpret_cast<const u4_t *>(tile + L::k_piece(li, lh) * 16);
+      p[n] = T::mfma(k, q[0], less);
+#pragma unroll
+      for (int c = 1; c < NQ; ++c) {
+        k = *reinterpret_cast<const u4_t *>(tile + L::k_piece(li, 2 * c + lh) * 16);
+        p[n] = T::mfma(k, q[c], p[n]);
+      }
+    }
+    const bool masked = key + L::kKeys > all_see || key + L::kKeys > piece1;
+    if (masked) {
+      const int limit = seen - key - 4 * lh;
+#pragma unroll
+      for (int n = 0; n < NK; ++n)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) p[n][e] = 32 * n + 8 * (e / 4) + e % 4 < limit ? p[n][e] : -INFINITY;
+    }
+    float top = p[0][0];
+#pragma unroll
+    for (int n = 0; n < NK; ++n)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, p[n][e]);
+    top = fmaxf(top, other_half(top, lane));
+    const bool grown = top * a.scale_log2 > kSlack || (fresh && top != -INFINITY);
+    if (__builtin_amdgcn_ballot_w64(grown)) {
+      const float by = grown ? top : 0.0f;
+      const float f = grown && fresh ? 0.0f : __builtin_amdgcn_exp2f(-by * a.scale_log2);
+      fresh = fresh && !grown;
+      sum *= f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) less[e] -= by;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[c][e] *= f;
+#pragma unroll
+      for (int n = 0; n < NK; ++n)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) p[n][e] -= by;
+    }
+    u4_t w[NK][2];
+#pragma unroll
+    for (int n = 0; n < NK; ++n) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        p[n][e] = __builtin_amdgcn_exp2f(fmaf(p[n][e], a.scale_log2, T::kHeadroom));
+        sum += p[n][e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[n][e / 4][e % 4] = two<T>(p[n][2 * e], p[n][2 * e + 1]);
+    }
+    const char *tile = stage + L::kBytes;
+    bool strange = false;  // values that are not finite may lie where a row does not see them
+    if (masked) {
+      float test = 0;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int x = 0; x < 2 * NK; ++x) {
+          const u4_t v = read_v(tile, c, x);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) test = T::dot(v[e], 0u, test);
+        }
+      strange = __builtin_amdgcn_ballot_w64(!(test == 0.0f)) != 0;
+    }
+    if (!strange) {
+#pragma unroll
+      for (int x = 0; x < 2 * NK; ++x)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) o[c] = T::mfma(read_v(tile, c, x), w[x / 2][x % 2], o[c]);
+      return;
+    }
+    // the finite ones as usual; then whether the row sees a +inf (-inf, either
+    // for a NaN) in the channel
+    const int limit = seen - key - 4 * lh;
+#pragma unroll 1
+    for (int x = 0; x < 2 * NK; ++x) {
+      u4_t sees, weight;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int at = 16 * x + 8 * (e / 2) + 2 * (e % 2);
+        sees[e] = (at < limit ? T::kOne : 0u) | (at + 1 < limit ? T::kOne << 16 : 0u);
+        weight[e] = x == 0 ? w[0][0][e] : (x == 1 ? w[0][1][e] : (x == 2 ? w[NK - 1][0][e] : w[NK - 1][1][e]));
+      }
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        u4_t v = read_v(tile, c, x), plus, minus;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t keep = 0, up = 0, down = 0;
+#pragma unroll
+          for (int b = 0; b < 32; b += 16) {
+            const uint32_t bits = v[e] >> b & 0xFFFFu, size = bits & 0x7FFFu;
+            if (size < T::kInf) keep |= bits << b;
+            if (size > T::kInf || bits == T::kInf) up |= T::kOne << b;
+            if (size > T::kInf || bits == (T::kInf | 0x8000u)) down |= T::kOne << b;
+          }
+          v[e] = keep, plus[e] = up, minus[e] = down;
+        }
+        o[c] = T::mfma(v, weight, o[c]);
+        f16_t zero;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) zero[e] = 0;
+        const f16_t ups = T::mfma(plus, sees, zero), downs = T::mfma(minus, sees, zero);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (ups[e] > 0) o[c][e] += INFINITY;
+          if (downs[e] > 0) o[c][e] -= INFINITY;
+        }
+      }
+    }
+  };
+
+  if (piece0 < piece1) {
+    load_step(piece0, 0);
+    int stage = 0;
+    for (int key = piece0; key < piece1; key += L::kKeys) {
+      wait_loads<0>();
+      meet();  // this step's tiles are here, and nobody reads the other stage
+      if (key + L::kKeys < piece1) load_step(key + L::kKeys, stage ^ 1);
+      if (key < any_sees) step(key, lds + stage * 2 * L::kBytes);
+      stage ^= 1;
+    }
+  }
+
+  sum += other_half(sum, lane);
+  if (row >= rows) return;
+  const int64_t out_row = (int64_t)(s.q0 + t) * a.kv_heads * a.share + q_head;
+  if (a.splits > 1) {
+    const int64_t at = (int64_t)blockIdx.y * a.num_tokens * a.kv_heads * a.share + out_row;
+    float *to = a.part_o + at * D + 4 * lh;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<f4_t *>(to + 32 * c + 8 * e) =
+            f4_t{o[c][4 * e], o[c][4 * e + 1], o[c][4 * e + 2], o[c][4 * e + 3]};
+    if (lh == 0) {
+      a.part_ml[2 * at] = fresh ? -FLT_MAX : -less[0];
+      a.part_ml[2 * at + 1] = sum;
+    }
+    return;
+  }
+  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+  uint16_t *to = static_cast<uint16_t *>(a.out) + out_row * D + 4 * lh;
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      *reinterpret_cast<u2_t *>(to + 32 * c + 8 * e) =
+          u2_t{two<T>(o[c][4 * e] * f, o[c][4 * e + 1] * f), two<T>(o[c][4 * e + 2] * f, o[c][4 * e + 3] * f)};
+  if (a.lse && lh == 0) a.lse[out_row] = lse_of(-less[0], sum, a.scale_log2, T::kHeadroom);
+}
+
+// Joins the pieces of a row: a wave a row, D / 64 channels a lane.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void prompt_join_kernel(PromptKernelArgs a) {
+  constexpr int N = D / 64;
+  const int seq = blockIdx.y, lane = threadIdx.x & 63, heads = a.kv_heads * a.share;
+  const Sequence s = sequence_of(a, seq);
+  const int tokens = s.nq < a.max_q ? s.nq : a.max_q;
+  const int64_t at = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  if (at >= (int64_t)tokens * heads) return;
+  const int64_t row = (int64_t)s.q0 * heads + at, all = (int64_t)a.num_tokens * heads;
+  const int seen = keys_seen(a, s, (int)(at / heads));
+  const int used = clamp_to((int)(((int64_t)seen + a.chunk - 1) / a.chunk), 1, a.splits);
+  float top = -FLT_MAX;
+  for (int p = 0; p < used; ++p) top = fmaxf(top, a.part_ml[2 * (p * all + row)]);
+  float sum = 0, o[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) o[i] = 0;
+  for (int p = 0; p < used; ++p) {
+    const float *ml = a.part_ml + 2 * (p * all + row);
+    if (ml[1] == 0.0f) continue;
+    const float f = __builtin_amdgcn_exp2f((ml[0] - top) * a.scale_log2);
+    sum += f * ml[1];
+    const float *from = a.part_o + (p * all + row) * D + lane * N;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] += f * from[i];
+  }
+  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+  uint16_t *to = static_cast<uint16_t *>(a.out) + row * D + lane * N;
+#pragma unroll
+  for (int i = 0; i < N; ++i) to[i] = (uint16_t)(two<T>(o[i] * f, 0.0f) & 0xFFFFu);
+  if (a.lse && lane == 0) a.lse[row] = lse_of(top, sum, a.scale_log2, T::kHeadroom);
+}
+
+template <typename T, int D, int WAVES>
+hipError_t launch_shape(const PromptKernelArgs &a, hipStream_t stream) {
+  const unsigned blocks = (unsigned)((int64_t)a.num_seqs * a.kv_heads * a.row_blocks);
+  constexpr size_t lds = 4 * Tile<D>::kBytes;
+  hipLaunchKernelGGL((prompt_kernel<T, D, WAVES>), dim3(blocks, a.splits), dim3(64 * WAVES), lds, stream, a);
+  if (a.splits > 1) {
+    const int64_t rows = (int64_t)a.max_q * a.kv_heads * a.share;
+    hipLaunchKernelGGL((prompt_join_kernel<T, D>), dim3((unsigned)((rows + 3) / 4), a.num_seqs), dim3(256), 0, stream, a);
+  }
+  return hipGetLastError();
+}
+
+template <typename T, int D>
+hipError_t launch_dim(const PromptKernelArgs &a, const PromptPlan &p, hipStream_t stream) {
+  return p.waves == 1 ? launch_shape<T, D, 1>(a, stream) : launch_shape<T, D, 4>(a, stream);
+}
+
+template <typename T>
+hipError_t launch_type(const PromptKernelArgs &a, const PromptPlan &p, int32_t head_dim, hipStream_t stream) {
+  if (head_dim == 64) return launch_dim<T, 64>(a, p, stream);
+  if (head_dim == 128) return launch_dim<T, 128>(a, p, stream);
+  return launch_dim<T, 256>(a, p, stream);
+}
+
+}  // namespace
+
+hipError_t launch_prompt_attention(const PromptKernelArgs &a, const PromptPlan &p, int32_t head_dim, int32_t dtype,
+                                   hipStream_t stream) {
+  return dtype == I4S_F16 ? launch_type<Half>(a, p, head_dim, stream) : launch_type<Brain>(a, p, head_dim, stream);
+}
+
+}  // namespace i4s

@@ -12,35 +12,14 @@
 
 using i4s::aligned;
 using i4s::check_device;
+using i4s::check_spans;
 using i4s::device_error;
+using i4s::dtype_size;
 using i4s::fail;
-using i4s::overlap;
+using i4s::kMaxBlocks;
+using i4s::Span;
 
 namespace {
-
-// blocks along one axis of a grid: threads are counted in 32 bits, up to 512 a block
-constexpr int64_t kMaxBlocks = 0x7FFFFF;
-
-struct Span {
-  const void *p;
-  uint64_t n;
-  const char *name;
-};
-
-// No output may share a byte with an input or with another output.
-template <int NO, int NI>
-i4s_status check_spans(const Span (&out)[NO], const Span (&in)[NI]) {
-  for (int i = 0; i < NO; ++i) {
-    if (!out[i].p || !out[i].n) continue;
-    for (int j = i + 1; j < NO; ++j)
-      if (out[j].p && out[j].n && overlap(out[i].p, out[i].n, out[j].p, out[j].n))
-        return fail(I4S_ERR_INVALID_ARGUMENT, "%s and %s overlap", out[i].name, out[j].name);
-    for (const Span &r : in)
-      if (r.p && r.n && overlap(out[i].p, out[i].n, r.p, r.n))
-        return fail(I4S_ERR_INVALID_ARGUMENT, "%s overlaps %s", out[i].name, r.name);
-  }
-  return I4S_OK;
-}
 
 i4s_status check_page_size(int32_t page_size) {
   if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)))
@@ -133,8 +112,6 @@ i4s_status check_attention(const i4s_attention_args *a) {
     return fail(I4S_ERR_INVALID_ARGUMENT, "max_q=%d times q_heads=%d must be below 2^23", a->max_q, a->q_heads);
   return I4S_OK;
 }
-
-int dtype_size(int32_t dtype) { return dtype == I4S_F32 ? 4 : 2; }
 
 i4s_status check_logprobs(int32_t dtype, int32_t rows, int32_t vocab, int32_t top_k) {
   if (dtype != I4S_F16 && dtype != I4S_BF16 && dtype != I4S_F32)

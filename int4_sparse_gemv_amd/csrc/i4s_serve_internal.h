@@ -14,6 +14,32 @@ __host__ __device__ inline T clamp_to(T v, T lo, T hi) {
   return v < lo ? lo : (v > hi ? hi : v);
 }
 
+// blocks along one axis of a grid: threads are counted in 32 bits, up to 512 a block
+constexpr int64_t kMaxBlocks = 0x7FFFFF;
+
+struct Span {
+  const void *p;
+  uint64_t n;
+  const char *name;
+};
+
+// No output may share a byte with an input or with another output.
+template <int NO, int NI>
+i4s_status check_spans(const Span (&out)[NO], const Span (&in)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    if (!out[i].p || !out[i].n) continue;
+    for (int j = i + 1; j < NO; ++j)
+      if (out[j].p && out[j].n && overlap(out[i].p, out[i].n, out[j].p, out[j].n))
+        return fail(I4S_ERR_INVALID_ARGUMENT, "%s and %s overlap", out[i].name, out[j].name);
+    for (const Span &r : in)
+      if (r.p && r.n && overlap(out[i].p, out[i].n, r.p, r.n))
+        return fail(I4S_ERR_INVALID_ARGUMENT, "%s overlaps %s", out[i].name, r.name);
+  }
+  return I4S_OK;
+}
+
+inline int dtype_size(int32_t dtype) { return dtype == I4S_F32 ? 4 : 2; }
+
 // log2 of a page size (16 .. 256).
 inline int page_shift(int32_t page_size) { return __builtin_ctz((unsigned)page_size); }
 
