@@ -32,8 +32,6 @@ __device__ inline f4_t mx_mfma(u4_t a, uint32_t sa, u4_t b, uint32_t sb, f4_t c)
 __device__ inline u4_t load16(const void *p) { return *static_cast<const u4_t *>(p); }
 __device__ inline uint32_t load4(const void *p) { return *static_cast<const uint32_t *>(p); }
 
-template <typename Y>
-struct OutOf {};
 struct YHalf {
   typedef uint16_t type;
   static __device__ uint16_t of(float f) { return (uint16_t)float_to_fp16_bits(f); }
@@ -213,8 +211,27 @@ __device__ inline Place place_of(int id, int rows, int tokens) {
   return {band * kBand + in % wide, in / wide};
 }
 
-template <typename Y, int RT, int NT, int WR, int WC, bool SPLIT>
-__global__ __launch_bounds__(64 * WR *WC) void mx_tile_kernel(MxProductKernelArgs a) {
+// Eight neighbouring values of y as 16 bits: of two 16-row tiles of a lane's
+// token, rows 4 b .. 4 b + 3 of either in the lanes 16 b + n, lanes 16 b + n
+// get the rows 8 b .. 8 b + 7 of the 32.
+template <typename Y>
+__device__ inline u4_t eight_rows(f4_t lo, f4_t hi) {
+  u4_t r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t x = Y::of(lo[2 * i]) | (uint32_t)Y::of(lo[2 * i + 1]) << 16;
+    const uint32_t y = Y::of(hi[2 * i]) | (uint32_t)Y::of(hi[2 * i + 1]) << 16;
+    const auto s = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+    const auto t = __builtin_amdgcn_permlane16_swap(s[0], s[1], false, false);
+    r[i] = t[0], r[2 + i] = t[1];
+  }
+  return r;
+}
+// 16 bytes at the alignment of an element.
+typedef u4_t loose_t __attribute__((aligned(2)));
+
+template <typename Y, int RT, int NT, int WR, int WC>
+__global__ __launch_bounds__(64 * WR *WC, 2) void mx_tile_kernel(MxProductKernelArgs a) {
   typedef TileShape<RT, NT, WR, WC> S;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
@@ -223,8 +240,8 @@ __global__ __launch_bounds__(64 * WR *WC) void mx_tile_kernel(MxProductKernelArg
   const Place place = place_of(blockIdx.x, (row_tiles + S::kA - 1) / S::kA, (token_tiles + S::kB - 1) / S::kB);
   const int row0 = place.row * S::kA, token0 = place.token * S::kB;
   // this block's groups
-  const int g0 = SPLIT ? (int)((int64_t)groups_all * blockIdx.y / gridDim.y) : 0;
-  const int g1 = SPLIT ? (int)((int64_t)groups_all * (blockIdx.y + 1) / gridDim.y) : groups_all;
+  const int g0 = (int)((int64_t)groups_all * blockIdx.y / gridDim.y);
+  const int g1 = (int)((int64_t)groups_all * (blockIdx.y + 1) / gridDim.y);
   const int last = all - 1;
 
   // the tiles that this wave brings
@@ -319,26 +336,33 @@ __global__ __launch_bounds__(64 * WR *WC) void mx_tile_kernel(MxProductKernelArg
   }
   wait_loads<0>();
 
+  // 16 bytes a lane, 64 neighbouring bytes of a token an instruction, at whatever
+  // alignment y has
+  typedef typename Y::type T;
+  typedef typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type W;
+  constexpr int kMany = 16 / sizeof(T), kTiles = kMany / 4;
+  const int64_t row_at = (int64_t)(row0 + wr * RT) * 16 + lane / 16 * kMany, token_at = (int64_t)(token0 + wc * NT) * 16 + lane % 16;
+  T *const to = static_cast<T *>(a.y) + ((int64_t)blockIdx.y * a.tokens + token_at) * a.y_stride + row_at;
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int64_t token = (int64_t)(token0 + wc * NT + n) * 16 + lane % 16;
-    if (token >= a.tokens) continue;
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const int64_t row = (int64_t)(row0 + wr * RT + r) * 16 + lane / 16 * 4;
-      if constexpr (SPLIT) {
-        float *to = a.partial + ((int64_t)blockIdx.y * a.tokens + token) * a.rows + row;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (row + i < a.rows) to[i] = acc[r][n][i];
+    for (int r = 0; r < RT; r += kTiles) {
+      u4_t v;
+      if constexpr (kTiles == 1)
+        v = __builtin_bit_cast(u4_t, acc[r][n]);
+      else
+        v = eight_rows<Y>(acc[r][n], acc[r + 1][n]);
+      T *const p = to + 16 * n * a.y_stride + 16 * r;
+      const int64_t left = a.rows - (row_at + 16 * r);
+      if (token_at + 16 * n >= a.tokens) continue;
+      if (left >= kMany) {
+        *reinterpret_cast<loose_t *>(p) = v;
       } else {
-        typename Y::type *to = static_cast<typename Y::type *>(a.y) + token * a.y_stride + row;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (row + i < a.rows) to[i] = Y::of(acc[r][n][i]);
+        for (int i = 0; i < kMany; ++i)
+          if (i < left) reinterpret_cast<W *>(p)[i] = (W)(kTiles == 1 ? v[i % 4] : v[i / 2] >> (16 * (i % 2)));
       }
     }
-  }
 }
 
 template <typename Y>
@@ -362,7 +386,7 @@ template <typename Y, int RT, int NT, int WR, int WC>
 hipError_t launch_tiles(const MxProductKernelArgs &a, hipStream_t stream) {
   typedef TileShape<RT, NT, WR, WC> S;
   const int64_t blocks = (int64_t)((mx_row_tiles(a.rows) + S::kA - 1) / S::kA) * ((mx_row_tiles(a.tokens) + S::kB - 1) / S::kB);
-  hipLaunchKernelGGL((mx_tile_kernel<Y, RT, NT, WR, WC, false>), dim3((unsigned)blocks), dim3(S::kThreads), S::kLds, stream, a);
+  hipLaunchKernelGGL((mx_tile_kernel<Y, RT, NT, WR, WC>), dim3((unsigned)blocks), dim3(S::kThreads), S::kLds, stream, a);
   return hipGetLastError();
 }
 
