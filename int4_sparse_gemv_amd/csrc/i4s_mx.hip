@@ -18,12 +18,6 @@ namespace {
 constexpr int kMxThreads = 256;
 constexpr int kMxWavesPerBlock = kMxThreads / 64;
 
-// Largest of the four lanes of a quad.
-__device__ inline uint32_t quad_max(uint32_t v) {
-  v = max_halves(v, __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, false));  // lanes 1 0 3 2
-  return max_halves(v, __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, false));  // lanes 2 3 0 1
-}
-
 template <typename X>
 __global__ __launch_bounds__(kMxThreads) void mx_quantize_kernel(MxQuantizeArgs a) {
   const int groups = mx_groups(a.cols), steps = mx_steps(a.cols);

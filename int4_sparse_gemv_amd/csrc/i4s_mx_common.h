@@ -43,6 +43,12 @@ __device__ inline uint32_t top_bits(u4_t v) {
   return max_halves(max_halves(v.x & kAbs, v.y & kAbs), max_halves(v.z & kAbs, v.w & kAbs));
 }
 
+// Largest of the four lanes of a quad.
+__device__ inline uint32_t quad_max(uint32_t v) {
+  v = max_halves(v, __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, false));  // lanes 1 0 3 2
+  return max_halves(v, __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, false));  // lanes 2 3 0 1
+}
+
 // A block's scale byte from the bits of its largest magnitude (their order is
 // that of the values; a NaN lies above infinity).
 template <typename X>

@@ -49,13 +49,16 @@ struct YFloat {
 // few tokens: the weight's bytes are the time
 //
 // A block takes RT weight tiles and up to 16 * NT tokens; its waves take the
-// groups of 512 columns in turn and join their sums in LDS.
+// groups of 512 columns in turn, the next one's tiles on their way while one is
+// multiplied, and join their sums in LDS.
+//
+// 16-bit tokens are quantized on the way, each wave the columns that it
+// multiplies: a token's 512 columns are one 16-byte load per lane, four
+// neighbouring lanes hold a block, and codes and scales pass through the wave's
+// own LDS into the matrix instruction's order.  Their loads go out first: they
+// come from L2, and loads return in order.
 
-constexpr int kFewWaves = 8;
-
-struct NoX {};  // tokens in the format
-
-// One group's operands in registers.
+// One group's tiles in registers.
 template <int N>
 struct Operand {
   u4_t v[N][4];
@@ -64,35 +67,27 @@ struct Operand {
 
 template <int N>
 __device__ inline void load_operand(Operand<N> &o, const uint8_t *vals, const uint8_t *scales, int first, int tiles, int steps,
-                                    int groups, int group, int left, int lane) {
+                                    int groups, int group, int lane) {
+  const int left = steps - 4 * group;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int64_t tile = first + i < tiles ? first + i : tiles - 1;
     o.s[i] = load4(scales + (tile * groups + group) * kMxGroupBytes + lane * 4);
     const uint8_t *p = vals + (tile * steps + 4 * group) * kMxTileBytes + lane * 16;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) o.v[i][c] = c < left ? load16(p + c * kMxTileBytes) : u4_t{0, 0, 0, 0};
+    for (int c = 0; c < 4; ++c)
+      if (c < 2 || left > 2) o.v[i][c] = load16(p + c * kMxTileBytes);
   }
 }
 
-// A lane's block of a 16-bit token: 32 values quantized.
-template <typename X>
-__device__ inline uint32_t quantize_block(const u4_t v[4], u4_t &out) {
-  uint32_t m = top_bits(v[0]);
-#pragma unroll
-  for (int i = 1; i < 4; ++i) m = max_halves(m, top_bits(v[i]));
-  const uint32_t top = (m & 0xFFFFu) > m >> 16 ? m & 0xFFFFu : m >> 16;
-  const uint32_t byte = scale_byte<X>(top);
-  const float scale = scale_value(byte);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) out[i] = byte == kMxNaN ? 0u : codes<X>(v[i], scale);
-  return byte;
-}
+struct NoX {};  // tokens in the format
 
-template <typename X, typename Y, int RT, int NT>
-__global__ __launch_bounds__(kFewWaves * 64) void mx_few_kernel(MxProductKernelArgs a) {
+template <typename X, typename Y, int RT, int NT, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void mx_few_kernel(MxProductKernelArgs a) {
   constexpr bool kFused = !std::is_same<X, NoX>::value;
-  __shared__ float sums[kFewWaves][RT * NT][64][4];
+  constexpr int kBatch = 4;  // tokens whose loads are on their way together
+  __shared__ float sums[WAVES][RT * NT][64][4];
+  __shared__ uint32_t own[kFused ? WAVES : 1][kFused ? 5 : 1][64][4];  // four tiles, and in the fifth place the scales
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
   const int steps = mx_steps(a.cols), groups = mx_groups(a.cols), tiles = mx_row_tiles(a.rows);
   const int first = blockIdx.x * RT;
@@ -101,36 +96,61 @@ __global__ __launch_bounds__(kFewWaves * 64) void mx_few_kernel(MxProductKernelA
   for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[r][n] = f4_t{0, 0, 0, 0};
-  for (int g = wave; g < groups; g += kFewWaves) {
-    const int left = steps - 4 * g < 4 ? steps - 4 * g : 4;
-    Operand<RT> w;
-    load_operand<RT>(w, a.w_vals, a.w_scales, first, tiles, steps, groups, g, left, lane);
-    Operand<NT> x;
-    if constexpr (kFused) {
-      const int token = lane % 16 < a.tokens ? lane % 16 : a.tokens - 1;
-      const uint16_t *p = static_cast<const uint16_t *>(a.x) + token * a.x_stride;
-      u4_t raw[4][4];
+
+  u4_t raw[kBatch];
+  auto load_tokens = [&](int g, int t0) {
+    const int at = g * kMxGroup + lane * 8;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int at = g * kMxGroup + c * kMxStep + lane / 16 * 32;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) raw[c][i] = at < a.cols ? load16(p + at + 8 * i) : u4_t{0, 0, 0, 0};
-      }
-      x.s[0] = 0;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) x.s[0] |= quantize_block<X>(raw[c], x.v[0][c]) << (8 * c);
-    } else {
-      load_operand<NT>(x, a.x_vals, a.x_scales, 0, mx_row_tiles(a.tokens), steps, groups, g, left, lane);
+    for (int i = 0; i < kBatch; ++i) {
+      raw[i] = u4_t{0, 0, 0, 0};
+      if (t0 + i < a.tokens && at < a.cols)
+        raw[i] = load16(static_cast<const uint16_t *>(a.x) + (t0 + i) * a.x_stride + at);
     }
+  };
+  Operand<RT> w;
+  Operand<NT> x;
+  auto load = [&](int g) {
+    if constexpr (kFused) load_tokens(g, 0);
+    load_operand<RT>(w, a.w_vals, a.w_scales, first, tiles, steps, groups, g, lane);
+    if constexpr (!kFused) load_operand<NT>(x, a.x_vals, a.x_scales, 0, mx_row_tiles(a.tokens), steps, groups, g, lane);
+  };
+  if (wave < groups) load(wave);
+  for (int g = wave; g < groups; g += WAVES) {
+    const Operand<RT> u = w;
+    Operand<NT> t = x;
+    if constexpr (kFused) {
+      // lane = 16 c + 4 b + quad: step c, block b
+      uint32_t *codes_at = &own[wave][lane / 16][lane / 4 % 4 * 16][lane % 4];
+      uint8_t *scale_at = reinterpret_cast<uint8_t *>(own[wave][4]) + lane / 4 % 4 * 64 + lane / 16;
+      for (int t0 = 0; t0 < a.tokens; t0 += kBatch) {
+        if (t0) load_tokens(g, t0);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (t0 + i < a.tokens) {
+            const uint32_t pair = quad_max(top_bits(raw[i]));
+            const uint32_t byte = scale_byte<X>((pair & 0xFFFFu) > pair >> 16 ? pair & 0xFFFFu : pair >> 16);
+            codes_at[(t0 + i) * 4] = byte == kMxNaN ? 0u : codes<X>(raw[i], scale_value(byte));
+            if (lane % 4 == 0) scale_at[(t0 + i) * 4] = (uint8_t)byte;
+          }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      t.s[0] = reinterpret_cast<const uint32_t *>(own[wave][4])[lane];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) t.v[0][c] = load16(own[wave][c][lane]);
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+    if (g + WAVES < groups) load(g + WAVES);
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        acc[r][n] = mx_mfma<0>(w.v[r][0], w.s[r], x.v[n][0], x.s[n], acc[r][n]);
-        acc[r][n] = mx_mfma<1>(w.v[r][1], w.s[r], x.v[n][1], x.s[n], acc[r][n]);
-        if (left == 4) {
-          acc[r][n] = mx_mfma<2>(w.v[r][2], w.s[r], x.v[n][2], x.s[n], acc[r][n]);
-          acc[r][n] = mx_mfma<3>(w.v[r][3], w.s[r], x.v[n][3], x.s[n], acc[r][n]);
+        acc[r][n] = mx_mfma<0>(u.v[r][0], u.s[r], t.v[n][0], t.s[n], acc[r][n]);
+        acc[r][n] = mx_mfma<1>(u.v[r][1], u.s[r], t.v[n][1], t.s[n], acc[r][n]);
+        if (steps - 4 * g > 2) {
+          acc[r][n] = mx_mfma<2>(u.v[r][2], u.s[r], t.v[n][2], t.s[n], acc[r][n]);
+          acc[r][n] = mx_mfma<3>(u.v[r][3], u.s[r], t.v[n][3], t.s[n], acc[r][n]);
         }
       }
   }
@@ -139,16 +159,16 @@ __global__ __launch_bounds__(kFewWaves * 64) void mx_few_kernel(MxProductKernelA
 #pragma unroll
     for (int n = 0; n < NT; ++n) *reinterpret_cast<f4_t *>(sums[wave][r * NT + n][lane]) = acc[r][n];
   __syncthreads();
-  // 16 neighbouring rows of a token go out together
+  // neighbouring rows of a token go out together
   typename Y::type *y = static_cast<typename Y::type *>(a.y);
-  for (int at = threadIdx.x; at < RT * NT * 256; at += kFewWaves * 64) {
-    const int row = at % 16, token = at / 16 % 16, part = at / 256;
-    const int r = part % RT, n = part / RT, from = row / 4 * 16 + token;
+  for (int at = threadIdx.x; at < RT * NT * 256; at += WAVES * 64) {
+    const int row = at % (16 * RT), token = at / (16 * RT);
+    const int r = row / 16, n = token / 16, from = row % 16 / 4 * 16 + token % 16;
     float s = 0;
 #pragma unroll
-    for (int w = 0; w < kFewWaves; ++w) s += sums[w][r * NT + n][from][row % 4];
-    const int64_t t = 16 * n + token, out = (int64_t)(first + r) * 16 + row;
-    if (t < a.tokens && out < a.rows) y[t * a.y_stride + out] = Y::of(s);
+    for (int w = 0; w < WAVES; ++w) s += sums[w][r * NT + n][from][row % 4];
+    const int64_t out = (int64_t)first * 16 + row;
+    if (token < a.tokens && out < a.rows) y[token * a.y_stride + out] = Y::of(s);
   }
 }
 
@@ -365,21 +385,30 @@ __global__ __launch_bounds__(64 * WR *WC, 2) void mx_tile_kernel(MxProductKernel
     }
 }
 
+template <typename X, typename Y, int RT, int NT, int WAVES>
+hipError_t launch_few_shape(const MxProductKernelArgs &a, hipStream_t stream) {
+  const dim3 grid((mx_row_tiles(a.rows) + RT - 1) / RT);
+  hipLaunchKernelGGL((mx_few_kernel<X, Y, RT, NT, WAVES>), grid, dim3(64 * WAVES), 0, stream, a);
+  return hipGetLastError();
+}
+
+template <typename X, typename Y, int NT>
+hipError_t launch_few_tokens(const MxProductKernelArgs &a, const MxProductPlan &p, hipStream_t stream) {
+  if (p.waves == 4) return launch_few_shape<X, Y, 2, NT, 4>(a, stream);
+  if constexpr (!std::is_same<X, NoX>::value)
+    if (p.row_tiles == 4) return launch_few_shape<X, Y, 4, NT, 8>(a, stream);
+  return p.row_tiles == 1 ? launch_few_shape<X, Y, 1, NT, 8>(a, stream) : launch_few_shape<X, Y, 2, NT, 8>(a, stream);
+}
+
 template <typename Y>
 hipError_t launch_few(const MxProductKernelArgs &a, const MxProductPlan &p, hipStream_t stream) {
-  const dim3 grid((mx_row_tiles(a.rows) + p.row_tiles - 1) / p.row_tiles), block(kFewWaves * 64);
-#define I4S_FEW(X, RT, NT) hipLaunchKernelGGL((mx_few_kernel<X, Y, RT, NT>), grid, block, 0, stream, a)
-  if (a.x) {
-    if (a.x_dtype == I4S_F16) I4S_FEW(HalfX, 1, 1); else I4S_FEW(BrainX, 1, 1);
-  } else if (p.token_tiles == 1) {
-    I4S_FEW(NoX, 1, 1);
-  } else if (p.token_tiles == 2) {
-    I4S_FEW(NoX, 1, 2);
-  } else {
-    I4S_FEW(NoX, 1, 4);
+  if (a.x) return a.x_dtype == I4S_F16 ? launch_few_tokens<HalfX, Y, 1>(a, p, stream) : launch_few_tokens<BrainX, Y, 1>(a, p, stream);
+  switch (p.token_tiles) {
+    case 1: return launch_few_tokens<NoX, Y, 1>(a, p, stream);
+    case 2: return launch_few_tokens<NoX, Y, 2>(a, p, stream);
+    case 3: return launch_few_tokens<NoX, Y, 3>(a, p, stream);
+    default: return launch_few_tokens<NoX, Y, 4>(a, p, stream);
   }
-#undef I4S_FEW
-  return hipGetLastError();
 }
 
 template <typename Y, int RT, int NT, int WR, int WC>

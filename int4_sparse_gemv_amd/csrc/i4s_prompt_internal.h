@@ -48,13 +48,13 @@ hipError_t launch_mx_read(const MxReadArgs &a, int32_t dtype, hipStream_t stream
 
 // How a product runs.  `quantize`: the 16-bit tokens are quantized into the
 // workspace first (otherwise the kernel does it on the way).  Few: blocks of
-// `rows_tiles` weight tiles and all tokens, whose waves split the columns.
-// Tiles: blocks of `tile` x `tile` outputs.  `splits` pieces of the columns,
-// whose partial sums a further launch adds.
+// `waves` waves that split the columns of `row_tiles` weight tiles and all
+// tokens.  Else blocks of `tile` x `tile` outputs, and `splits` pieces of the
+// columns, whose partial sums a further launch adds.
 struct MxProductPlan {
   bool quantize, few;
-  int32_t token_tiles;   // few: 16-token tiles of a block (1, 2 or 4)
-  int32_t row_tiles;     // few: 16-row tiles of a block
+  int32_t token_tiles;       // 16-token tiles
+  int32_t row_tiles, waves;  // few: (1, 8), (2, 8), (2, 4), or (4, 8) for 16-bit tokens
   int32_t tile;
   int32_t splits;
   uint64_t x_vals, x_scales;  // workspace bytes of the quantized tokens
