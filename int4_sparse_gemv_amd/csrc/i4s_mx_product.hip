@@ -112,7 +112,7 @@ __global__ __launch_bounds__(WAVES * 64) void mx_few_kernel(MxProductKernelArgs 
   auto load = [&](int g) {
     if constexpr (kFused) load_tokens(g, 0);
     load_operand<RT>(w, a.w_vals, a.w_scales, first, tiles, steps, groups, g, lane);
-    if constexpr (!kFused) load_operand<NT>(x, a.x_vals, a.x_scales, 0, mx_row_tiles(a.tokens), steps, groups, g, lane);
+    if constexpr (!kFused) load_operand<NT>(x, a.x_vals, a.x_scales, blockIdx.y * NT, mx_row_tiles(a.tokens), steps, groups, g, lane);
   };
   if (wave < groups) load(wave);
   for (int g = wave; g < groups; g += WAVES) {
@@ -167,8 +167,8 @@ __global__ __launch_bounds__(WAVES * 64) void mx_few_kernel(MxProductKernelArgs 
     float s = 0;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) s += sums[w][r * NT + n][from][row % 4];
-    const int64_t out = (int64_t)first * 16 + row;
-    if (token < a.tokens && out < a.rows) y[token * a.y_stride + out] = Y::of(s);
+    const int64_t out = (int64_t)first * 16 + row, t = (int64_t)blockIdx.y * NT * 16 + token;
+    if (t < a.tokens && out < a.rows) y[t * a.y_stride + out] = Y::of(s);
   }
 }
 
@@ -213,6 +213,7 @@ struct TileShape {
   static constexpr int kLds = kRing * kStep + 2 * kScales;
   static constexpr int kLoads = (kA + kB) / kWaves;         // load instructions of a wave and step
   static_assert((kA + kB) % kWaves == 0, "tiles of a step are dealt evenly");
+  static constexpr bool kTwice = RT * NT <= 16;              // registers for two steps' operands
   static constexpr int kScaleLoads = (kScales / 1024 + kWaves - 1) / kWaves;
 };
 
@@ -293,11 +294,13 @@ __global__ __launch_bounds__(64 * WR *WC, 2) void mx_tile_kernel(MxProductKernel
   }
   char *const ring = lds;
   char *const scale_area = lds + kRing * S::kStep;
+  auto load_tile = [&](int step, int i) {
+    copy16(from[i] + (int64_t)(step < last ? step : last) * kMxTileBytes,
+           ring + (step & (kRing - 1)) * S::kStep + (wave * S::kLoads + i) * kMxTileBytes);
+  };
   auto load_step = [&](int step) {
-    const int64_t at = (int64_t)(step < last ? step : last) * kMxTileBytes;
 #pragma unroll
-    for (int i = 0; i < S::kLoads; ++i)
-      copy16(from[i] + at, ring + (step & (kRing - 1)) * S::kStep + (wave * S::kLoads + i) * kMxTileBytes);
+    for (int i = 0; i < S::kLoads; ++i) load_tile(step, i);
   };
   auto load_scales = [&](int group) {
     const int64_t at = (int64_t)(group < groups_all ? group : groups_all - 1) * kMxGroupBytes;
@@ -316,43 +319,98 @@ __global__ __launch_bounds__(64 * WR *WC, 2) void mx_tile_kernel(MxProductKernel
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[r][n] = f4_t{0, 0, 0, 0};
 
-  load_scales(g0);
-  load_step(4 * g0);
-  load_step(4 * g0 + 1);
-  load_step(4 * g0 + 2);
-  uint32_t sa[RT], sb[NT];
-  auto step = [&](int s, auto C) {
-    constexpr int c = decltype(C)::value;
-    // on their way behind this step's tiles: two more steps (and scales)
-    wait_loads<2 * S::kLoads>();
-    meet();
-    if (c == 0) load_scales(s / 4 + 1);
-    load_step(s + 3);
-    const char *base = ring + (s & (kRing - 1)) * S::kStep + lane * 16;
-    if (c == 0) {
-      const char *p = scale_area + (s / 4 & 1) * S::kScales + lane * 4;
-#pragma unroll
-      for (int r = 0; r < RT; ++r) sa[r] = load4(p + (wr * RT + r) * kMxGroupBytes);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) sb[n] = load4(p + (S::kA + wc * NT + n) * kMxGroupBytes);
+  auto run = [&](auto step) {
+    for (int g = g0; g < g1; ++g) {
+      step(4 * g, std::integral_constant<int, 0>());
+      step(4 * g + 1, std::integral_constant<int, 1>());
+      if (4 * g + 2 < all) {
+        step(4 * g + 2, std::integral_constant<int, 2>());
+        step(4 * g + 3, std::integral_constant<int, 3>());
+      }
     }
-    u4_t va[RT], vb[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) vb[n] = load16(base + (S::kA + wc * NT + n) * kMxTileBytes);
-#pragma unroll
-    for (int r = 0; r < RT; ++r) va[r] = load16(base + (wr * RT + r) * kMxTileBytes);
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) acc[r][n] = mx_mfma<c>(va[r], sa[r], vb[n], sb[n], acc[r][n]);
   };
-  for (int g = g0; g < g1; ++g) {
-    step(4 * g, std::integral_constant<int, 0>());
-    step(4 * g + 1, std::integral_constant<int, 1>());
-    if (4 * g + 2 < all) {
-      step(4 * g + 2, std::integral_constant<int, 2>());
-      step(4 * g + 3, std::integral_constant<int, 3>());
-    }
+  if constexpr (S::kTwice) {
+    // Operands in two sets of registers, read a step ahead between this step's
+    // products, where a SIMD has one wave and nothing else to do meanwhile.
+    u4_t va[2][RT], vb[2][NT];
+    uint32_t sa[RT], sb[NT], next_sa[RT], next_sb[NT];
+    auto read_a = [&](int set, int s, int r) {
+      va[set][r] = load16(ring + (s & (kRing - 1)) * S::kStep + (wr * RT + r) * kMxTileBytes + lane * 16);
+    };
+    auto read_b = [&](int set, int s, int n) {
+      vb[set][n] = load16(ring + (s & (kRing - 1)) * S::kStep + (S::kA + wc * NT + n) * kMxTileBytes + lane * 16);
+    };
+    auto read_scales = [&](uint32_t *pa, uint32_t *pb, int g) {
+      const char *p = scale_area + (g & 1) * S::kScales + lane * 4;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) pa[r] = load4(p + (wr * RT + r) * kMxGroupBytes);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) pb[n] = load4(p + (S::kA + wc * NT + n) * kMxGroupBytes);
+    };
+    load_scales(g0);
+#pragma unroll
+    for (int i = 0; i < kRing; ++i) load_step(4 * g0 + i);
+    wait_loads<(kRing - 1) * S::kLoads>();
+    meet();
+    read_scales(sa, sb, g0);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) read_b(0, 4 * g0, n);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) read_a(0, 4 * g0, r);
+    run([&](int s, auto C) {
+      constexpr int c = decltype(C)::value, set = c & 1;
+      // two more steps (and scales) are on their way behind the next one
+      wait_loads<2 * S::kLoads>();
+      meet();  // this step's tiles are in registers: their place takes the fourth step from here
+      if (c == 0) load_scales(s / 4 + 1);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[r][n] = mx_mfma<c>(va[set][r], sa[r], vb[set][n], sb[n], acc[r][n]);
+#pragma unroll
+        for (int i = r * S::kLoads / RT; i < (r + 1) * S::kLoads / RT; ++i) load_tile(s + kRing, i);
+        if (c == 3 && r == 0) read_scales(next_sa, next_sb, s / 4 + 1);
+        read_a(set ^ 1, s + 1, r);
+#pragma unroll
+        for (int n = r * NT / RT; n < (r + 1) * NT / RT; ++n) read_b(set ^ 1, s + 1, n);
+      }
+      if (c == 3) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) sa[r] = next_sa[r];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) sb[n] = next_sb[n];
+      }
+    });
+  } else {
+    load_scales(g0);
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) load_step(4 * g0 + i);
+    uint32_t sa[RT], sb[NT];
+    run([&](int s, auto C) {
+      constexpr int c = decltype(C)::value;
+      // two more steps (and scales) are on their way behind this one
+      wait_loads<2 * S::kLoads>();
+      meet();  // nobody reads the step before this one any more
+      if (c == 0) load_scales(s / 4 + 1);
+      load_step(s + kRing - 1);
+      const char *base = ring + (s & (kRing - 1)) * S::kStep + lane * 16;
+      if (c == 0) {
+        const char *p = scale_area + (s / 4 & 1) * S::kScales + lane * 4;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) sa[r] = load4(p + (wr * RT + r) * kMxGroupBytes);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) sb[n] = load4(p + (S::kA + wc * NT + n) * kMxGroupBytes);
+      }
+      u4_t va[RT], vb[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) vb[n] = load16(base + (S::kA + wc * NT + n) * kMxTileBytes);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) va[r] = load16(base + (wr * RT + r) * kMxTileBytes);
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[r][n] = mx_mfma<c>(va[r], sa[r], vb[n], sb[n], acc[r][n]);
+    });
   }
   wait_loads<0>();
 
@@ -387,7 +445,7 @@ __global__ __launch_bounds__(64 * WR *WC, 2) void mx_tile_kernel(MxProductKernel
 
 template <typename X, typename Y, int RT, int NT, int WAVES>
 hipError_t launch_few_shape(const MxProductKernelArgs &a, hipStream_t stream) {
-  const dim3 grid((mx_row_tiles(a.rows) + RT - 1) / RT);
+  const dim3 grid((mx_row_tiles(a.rows) + RT - 1) / RT, (mx_row_tiles(a.tokens) + NT - 1) / NT);
   hipLaunchKernelGGL((mx_few_kernel<X, Y, RT, NT, WAVES>), grid, dim3(64 * WAVES), 0, stream, a);
   return hipGetLastError();
 }

@@ -143,7 +143,6 @@ MxProductPlan mx_product_plan(int32_t tokens, int32_t rows, int32_t cols, bool x
   // tokens 9.6 / 12.7, 8: 10.9 / 12.8, 16: 15.3 / 13.0; 4096 x 4096, 16 tokens: 7.3 / 7.0;
   // 4096 x 11008: 4: 7.8 / 10.2, 8: 11.4 / 10.3.
   p.quantize = !x_given && (tokens > 16 || (int64_t)tokens * cols >= 1 << 16);
-  p.few = tokens <= 64;
   p.token_tiles = (tokens + 15) / 16;
   // Blocks of eight waves and 1, 2 or (where each quantizes the tokens) 4 weight
   // tiles, about one for each of the 256 compute units; beyond, four waves and 2.
@@ -155,7 +154,18 @@ MxProductPlan mx_product_plan(int32_t tokens, int32_t rows, int32_t cols, bool x
   p.row_tiles = tiles <= 256 ? 1 : 2;
   p.waves = tiles <= 512 ? 8 : 4;
   if (!x_given && !p.quantize && tiles > 512 && tiles <= 1024) p.row_tiles = 4, p.waves = 8;
-  p.tile = ((int64_t)tokens + 255) / 256 * (((int64_t)rows + 255) / 256) >= 256 ? 256 : 128;
+  // Few tokens' blocks (more than 64 tokens: several of them, 2x4) while they fill
+  // the chip better than 128 x 128 outputs.  Us, few / 128 x 128: 4096 x 4096: 128 tokens
+  // 6.8 / 11.5, 256: 8.9 / 11.7, 384: 12.1 / 12; 5120 x 13824: 128: 20 / 31, 256: 29 / 31;
+  // 11008 x 4096: 64: 11 / 13, 128: 14.4 / 12.9; 13824 x 5120: 64: 13.6 / 15, 128: 20 / 17.
+  p.few = p.token_tiles <= 4 || (int64_t)tiles * p.token_tiles <= 5120;
+  if (p.token_tiles > 4) p.row_tiles = 2, p.waves = 4;
+  // 256 x 256 outputs, one block a compute unit, where they fill whole rounds of
+  // them; else 128 x 128, two blocks.  Us, 256 / 128: 4096^3 39 / 41 (256 blocks); 8191
+  // x 13824 x 5120 327 / 357 (6.75 rounds); 3000 x 13824 x 5120 127 / 125 (2.5 of 3);
+  // 4096 x 5120 x 13824 197 / 147 (1.25 of 2); 2048 x 4096 x 4096 34 / 23 (half of one).
+  const int64_t large = ((int64_t)tokens + 255) / 256 * (((int64_t)rows + 255) / 256);
+  p.tile = 10 * large >= 9 * ((large + 255) / 256 * 256) ? 256 : 128;
   p.splits = 1;
   if (p.quantize) {
     p.x_vals = mx_vals_bytes(tokens, cols);
