@@ -144,8 +144,8 @@ typedef struct i4s_prompt_args {
   int32_t num_keys;          /* rows of k and v, 0 .. 2^30                   */
   int32_t num_seqs;          /* 0 .. 65535                                   */
   int32_t max_q;             /* largest number of query tokens of a          */
-                             /* sequence, 1 .. 2^24; times q_heads at most   */
-                             /* 2^25, and num_seqs * kv_heads times its      */
+                             /* sequence, 1 .. 2^23; times q_heads below     */
+                             /* 2^23, and num_seqs * kv_heads times its      */
                              /* blocks of 128 rows (tokens x query heads of  */
                              /* a KV head) below 2^23                        */
   int32_t max_k;             /* largest number of keys of a sequence (0:     */

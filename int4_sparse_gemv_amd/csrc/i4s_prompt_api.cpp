@@ -100,22 +100,20 @@ i4s_status check_prompt(const i4s_prompt_args *a) {
     return fail(I4S_ERR_INVALID_ARGUMENT, "num_tokens=%d and num_keys=%d must be in [0, 2^30]", a->num_tokens, a->num_keys);
   if (a->num_seqs < 0 || a->num_seqs > 65535)
     return fail(I4S_ERR_INVALID_ARGUMENT, "num_seqs=%d must be in [0, 65535]", a->num_seqs);
-  if (a->max_q < 1 || a->max_q > 1 << 24)
-    return fail(I4S_ERR_INVALID_ARGUMENT, "max_q=%d must be in [1, 2^24]", a->max_q);
+  if (a->max_q < 1 || a->max_q > 1 << 23)
+    return fail(I4S_ERR_INVALID_ARGUMENT, "max_q=%d must be in [1, 2^23]", a->max_q);
   if (a->max_k < 0) return fail(I4S_ERR_INVALID_ARGUMENT, "max_k=%d must be 0 or more", a->max_k);
   if (a->causal != 0 && a->causal != 1) return fail(I4S_ERR_INVALID_ARGUMENT, "causal=%d must be 0 or 1", a->causal);
   if (!(a->scale > 0.0f) || !std::isfinite(a->scale))
     return fail(I4S_ERR_INVALID_ARGUMENT, "scale=%g must be positive and finite", (double)a->scale);
   if (a->reserved) return fail(I4S_ERR_INVALID_ARGUMENT, "reserved=%d must be 0", a->reserved);
-  // rows of a KV head are counted in 32 bits; a joining block takes four rows
-  if ((int64_t)a->max_q * a->q_heads > 0x7FFFFFFF / 2)
-    return fail(I4S_ERR_INVALID_ARGUMENT, "max_q=%d times q_heads=%d must be below 2^30", a->max_q, a->q_heads);
+  // a block of the second launch takes one row
+  if ((int64_t)a->max_q * a->q_heads > kMaxBlocks)
+    return fail(I4S_ERR_INVALID_ARGUMENT, "max_q=%d times q_heads=%d must be below 2^23", a->max_q, a->q_heads);
   const int64_t rows = (int64_t)a->max_q * (a->q_heads / a->kv_heads);
   const int64_t blocks = (rows + 127) / 128 * a->kv_heads * (a->num_seqs > 0 ? a->num_seqs : 1);
-  if (blocks > kMaxBlocks || ((int64_t)a->max_q * a->q_heads + 3) / 4 > kMaxBlocks)
-    return fail(I4S_ERR_INVALID_ARGUMENT,
-                "max_q=%d, q_heads=%d and num_seqs=%d make %lld blocks of 128 rows; at most 2^23, and max_q * q_heads at "
-                "most 2^25",
+  if (blocks > kMaxBlocks)
+    return fail(I4S_ERR_INVALID_ARGUMENT, "max_q=%d, q_heads=%d and num_seqs=%d make %lld blocks of 128 rows; at most 2^23 - 1",
                 a->max_q, a->q_heads, a->num_seqs, (long long)blocks);
   return I4S_OK;
 }
@@ -178,14 +176,24 @@ MxProductPlan mx_product_plan(int32_t tokens, int32_t rows, int32_t cols, bool x
 PromptPlan prompt_plan(const i4s_prompt_args &a) {
   PromptPlan p{};
   const int64_t rows = (int64_t)a.max_q * (a.q_heads / a.kv_heads);
-  p.waves = rows <= kPromptRows ? 1 : 4;
-  p.row_blocks = (int32_t)((rows + p.waves * kPromptRows - 1) / (p.waves * kPromptRows));
+  p.few = rows <= kPromptRows;
+  p.row_blocks = p.few ? 1 : (int32_t)((rows + 4 * kPromptRows - 1) / (4 * kPromptRows));
   const int64_t len = a.max_k > 0 && a.max_k < a.num_keys ? a.max_k : a.num_keys;
   const int64_t units = (int64_t)p.row_blocks * a.kv_heads * (a.num_seqs > 0 ? a.num_seqs : 1);
-  const int64_t want = clamp_to<int64_t>(512 / units, 1, (len + 511) / 512 > 0 ? (len + 511) / 512 : 1);
+  // Pairs of sequence and KV head that run together: as many as keep their keys in
+  // the L2s, but enough that long rows of one are done next to short ones of others.
+  // Us, groups of 1 / 20 / 40 / all pairs: 16 x up to 2047 tokens, 8 x 4 heads (128
+  // pairs of 64 blocks) 395 / 385 / 387 / 494; 8191 tokens, 40 heads 821 / 789 / 783 / 803.
+  p.group = 8 * ((160 + p.row_blocks - 1) / p.row_blocks);
+  // The keys in pieces for about two blocks of 128 rows a compute unit, or one of
+  // 32, but none shorter than 512 keys: partial results are fp32 and need a second
+  // launch.  Us, for 256 / 512 / 1024 blocks: 65536 keys, 8 x 4 rows 60 / 60 / 76;
+  // 128 tokens behind 32767, 8 x 4 heads 110 / 102 / 117.  512 tokens, 40 heads in one
+  // piece / two of 256 keys 25 / 52.
+  const int64_t want = clamp_to<int64_t>((p.few ? 256 : 512) / units, 1, len > 512 ? (len + 511) / 512 : 1);
   const int64_t per = clamp_to<int64_t>((len + want * kPromptKeys - 1) / (want * kPromptKeys), 1, (1 << 30) / kPromptKeys);
   p.chunk = (int32_t)(per * kPromptKeys);
-  p.splits = (int32_t)clamp_to<int64_t>((len + p.chunk - 1) / p.chunk, 1, 512);
+  p.splits = (int32_t)clamp_to<int64_t>((len + p.chunk - 1) / p.chunk, 1, kMaxPromptSplits);
   if (p.splits > 1)
     p.workspace_bytes = (uint64_t)p.splits * a.num_tokens * a.q_heads * (a.head_dim + 2) * sizeof(float);
   return p;
@@ -369,7 +377,7 @@ i4s_status i4s_prompt_attention(const i4s_prompt_args *a, void *stream) {
   k.kv_heads = a->kv_heads, k.share = a->q_heads / a->kv_heads;
   k.num_tokens = a->num_tokens, k.num_keys = a->num_keys, k.num_seqs = a->num_seqs;
   k.max_q = a->max_q, k.causal = a->causal;
-  k.row_blocks = p.row_blocks, k.splits = p.splits, k.chunk = p.chunk;
+  k.row_blocks = p.row_blocks, k.group = p.group, k.splits = p.splits, k.chunk = p.chunk;
   k.scale_log2 = (float)std::fmin((double)a->scale * 1.4426950408889634, FLT_MAX);
   k.q_start = a->q_start, k.k_start = a->k_start, k.out = a->out, k.lse = a->lse;
   k.part_o = static_cast<float *>(a->workspace);

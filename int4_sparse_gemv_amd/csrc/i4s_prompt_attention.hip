@@ -1,7 +1,7 @@
 // Attention of packed sequences over their own 16-bit keys and values
 // (include/i4s_prompt.h), for gfx950.
 //
-// A block takes the query rows (tokens x query heads) of one sequence that
+// A block takes 128 query rows (tokens x query heads) of one sequence that
 // read one KV head, 32 a wave; its waves share tiles of keys and values in
 // LDS, filled with direct 16-byte loads one step ahead of their use.  Scores
 // and outputs are computed transposed, so that no value moves between lanes
@@ -19,6 +19,25 @@
 // running maximum): exponents are exact differences however far from 0 the
 // scores lie, and the reference follows the maximum only when that has grown
 // by 8 powers of two, so O is scaled rarely.
+//
+// Roundings: scores, sums and outputs are fp32.  A probability is rounded to
+// the values' type for its matrix instruction (relative 2^-9 for bf16, 2^-12
+// for fp16), the sum takes it unrounded; the output is rounded once.
+//
+// Long prompts are bound by the matrix cores and the power they may take: 8191
+// tokens, 40 heads of 128, causal, 725 us = 0.95 PFLOP/s with the masked halves
+// of tiles, without the causal mask 1460 us = 0.94; matrix instructions alone
+// reach 1.9, and are busy half of the cycles, the softmax's vector instructions
+// the other half.  Tried and no faster: 32-key tiles with the next scores ahead of
+// this softmax (the same time, D = 256 slower), 64 rows a wave (spills).
+//
+// 32 rows or fewer of a sequence and KV head (a token behind long keys) are bound
+// by memory: there each wave of a block has tiles of 32 keys of its own, two of
+// them, in its own time with no barrier, and all join in LDS; long keys are
+// split over blocks, joined by a second launch.  65536 keys of 8 KV heads of 128,
+// 32 query heads: 59 us = 4.6 TB/s.  Us, waves x tiles ahead 3x3 / 4x2 / 5x2: 60.2 /
+// 59.5 / 61.8, D = 64 38.1 / 36.8 / 39.6; blocks of four waves sharing tiles of
+// 64 keys took 115.
 
 #include <float.h>
 
@@ -102,6 +121,15 @@ __device__ inline void meet() {
   issue_fence();
 }
 
+// Four keys x 16 channels of a row-major tile, transposed: lane i of 16 brings
+// the address of four channels of key i / 4 and gets channel i of the four keys.
+// The pointer's __restrict tells the compiler that direct loads on their way
+// write elsewhere (the barriers see to that): it would wait for them here.
+typedef __attribute__((address_space(3))) s4_t *lds_s4;
+__device__ inline __attribute__((always_inline)) u2_t read_transposed(lds_s4 __restrict p) {
+  return __builtin_bit_cast(u2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(p));
+}
+
 // What a block works on, all made safe.
 struct Sequence {
   int q0, nq, k0, nk;
@@ -121,58 +149,69 @@ __device__ inline int keys_seen(const PromptKernelArgs &a, const Sequence &s, in
 
 // Tiles of K and V in LDS: rows of 2 D bytes, the 16-byte pieces of a row
 // exchanged by the row's number so that the rows that an instruction reads
-// together lie in different banks: for K (16 bytes of 32 rows) by the row, for
-// V (32 bytes of 8 rows) by twice the row.
-template <int D>
+// together lie in different banks: for K (16 bytes of 32 rows) by 16 rows (D = 64:
+// by its 8 pieces), for V (32 bytes of 8 rows) by twice the row.  By 8 rows K's
+// reads took twice the cycles (half of all LDS cycles were conflicts).
+template <int D, int KEYS>
 struct Tile {
   static constexpr int kPieces = D / 8;  // of a row
-  static constexpr int kKeys = D == 256 ? 32 : 64;
+  static constexpr int kKeys = KEYS;
   static constexpr int kBytes = kKeys * D * 2;
-  static __device__ int k_piece(int row, int piece) { return piece ^ (row & 7); }
+  static __device__ int k_piece(int row, int piece) { return piece ^ (row & (kPieces < 16 ? 7 : 15)); }
   static __device__ int v_piece(int row, int piece) { return piece ^ ((row & 7) << 1 & (kPieces - 1)); }
 };
 
 constexpr float kSlack = 8.0f;  // log2: how far a probability may pass 2^kHeadroom
 
-template <typename T, int D, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt_kernel(PromptKernelArgs a) {
-  typedef Tile<D> L;
-  constexpr int NK = L::kKeys / 32, NC = D / 32, NQ = D / 16;
-  constexpr int kLoads = 2 * L::kBytes / 1024 / WAVES;  // load instructions of a wave and step, half of them K's
+// FEW: all query rows of a sequence and KV head fit a wave.  Then the waves of a
+// block take the same rows and tiles of their own in turn, and join at the end.
+// D = 256: 32 keys a tile, for 64 the registers do not reach.
+template <typename T, int D, bool FEW>
+struct Shape {
+  static constexpr int kWaves = FEW && D == 256 ? 2 : 4;
+  static constexpr int kBlockRows = FEW ? kPromptRows : kWaves * kPromptRows;
+  typedef Tile<D, FEW || D == 256 ? 32 : 64> L;
+  static constexpr int kLoaders = FEW ? 1 : kWaves;             // waves that share a tile's loads
+  static constexpr int kLoads = L::kBytes / 1024 / kLoaders;    // load instructions of a wave for K, and for V
+  static constexpr int kLds = (FEW ? kWaves : 1) * 4 * L::kBytes;
+  static constexpr int kRowFloats = D + 4;                      // of an output row where waves join
+  static_assert(!FEW || kWaves * kPromptRows * kRowFloats * 4 + kWaves * kPromptRows * 8 <= kLds, "joined in the tiles' LDS");
+};
+
+template <typename T, int D, bool FEW>
+__global__ __launch_bounds__((64 * Shape<T, D, FEW>::kWaves), (D == 256 || FEW ? 1 : 2)) void prompt_kernel(PromptKernelArgs a) {
+  typedef Shape<T, D, FEW> S;
+  typedef typename S::L L;
+  constexpr int NK = L::kKeys / 32, NC = D / 32, NQ = D / 16, kWaves = S::kWaves;
   constexpr int kRowsPerLoad = 64 / L::kPieces;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
   const int li = lane & 31, lh = lane >> 5;
 
-  // long rows first; where the pairs of sequence and head are a multiple of
-  // eight each XCD takes its own ones, one after the other
-  const int pairs = a.num_seqs * a.kv_heads;
-  int pair, rb;
-  if (pairs % 8 == 0) {
-    const int j = blockIdx.x / 8;
-    pair = j / a.row_blocks * 8 + blockIdx.x % 8, rb = a.row_blocks - 1 - j % a.row_blocks;
-  } else {
-    pair = blockIdx.x % pairs, rb = a.row_blocks - 1 - blockIdx.x / pairs;
-  }
+  // Groups of pairs (sequence, KV head) that share the L2s, in each the rows that
+  // see the most keys first; pairs in turn, so that XCDs share out the heads.
+  const int pairs = a.num_seqs * a.kv_heads, first_pair = blockIdx.x / (a.group * a.row_blocks) * a.group;
+  const int many = pairs - first_pair < a.group ? pairs - first_pair : a.group, in = blockIdx.x - first_pair * a.row_blocks;
+  const int pair = first_pair + in % many, rb = a.row_blocks - 1 - in / many;
   const int seq = pair / a.kv_heads, head = pair % a.kv_heads;
   const Sequence s = sequence_of(a, seq);
   const int tokens = s.nq < a.max_q ? s.nq : a.max_q;
-  const int rows = tokens * a.share, block_row = rb * WAVES * kPromptRows;
+  const int rows = tokens * a.share, block_row = rb * S::kBlockRows;
   if (block_row >= rows) return;
 
   // keys of this piece that any row of the block sees
-  const int last_row = block_row + WAVES * kPromptRows < rows ? block_row + WAVES * kPromptRows - 1 : rows - 1;
+  const int last_row = block_row + S::kBlockRows < rows ? block_row + S::kBlockRows - 1 : rows - 1;
   const int most = keys_seen(a, s, last_row / a.share);
   const int piece0 = blockIdx.y * a.chunk;
   const int piece1 = (int)blockIdx.y + 1 < a.splits && most - piece0 > a.chunk ? piece0 + a.chunk : most;
   if (blockIdx.y && piece0 >= most) return;
 
-  const int row = block_row + wave * kPromptRows + li;
+  const int first_row = block_row + (FEW ? 0 : wave * kPromptRows);
+  const int row = first_row + li;
   const int safe = row < rows ? row : rows - 1;
   const int t = safe / a.share, q_head = head * a.share + (safe - t * a.share);
   const int seen = keys_seen(a, s, t) < piece1 ? keys_seen(a, s, t) : piece1;  // this lane's row sees the keys below
-  const int wave_row = block_row + wave * kPromptRows < rows ? block_row + wave * kPromptRows : rows - 1;
-  const int all_see = keys_seen(a, s, wave_row / a.share);  // every row of the wave sees these
+  const int wave_row = first_row < rows ? first_row : rows - 1;
   const int wave_last = wave_row + kPromptRows - 1 < rows ? wave_row + kPromptRows - 1 : rows - 1;
   const int any_sees = keys_seen(a, s, wave_last / a.share);
 
@@ -186,20 +225,22 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt_kernel(Pr
   const char *kb = static_cast<const char *>(a.k) + 2 * (s.k0 * a.k_token + head * a.k_head);
   const char *vb = static_cast<const char *>(a.v) + 2 * (s.k0 * a.v_token + head * a.v_head);
   const uint32_t k_step = 2 * (uint32_t)a.k_token, v_step = 2 * (uint32_t)a.v_token;
-  // each wave brings kLoads / 2 pieces of 1024 bytes of K and of V
+  // this wave's pieces of 1024 bytes of K and of V
+  char *const tiles = lds + (FEW ? wave * 4 * L::kBytes : 0);
+  const int loader = FEW ? 0 : wave;
   auto load_step = [&](int key, int stage) {
-    char *to = lds + stage * 2 * L::kBytes;
+    char *to = tiles + stage * 2 * L::kBytes;
     const char *k0 = kb + (int64_t)key * k_step, *v0 = vb + (int64_t)key * v_step;
     const int left = s.nk - 1 - key;  // rows past it repeat the last: their scores are masked
 #pragma unroll
-    for (int i = 0; i < kLoads / 2; ++i) {
-      const int at = wave * (kLoads / 2) + i, r = at * kRowsPerLoad + lane / L::kPieces, p = lane % L::kPieces;
+    for (int i = 0; i < S::kLoads; ++i) {
+      const int at = loader * S::kLoads + i, r = at * kRowsPerLoad + lane / L::kPieces, p = lane % L::kPieces;
       const int from = r < left ? r : left;
       copy16(k0 + (uint32_t)(from * k_step + L::k_piece(r, p) * 16), to + at * 1024);
     }
 #pragma unroll
-    for (int i = 0; i < kLoads / 2; ++i) {
-      const int at = wave * (kLoads / 2) + i, r = at * kRowsPerLoad + lane / L::kPieces, p = lane % L::kPieces;
+    for (int i = 0; i < S::kLoads; ++i) {
+      const int at = loader * S::kLoads + i, r = at * kRowsPerLoad + lane / L::kPieces, p = lane % L::kPieces;
       const int from = r < left ? r : left;
       copy16(v0 + (uint32_t)(from * v_step + L::v_piece(r, p) * 16), to + L::kBytes + at * 1024);
     }
@@ -223,14 +264,14 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt_kernel(Pr
     for (int y = 0; y < 2; ++y) {
       const int key = 16 * x + 8 * y + tr_row;
       const char *p = tile + key * 2 * D + L::v_piece(tr_row, 4 * c + tr_piece) * 16 + (lane & 1) * 8;
-      const u2_t w = __builtin_bit_cast(
-          u2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4_t *)p));
+      const u2_t w = read_transposed((lds_s4)p);
       r[2 * y] = w.x, r[2 * y + 1] = w.y;
     }
     return r;
   };
 
-  auto step = [&](int key, const char *stage) {
+  auto step = [&](int key, const char *stage, auto MASKED) {
+    constexpr bool masked = decltype(MASKED)::value;
     f16_t p[NK];
 #pragma unroll
     for (int n = 0; n < NK; ++n) {
@@ -243,8 +284,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt_kernel(Pr
         p[n] = T::mfma(k, q[c], p[n]);
       }
     }
-    const bool masked = key + L::kKeys > all_see || key + L::kKeys > piece1;
-    if (masked) {
+    if constexpr (masked) {
       const int limit = seen - key - 4 * lh;
 #pragma unroll
       for (int n = 0; n < NK; ++n)
@@ -255,8 +295,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt_kernel(Pr
 #pragma unroll
     for (int n = 0; n < NK; ++n)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) top = fmaxf(top, p[n][e]);
-    top = fmaxf(top, other_half(top, lane));
+      for (int e = 0; e < 16; ++e) top = __builtin_elementwise_maximum(top, p[n][e]);
+    top = __builtin_elementwise_maximum(top, other_half(top, lane));
     const bool grown = top * a.scale_log2 > kSlack || (fresh && top != -INFINITY);
     if (__builtin_amdgcn_ballot_w64(grown)) {
       const float by = grown ? top : 0.0f;
@@ -287,7 +327,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt_kernel(Pr
     }
     const char *tile = stage + L::kBytes;
     bool strange = false;  // values that are not finite may lie where a row does not see them
-    if (masked) {
+    if constexpr (masked) {
       float test = 0;
 #pragma unroll
       for (int c = 0; c < NC; ++c)
@@ -347,19 +387,82 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt_kernel(Pr
     }
   };
 
-  if (piece0 < piece1) {
-    load_step(piece0, 0);
-    int stage = 0;
-    for (int key = piece0; key < piece1; key += L::kKeys) {
-      wait_loads<0>();
-      meet();  // this step's tiles are here, and nobody reads the other stage
-      if (key + L::kKeys < piece1) load_step(key + L::kKeys, stage ^ 1);
-      if (key < any_sees) step(key, lds + stage * 2 * L::kBytes);
-      stage ^= 1;
+  // every row of the block sees the keys of the first tiles; the others are masked
+  const int all_see = keys_seen(a, s, block_row / a.share);
+  const int plain = (all_see < piece1 ? all_see : piece1) - L::kKeys;
+  constexpr int kStride = FEW ? kWaves * L::kKeys : L::kKeys;
+  int key = piece0 + (FEW ? wave * L::kKeys : 0), stage = 0;
+  if (key < piece1) load_step(key, 0);
+  auto next = [&]() {
+    wait_loads<0>();
+    if constexpr (FEW) {
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the other stage is read
+      issue_fence();
+    } else {
+      meet();  // everybody's part of this step's tiles is here, and nobody reads the other stage
     }
+    if (key + kStride < piece1) load_step(key + kStride, stage ^ 1);
+  };
+  auto turn = [&]() { key += kStride, stage ^= 1; };
+#pragma unroll 1
+  while (key <= plain) {
+    next();
+    step(key, tiles + stage * 2 * L::kBytes, std::false_type());
+    turn();
+  }
+#pragma unroll 1
+  while (key < piece1) {
+    next();
+    if (key < any_sees) step(key, tiles + stage * 2 * L::kBytes, std::true_type());
+    turn();
   }
 
   sum += other_half(sum, lane);
+  if constexpr (FEW) {
+    // the waves join: references and sums first, then outputs at a common reference
+    wait_loads<0>();
+    __syncthreads();
+    float *const ml = reinterpret_cast<float *>(lds), *const rows_at = ml + kWaves * kPromptRows * 2;
+    if (lh == 0) {
+      ml[(wave * kPromptRows + li) * 2] = fresh ? -FLT_MAX : -less[0];
+      ml[(wave * kPromptRows + li) * 2 + 1] = sum;
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<f4_t *>(rows_at + (wave * kPromptRows + li) * S::kRowFloats + 32 * c + 8 * e + 4 * lh) =
+            f4_t{o[c][4 * e], o[c][4 * e + 1], o[c][4 * e + 2], o[c][4 * e + 3]};
+    __syncthreads();
+    constexpr int kFour = D / 4;  // lanes of an output row
+    for (int at = threadIdx.x; at < (rows < kPromptRows ? rows : kPromptRows) * kFour; at += 64 * kWaves) {
+      const int r = at / kFour, x = at % kFour * 4, tr = r / a.share;
+      float top = -FLT_MAX, l = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, ml[(w * kPromptRows + r) * 2]);
+      f4_t y = {0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float lw = ml[(w * kPromptRows + r) * 2 + 1];
+        if (lw == 0.0f) continue;  // saw no key
+        const float f = __builtin_amdgcn_exp2f((ml[(w * kPromptRows + r) * 2] - top) * a.scale_log2);
+        l += f * lw;
+        y += f * *reinterpret_cast<const f4_t *>(rows_at + (w * kPromptRows + r) * S::kRowFloats + x);
+      }
+      const int64_t out_row = ((int64_t)(s.q0 + tr) * a.kv_heads + head) * a.share + (r - tr * a.share);
+      if (a.splits > 1) {
+        const int64_t to = (int64_t)blockIdx.y * a.num_tokens * a.kv_heads * a.share + out_row;
+        *reinterpret_cast<f4_t *>(a.part_o + to * D + x) = y;
+        if (x == 0) a.part_ml[2 * to] = top, a.part_ml[2 * to + 1] = l;
+      } else {
+        const float f = l == 0.0f ? 0.0f : 1.0f / l;
+        *reinterpret_cast<u2_t *>(static_cast<uint16_t *>(a.out) + out_row * D + x) =
+            u2_t{two<T>(y.x * f, y.y * f), two<T>(y.z * f, y.w * f)};
+        if (a.lse && x == 0) a.lse[out_row] = lse_of(top, l, a.scale_log2, T::kHeadroom);
+      }
+    }
+    return;
+  }
   if (row >= rows) return;
   const int64_t out_row = (int64_t)(s.q0 + t) * a.kv_heads * a.share + q_head;
   if (a.splits > 1) {
@@ -388,54 +491,76 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt_kernel(Pr
   if (a.lse && lh == 0) a.lse[out_row] = lse_of(-less[0], sum, a.scale_log2, T::kHeadroom);
 }
 
-// Joins the pieces of a row: a wave a row, D / 64 channels a lane.
+// Joins the pieces of a row: a block a row.  Its threads take the pieces'
+// references and sums first, then D / 4 lanes an output of a piece.
+constexpr int kJoinThreads = 256;
 template <typename T, int D>
-__global__ __launch_bounds__(256) void prompt_join_kernel(PromptKernelArgs a) {
-  constexpr int N = D / 64;
-  const int seq = blockIdx.y, lane = threadIdx.x & 63, heads = a.kv_heads * a.share;
-  const Sequence s = sequence_of(a, seq);
+__global__ __launch_bounds__(kJoinThreads) void prompt_join_kernel(PromptKernelArgs a) {
+  constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
+  __shared__ float weight[kMaxPromptSplits];
+  __shared__ float waves[2][kJoinThreads / 64];
+  __shared__ f4_t part[kJoinThreads];
+  const int heads = a.kv_heads * a.share, lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+  const Sequence s = sequence_of(a, blockIdx.y);
   const int tokens = s.nq < a.max_q ? s.nq : a.max_q;
-  const int64_t at = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  if (at >= (int64_t)tokens * heads) return;
-  const int64_t row = (int64_t)s.q0 * heads + at, all = (int64_t)a.num_tokens * heads;
-  const int seen = keys_seen(a, s, (int)(at / heads));
+  if ((int64_t)blockIdx.x >= (int64_t)tokens * heads) return;
+  const int64_t row = (int64_t)s.q0 * heads + blockIdx.x, all = (int64_t)a.num_tokens * heads;
+  const int seen = keys_seen(a, s, (int)(blockIdx.x / heads));
   const int used = clamp_to((int)(((int64_t)seen + a.chunk - 1) / a.chunk), 1, a.splits);
-  float top = -FLT_MAX;
-  for (int p = 0; p < used; ++p) top = fmaxf(top, a.part_ml[2 * (p * all + row)]);
-  float sum = 0, o[N];
+  auto across = [&](float v, bool largest, int at) {  // of the whole block
 #pragma unroll
-  for (int i = 0; i < N; ++i) o[i] = 0;
-  for (int p = 0; p < used; ++p) {
+    for (int x = 1; x < 64; x *= 2) {
+      const float y = __shfl_xor(v, x);
+      v = largest ? fmaxf(v, y) : v + y;
+    }
+    if (lane == 0) waves[at][wave] = v;
+    __syncthreads();
+    v = waves[at][0];
+#pragma unroll
+    for (int x = 1; x < kJoinThreads / 64; ++x) v = largest ? fmaxf(v, waves[at][x]) : v + waves[at][x];
+    return v;
+  };
+  float top = -FLT_MAX, sum = 0;
+  for (int p = threadIdx.x; p < used; p += kJoinThreads) top = fmaxf(top, a.part_ml[2 * (p * all + row)]);
+  top = across(top, true, 0);
+  for (int p = threadIdx.x; p < used; p += kJoinThreads) {
     const float *ml = a.part_ml + 2 * (p * all + row);
-    if (ml[1] == 0.0f) continue;
-    const float f = __builtin_amdgcn_exp2f((ml[0] - top) * a.scale_log2);
+    const float f = ml[1] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f((ml[0] - top) * a.scale_log2);  // no key: 0
+    weight[p] = f;
     sum += f * ml[1];
-    const float *from = a.part_o + (p * all + row) * D + lane * N;
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] += f * from[i];
   }
-  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-  uint16_t *to = static_cast<uint16_t *>(a.out) + row * D + lane * N;
+  sum = across(sum, false, 1);
+  const int x = threadIdx.x % kLanes * 4, group = threadIdx.x / kLanes;
+  f4_t o = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int p = group; p < used; p += kGroups)
+    if (weight[p] != 0.0f) o += weight[p] * *reinterpret_cast<const f4_t *>(a.part_o + (p * all + row) * D + x);
+  part[threadIdx.x] = o;
+  __syncthreads();
+  if (group) return;
 #pragma unroll
-  for (int i = 0; i < N; ++i) to[i] = (uint16_t)(two<T>(o[i] * f, 0.0f) & 0xFFFFu);
-  if (a.lse && lane == 0) a.lse[row] = lse_of(top, sum, a.scale_log2, T::kHeadroom);
+  for (int g = 1; g < kGroups; ++g) o += part[g * kLanes + threadIdx.x];
+  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+  *reinterpret_cast<u2_t *>(static_cast<uint16_t *>(a.out) + row * D + x) =
+      u2_t{two<T>(o.x * f, o.y * f), two<T>(o.z * f, o.w * f)};
+  if (a.lse && threadIdx.x == 0) a.lse[row] = lse_of(top, sum, a.scale_log2, T::kHeadroom);
 }
 
-template <typename T, int D, int WAVES>
+template <typename T, int D, bool FEW>
 hipError_t launch_shape(const PromptKernelArgs &a, hipStream_t stream) {
+  typedef Shape<T, D, FEW> S;
   const unsigned blocks = (unsigned)((int64_t)a.num_seqs * a.kv_heads * a.row_blocks);
-  constexpr size_t lds = 4 * Tile<D>::kBytes;
-  hipLaunchKernelGGL((prompt_kernel<T, D, WAVES>), dim3(blocks, a.splits), dim3(64 * WAVES), lds, stream, a);
+  hipLaunchKernelGGL((prompt_kernel<T, D, FEW>), dim3(blocks, a.splits), dim3(64 * S::kWaves), S::kLds, stream, a);
   if (a.splits > 1) {
     const int64_t rows = (int64_t)a.max_q * a.kv_heads * a.share;
-    hipLaunchKernelGGL((prompt_join_kernel<T, D>), dim3((unsigned)((rows + 3) / 4), a.num_seqs), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((prompt_join_kernel<T, D>), dim3((unsigned)rows, a.num_seqs), dim3(kJoinThreads), 0, stream, a);
   }
   return hipGetLastError();
 }
 
 template <typename T, int D>
 hipError_t launch_dim(const PromptKernelArgs &a, const PromptPlan &p, hipStream_t stream) {
-  return p.waves == 1 ? launch_shape<T, D, 1>(a, stream) : launch_shape<T, D, 4>(a, stream);
+  return p.few ? launch_shape<T, D, true>(a, stream) : launch_shape<T, D, false>(a, stream);
 }
 
 template <typename T>

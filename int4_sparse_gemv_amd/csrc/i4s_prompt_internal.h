@@ -79,26 +79,29 @@ hipError_t launch_mx_product(const MxProductKernelArgs &a, const MxProductPlan &
 // ---------------------------------------------------------------------------
 // attention of whole prompts (i4s_prompt_attention.hip)
 
-// Launch shape: `waves` waves of 32 query rows (tokens x query heads of one KV
-// head) a block, row_blocks blocks a sequence and KV head, the keys in
-// `splits` pieces of `chunk` keys (the last takes what is left).
+// Launch shape: blocks of 128 query rows (tokens x query heads of one KV head),
+// or, `few`, of up to 32 that a sequence and KV head has in all, row_blocks such
+// blocks a sequence and KV head, the keys in `splits` pieces of `chunk` keys (the
+// last takes what is left).
 struct PromptPlan {
-  int32_t waves;
+  bool few;
   int32_t row_blocks;
+  int32_t group;  // pairs of sequence and KV head that run together
   int32_t splits, chunk;
   uint64_t workspace_bytes;
 };
 PromptPlan prompt_plan(const i4s_prompt_args &a);
 
 constexpr int kPromptRows = 32;  // query rows of a wave
-constexpr int kPromptKeys = 64;  // keys of a step
+constexpr int kMaxPromptSplits = 512;
+constexpr int kPromptKeys = 64;  // pieces of the keys are multiples of it
 
 struct PromptKernelArgs {
   const void *q, *k, *v;
   int64_t q_token, q_head, k_token, k_head, v_token, v_head;  // strides in elements
   int32_t kv_heads, share;
   int32_t num_tokens, num_keys, num_seqs, max_q, causal;
-  int32_t row_blocks, splits, chunk;
+  int32_t row_blocks, group, splits, chunk;
   float scale_log2;
   const int32_t *q_start, *k_start;
   void *out;
