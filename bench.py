@@ -86,6 +86,9 @@ def parse():
                     help="time one 7B-shaped layer's verification step at this many candidate tokens (1-16): the packed "
                          "products, the 4-bit cache and its attention, and the scores of a 32000-word vocabulary")
     ap.add_argument("--context", type=int, default=2000, help="with --verify-step: tokens held before the candidates")
+    ap.add_argument("--prompt-step", type=int, default=None, metavar="TOKENS",
+                    help="time one 7B-shaped layer's step over a whole prompt of this many tokens (1-65536): the microscaled "
+                         "4-bit products, attention over the prompt, the 4-bit cache, and the last token's scores")
     ap.add_argument("--stack", default=None,
                     help="instead of the headline: one 7B stack (c4_stack7b or x2_mix_stack7b), per pass and per layer")
     ap.add_argument("--summarize-rocprof", nargs=2, metavar=("DIR", "OUT"), default=None,
@@ -94,6 +97,8 @@ def parse():
     args = ap.parse_args()
     if args.verify_step is not None and not 1 <= args.verify_step <= 16:
         ap.error("--verify-step takes 1 to 16 candidate tokens, the batches of the packed products")
+    if args.prompt_step is not None and not 1 <= args.prompt_step <= 65536:
+        ap.error("--prompt-step takes 1 to 65536 tokens")
     if args.context < 0:
         ap.error("--context takes 0 or more tokens")
     return args
@@ -502,6 +507,31 @@ class VerifyStep:
         return a, y, self.score(y)
 
 
+def graph_us(torch, trials, f, order):
+    """f(i) for each i of order in one graph, us each: the best of some trials."""
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        f(0)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in order:
+            f(i)
+    best = None
+    for _ in range(trials):
+        b, e = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        graph.replay()
+        b.record()
+        for _ in range(5):
+            graph.replay()
+        e.record()
+        e.synchronize()
+        us = b.elapsed_time(e) * 1e3 / 5 / len(order)
+        best = us if best is None else min(best, us)
+    return round(best, 2)
+
+
 VERIFY_COPIES = 64  # of a layer: 8 GB, and over 0.5 GB of every part but extend and append, past every cache
 
 
@@ -519,28 +549,6 @@ def verify_step(R, args):
         a = s.attend(q, r)
         held.append((q, k, v, r, a, s.mlp(a)))
 
-    def timed(f, order):
-        side = torch.cuda.Stream()
-        side.wait_stream(torch.cuda.current_stream())
-        with torch.cuda.stream(side):
-            f(0)
-        torch.cuda.current_stream().wait_stream(side)
-        graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(graph):
-            for i in order:
-                f(i)
-        best = None
-        for _ in range(args.trials):
-            b, e = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-            graph.replay()
-            b.record()
-            for _ in range(5):
-                graph.replay()
-            e.record()
-            e.synchronize()
-            us = b.elapsed_time(e) * 1e3 / 5 / len(order)
-            best = us if best is None else min(best, us)
-        return round(best, 2)
     parts = {"step": lambda i: steps[i].run(), "qkv": lambda i: steps[i].project(), "kv_extend": lambda i: steps[i].extend(),
              "kv_append": lambda i: steps[i].append(held[i][1], held[i][2], held[i][3]),
              "kv_attention": lambda i: steps[i].attend(held[i][0], held[i][3]),
@@ -548,9 +556,97 @@ def verify_step(R, args):
     out = {"workload": "verify_step_7b_layer", "tokens": args.verify_step, "context": args.context, "data": "synthetic",
            "layers": len(steps), "cold_us": {}, "hot_us": {}}
     for n, f in parts.items():
-        out["cold_us"][n] = timed(f, range(len(steps)))
-        out["hot_us"][n] = timed(f, [0] * 10)
+        out["cold_us"][n] = graph_us(torch, args.trials, f, range(len(steps)))
+        out["hot_us"][n] = graph_us(torch, args.trials, f, [0] * 10)
         say(f"verify step: {n} cold {out['cold_us'][n]} us, hot {out['hot_us'][n]} us")
+    return out
+
+
+class PromptStep:
+    """One layer of a 7B-shaped decoder over a whole prompt, and the scores
+    after it: products in the microscaled 4-bit format, attention over the
+    prompt's own keys and values, and those into the 4-bit cache, from where
+    decoding goes on.  (Norms, rotary positions, the gate's activation and the
+    residual sums are the caller's and not part of this library.)  Inputs are
+    synthetic; ``lengths`` are the tokens of each request."""
+
+    HEADS, HIDDEN, MLP, VOCAB, PAGE = 32, 4096, 11008, 32000, 16
+
+    def __init__(self, I, lengths, seed=0, device="cuda", hidden=None, heads=None, kv_heads=None, mlp=None, vocab=None):
+        import torch
+        self.torch, self.I, self.lengths, self.tokens = torch, I, list(lengths), sum(lengths)
+        h, n, m, v = hidden or self.HIDDEN, heads or self.HEADS, mlp or self.MLP, vocab or self.VOCAB
+        self.heads, self.kv_heads, self.dim = n, kv_heads or n, h // n
+        g = torch.Generator(device=device)
+        g.manual_seed(seed)
+
+        def layer(rows, cols):
+            return I.mx_quantize((cols ** -0.5 * torch.randn(rows, cols, generator=g, device=device)).half())
+        self.qkv, self.o = layer((n + 2 * self.kv_heads) * self.dim, h), layer(h, h)
+        self.gate_up, self.down, self.head = layer(2 * m, h), layer(h, m), layer(v, h)
+        i32 = dict(dtype=torch.int32, device=device)
+        width = -(-max(lengths) // self.PAGE) + 1
+        pages = width * len(lengths)
+        self.cache = I.kv_cache(pages, self.PAGE, self.kv_heads, self.dim, min(64, self.dim), device)
+        self.table, self.lens = torch.full((len(lengths), width), -1, **i32), torch.zeros(len(lengths), **i32)
+        self.free, self.count = torch.randperm(pages, generator=g, **i32), torch.full((1,), pages, **i32)
+        self.new = torch.tensor(lengths, **i32)
+        self.last = torch.tensor(lengths, device=device).cumsum(0) - 1
+        self.x = torch.randn(self.tokens, h, generator=g, device=device).half()
+        self.given = torch.randint(v, (len(lengths),), generator=g, device=device)
+
+    def project(self, x=None):
+        y = self.I.mx_product(self.x if x is None else x, self.qkv)
+        return y.unflatten(1, (-1, self.dim)).split((self.heads, self.kv_heads, self.kv_heads), 1)
+
+    def extend(self):
+        return self.I.kv_extend(self.table, self.lens, self.new, self.free, self.count, self.PAGE, self.tokens)
+
+    def append(self, k, v, r):
+        self.I.kv_append(self.cache, k, v, r.slots)
+
+    def attend(self, q, k, v, r):
+        return self.I.prompt_attention(q, k, v, r.q_start, max_q=max(self.lengths), max_k=max(self.lengths)).flatten(1)
+
+    def mlp(self, a):
+        I = self.I
+        gate, up = I.mx_product(I.mx_product(a, self.o), self.gate_up).chunk(2, 1)
+        return I.mx_product(gate * up, self.down)
+
+    def score(self, y):
+        return self.I.token_logprobs(self.I.mx_product(y, self.head), self.given, top_k=8)
+
+    def run(self):
+        q, k, v = self.project()
+        r = self.extend()
+        self.append(k, v, r)
+        a = self.attend(q, k, v, r)
+        y = self.mlp(a)
+        return a, y, self.score(y[self.last])
+
+
+PROMPT_COPIES = 6  # of a layer: 0.65 GB of weights, past every cache
+
+
+def prompt_step(R, args):
+    """The step in a graph, whole and in its parts, us each: as in a model of
+    many layers, where each step finds another layer's weights."""
+    torch = R.torch
+    steps = [PromptStep(R.I, [args.prompt_step], seed) for seed in range(PROMPT_COPIES)]
+    say(f"prompt step: {len(steps)} layers made")
+    held = []
+    for s in steps:
+        q, k, v = s.project()
+        r = s.extend()
+        a = s.attend(q, k, v, r)
+        held.append((q, k, v, r, a, s.mlp(a)[s.last]))
+    parts = {"step": lambda i: steps[i].run(), "qkv": lambda i: steps[i].project(), "kv_extend": lambda i: steps[i].extend(),
+             "kv_append": lambda i: steps[i].append(*held[i][1:4]), "prompt_attention": lambda i: steps[i].attend(*held[i][:4]),
+             "o_gate_up_down": lambda i: steps[i].mlp(held[i][4]), "head_and_scores": lambda i: steps[i].score(held[i][5])}
+    out = {"workload": "prompt_step_7b_layer", "tokens": args.prompt_step, "data": "synthetic", "layers": len(steps), "us": {}}
+    for n, f in parts.items():
+        out["us"][n] = graph_us(torch, args.trials, f, range(len(steps)))
+        say(f"prompt step: {n} {out['us'][n]} us")
     return out
 
 
@@ -627,6 +723,9 @@ def main():
         return
     if args.verify_step is not None:
         print(json.dumps(verify_step(R, args)), flush=True)
+        return
+    if args.prompt_step is not None:
+        print(json.dumps(prompt_step(R, args)), flush=True)
         return
     if args.stack:
         items = R.stack_items(args.stack)

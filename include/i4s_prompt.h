@@ -105,7 +105,7 @@ typedef struct i4s_mx_product_args {
  * Errors: I4S_ERR_INVALID_ARGUMENT. */
 i4s_status i4s_mx_product_workspace_size(const i4s_mx_product_args *a /* host */, uint64_t *bytes /* host */);
 
-/* The call.  One to three kernel launches; results do not depend on the order
+/* The call.  One or two kernel launches; results do not depend on the order
  * of blocks.  Calls that share a workspace must not overlap.  y and the
  * workspace must not overlap one another or an input.  Columns of y between
  * rows and y_stride are left as they were.
@@ -144,10 +144,9 @@ typedef struct i4s_prompt_args {
   int32_t num_keys;          /* rows of k and v, 0 .. 2^30                   */
   int32_t num_seqs;          /* 0 .. 65535                                   */
   int32_t max_q;             /* largest number of query tokens of a          */
-                             /* sequence, 1 .. 2^23; times q_heads below     */
-                             /* 2^23, and num_seqs * kv_heads times its      */
-                             /* blocks of 128 rows (tokens x query heads of  */
-                             /* a KV head) below 2^23                        */
+                             /* sequence, 1 .. 2^24; num_seqs * kv_heads     */
+                             /* times its blocks of 128 rows (tokens x query */
+                             /* heads of a KV head) below 2^23               */
   int32_t max_k;             /* largest number of keys of a sequence (0:     */
                              /* num_keys); sizes the launch                  */
   int32_t causal;            /* 0 or 1                                       */

@@ -14,7 +14,6 @@ typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
 // 4-bit codes.  v_cvt_scalef32_pk_fp4 divides by a power of two, rounds to
 // nearest even and saturates.
 struct HalfX {
-  typedef h2_t pair;
   static __device__ float to_float(uint32_t bits) { return fp16_bits_to_float(bits); }
   static constexpr uint32_t kInf = 0x7C00u;
   template <int B>

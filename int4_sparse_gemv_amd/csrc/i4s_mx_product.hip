@@ -260,9 +260,6 @@ __global__ __launch_bounds__(64 * WR *WC, 2) void mx_tile_kernel(MxProductKernel
   const int row_tiles = mx_row_tiles(a.rows), token_tiles = mx_row_tiles(a.tokens);
   const Place place = place_of(blockIdx.x, (row_tiles + S::kA - 1) / S::kA, (token_tiles + S::kB - 1) / S::kB);
   const int row0 = place.row * S::kA, token0 = place.token * S::kB;
-  // this block's groups
-  const int g0 = (int)((int64_t)groups_all * blockIdx.y / gridDim.y);
-  const int g1 = (int)((int64_t)groups_all * (blockIdx.y + 1) / gridDim.y);
   const int last = all - 1;
 
   // the tiles that this wave brings
@@ -320,7 +317,7 @@ __global__ __launch_bounds__(64 * WR *WC, 2) void mx_tile_kernel(MxProductKernel
     for (int n = 0; n < NT; ++n) acc[r][n] = f4_t{0, 0, 0, 0};
 
   auto run = [&](auto step) {
-    for (int g = g0; g < g1; ++g) {
+    for (int g = 0; g < groups_all; ++g) {
       step(4 * g, std::integral_constant<int, 0>());
       step(4 * g + 1, std::integral_constant<int, 1>());
       if (4 * g + 2 < all) {
@@ -347,16 +344,16 @@ __global__ __launch_bounds__(64 * WR *WC, 2) void mx_tile_kernel(MxProductKernel
 #pragma unroll
       for (int n = 0; n < NT; ++n) pb[n] = load4(p + (S::kA + wc * NT + n) * kMxGroupBytes);
     };
-    load_scales(g0);
+    load_scales(0);
 #pragma unroll
-    for (int i = 0; i < kRing; ++i) load_step(4 * g0 + i);
+    for (int i = 0; i < kRing; ++i) load_step(i);
     wait_loads<(kRing - 1) * S::kLoads>();
     meet();
-    read_scales(sa, sb, g0);
+    read_scales(sa, sb, 0);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) read_b(0, 4 * g0, n);
+    for (int n = 0; n < NT; ++n) read_b(0, 0, n);
 #pragma unroll
-    for (int r = 0; r < RT; ++r) read_a(0, 4 * g0, r);
+    for (int r = 0; r < RT; ++r) read_a(0, 0, r);
     run([&](int s, auto C) {
       constexpr int c = decltype(C)::value, set = c & 1;
       // two more steps (and scales) are on their way behind the next one
@@ -382,9 +379,9 @@ __global__ __launch_bounds__(64 * WR *WC, 2) void mx_tile_kernel(MxProductKernel
       }
     });
   } else {
-    load_scales(g0);
+    load_scales(0);
 #pragma unroll
-    for (int i = 0; i < kRing - 1; ++i) load_step(4 * g0 + i);
+    for (int i = 0; i < kRing - 1; ++i) load_step(i);
     uint32_t sa[RT], sb[NT];
     run([&](int s, auto C) {
       constexpr int c = decltype(C)::value;
@@ -420,7 +417,7 @@ __global__ __launch_bounds__(64 * WR *WC, 2) void mx_tile_kernel(MxProductKernel
   typedef typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type W;
   constexpr int kMany = 16 / sizeof(T), kTiles = kMany / 4;
   const int64_t row_at = (int64_t)(row0 + wr * RT) * 16 + lane / 16 * kMany, token_at = (int64_t)(token0 + wc * NT) * 16 + lane % 16;
-  T *const to = static_cast<T *>(a.y) + ((int64_t)blockIdx.y * a.tokens + token_at) * a.y_stride + row_at;
+  T *const to = static_cast<T *>(a.y) + token_at * a.y_stride + row_at;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll

@@ -100,16 +100,13 @@ i4s_status check_prompt(const i4s_prompt_args *a) {
     return fail(I4S_ERR_INVALID_ARGUMENT, "num_tokens=%d and num_keys=%d must be in [0, 2^30]", a->num_tokens, a->num_keys);
   if (a->num_seqs < 0 || a->num_seqs > 65535)
     return fail(I4S_ERR_INVALID_ARGUMENT, "num_seqs=%d must be in [0, 65535]", a->num_seqs);
-  if (a->max_q < 1 || a->max_q > 1 << 23)
-    return fail(I4S_ERR_INVALID_ARGUMENT, "max_q=%d must be in [1, 2^23]", a->max_q);
+  if (a->max_q < 1 || a->max_q > 1 << 24)
+    return fail(I4S_ERR_INVALID_ARGUMENT, "max_q=%d must be in [1, 2^24]", a->max_q);
   if (a->max_k < 0) return fail(I4S_ERR_INVALID_ARGUMENT, "max_k=%d must be 0 or more", a->max_k);
   if (a->causal != 0 && a->causal != 1) return fail(I4S_ERR_INVALID_ARGUMENT, "causal=%d must be 0 or 1", a->causal);
   if (!(a->scale > 0.0f) || !std::isfinite(a->scale))
     return fail(I4S_ERR_INVALID_ARGUMENT, "scale=%g must be positive and finite", (double)a->scale);
   if (a->reserved) return fail(I4S_ERR_INVALID_ARGUMENT, "reserved=%d must be 0", a->reserved);
-  // a block of the second launch takes one row
-  if ((int64_t)a->max_q * a->q_heads > kMaxBlocks)
-    return fail(I4S_ERR_INVALID_ARGUMENT, "max_q=%d times q_heads=%d must be below 2^23", a->max_q, a->q_heads);
   const int64_t rows = (int64_t)a->max_q * (a->q_heads / a->kv_heads);
   const int64_t blocks = (rows + 127) / 128 * a->kv_heads * (a->num_seqs > 0 ? a->num_seqs : 1);
   if (blocks > kMaxBlocks)
@@ -143,15 +140,17 @@ MxProductPlan mx_product_plan(int32_t tokens, int32_t rows, int32_t cols, bool x
   p.quantize = !x_given && (tokens > 16 || (int64_t)tokens * cols >= 1 << 16);
   p.token_tiles = (tokens + 15) / 16;
   // Blocks of eight waves and 1, 2 or (where each quantizes the tokens) 4 weight
-  // tiles, about one for each of the 256 compute units; beyond, four waves and 2.
+  // tiles, about one or two for each of the 256 compute units; beyond, and for
+  // more than 16 tokens sooner, four waves and 2.  Waves decide the order of the
+  // sums and so must not depend on how the tokens are given.
   // Us, 16 quantized tokens, tiles x waves 1x8 / 2x8 / 2x4: 4096 x 4096 3.7 / 4.1 / 4.3;
   // 5120 x 13824 11.9 / 10.6 / 10.8; 13824 x 5120 10.5 / 9.8 / 9.7, 64 tokens 21.4 / 17.8
   // / 13.5; 50257 x 4096, 48 tokens 45 / 42 / 30.  8 tokens quantized on the way,
   // 2x8 / 4x8 / 2x4: 13824 x 5120 14.5 / 10.9 / 12.8; 50257 x 4096 32 / 31 / 26.
   const int32_t tiles = mx_row_tiles(rows);
   p.row_tiles = tiles <= 256 ? 1 : 2;
-  p.waves = tiles <= 512 ? 8 : 4;
-  if (!x_given && !p.quantize && tiles > 512 && tiles <= 1024) p.row_tiles = 4, p.waves = 8;
+  p.waves = tiles <= (p.token_tiles == 1 ? 1024 : 512) ? 8 : 4;
+  if (!x_given && !p.quantize && tiles > 512 && p.waves == 8) p.row_tiles = 4;
   // Few tokens' blocks (more than 64 tokens: several of them, 2x4) while they fill
   // the chip better than 128 x 128 outputs.  Us, few / 128 x 128: 4096 x 4096: 128 tokens
   // 6.8 / 11.5, 256: 8.9 / 11.7, 384: 12.1 / 12; 5120 x 13824: 128: 20 / 31, 256: 29 / 31;
@@ -164,7 +163,6 @@ MxProductPlan mx_product_plan(int32_t tokens, int32_t rows, int32_t cols, bool x
   // 4096 x 5120 x 13824 197 / 147 (1.25 of 2); 2048 x 4096 x 4096 34 / 23 (half of one).
   const int64_t large = ((int64_t)tokens + 255) / 256 * (((int64_t)rows + 255) / 256);
   p.tile = 10 * large >= 9 * ((large + 255) / 256 * 256) ? 256 : 128;
-  p.splits = 1;
   if (p.quantize) {
     p.x_vals = mx_vals_bytes(tokens, cols);
     p.x_scales = mx_scales_bytes(tokens, cols);
@@ -317,7 +315,6 @@ i4s_status i4s_mx_product(const i4s_mx_product_args *a, void *stream) {
   } else {
     k.x = a->x_values, k.x_stride = a->x_stride, k.x_dtype = a->x_dtype;
   }
-  k.partial = reinterpret_cast<float *>(ws + p.x_vals + p.x_scales);
   const hipError_t e = i4s::launch_mx_product(k, p, a->y_dtype, reinterpret_cast<hipStream_t>(stream));
   return e == hipSuccess ? I4S_OK : device_error(e, "mx_product launch");
 }

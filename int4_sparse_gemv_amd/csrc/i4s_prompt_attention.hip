@@ -21,8 +21,8 @@
 // by 8 powers of two, so O is scaled rarely.
 //
 // Roundings: scores, sums and outputs are fp32.  A probability is rounded to
-// the values' type for its matrix instruction (relative 2^-9 for bf16, 2^-12
-// for fp16), the sum takes it unrounded; the output is rounded once.
+// the values' type for its matrix instruction (at most 2^-8 of itself for
+// bf16, 2^-11 for fp16), the sum takes it unrounded; the output is rounded once.
 //
 // Long prompts are bound by the matrix cores and the power they may take: 8191
 // tokens, 40 heads of 128, causal, 725 us = 0.95 PFLOP/s with the masked halves

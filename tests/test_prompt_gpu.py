@@ -18,12 +18,11 @@ least: 2^-32 of it), sums over n keys by n 2^-24, and so is the running
 rescaling, once a step of 32 keys: (n + 8) 2^-23 covers both.
 """
 
-import itertools
-
 import numpy as np
 import pytest
 
 from oracle import prompt_oracle as O
+from oracle import serve_oracle as S
 
 pytestmark = pytest.mark.gpu
 
@@ -182,7 +181,8 @@ def check_product(i4s, x, w, y, dtype):
 
 SIZES = [(1, 16, 32), (1, 4096, 4096), (2, 33, 96), (5, 1000, 512), (15, 77, 1056), (16, 256, 4096), (17, 100, 288),
          (31, 513, 768), (33, 48, 1024), (50, 300, 2080), (64, 129, 512), (65, 127, 256), (65, 1, 64), (100, 257, 544),
-         (128, 128, 128), (129, 400, 1312), (257, 640, 992), (300, 31, 4096), (511, 513, 800)]
+         (128, 128, 128), (129, 400, 1312), (257, 640, 992), (300, 31, 4096), (511, 513, 800), (3, 8300, 512), (15, 16400, 224),
+         (16, 9000, 4096)]
 
 
 @pytest.mark.parametrize("tokens,rows,cols", SIZES)
@@ -200,7 +200,8 @@ def test_product(i4s, tokens, rows, cols, dtype):
     assert torch.equal(i4s.mx_product(xq, w, dtype=F32), y)     # and again
 
 
-@pytest.mark.parametrize("tokens,rows,cols", [(4096, 4096, 1024), (2049, 8200, 544)])
+@pytest.mark.parametrize("tokens,rows,cols", [(4096, 4096, 1024), (2049, 8200, 544), (1100, 1501, 288), (1023, 1399, 1312),
+                                              (3897, 3801, 288), (3900, 3900, 96)])
 def test_product_many(i4s, tokens, rows, cols):
     """The largest blocks, whole and ragged."""
     say("product", tokens, rows, cols)
@@ -224,6 +225,54 @@ def test_product_strides(i4s, tokens):
     keep = buf.clone()
     keep[:tokens, 9:92] = 7.0
     assert (keep == 7.0).all()
+
+
+@pytest.mark.parametrize("tokens,rows,wide", [(1100, 1501, 1511), (3897, 3801, 3805)])
+@pytest.mark.parametrize("dtype", [F16, F32])
+def test_product_many_at_odd_places(i4s, tokens, rows, wide, dtype):
+    """Outputs of the largest blocks at odd offsets and strides: the same values, and what lies between stays."""
+    rng = np.random.default_rng(rows)
+    x, w = (i4s.mx_quantize(draw(rng, n, 160, F16, 0.3)) for n in (tokens, rows))
+    buf = torch.full((tokens, wide), 7.0, dtype=dtype, device="cuda")
+    y = i4s.mx_product(x, w, out=buf[:, 3:3 + rows])
+    assert torch.equal(y, i4s.mx_product(x, w, dtype=dtype))
+    assert (buf[:, :3] == 7.0).all() and (buf[:, 3 + rows:] == 7.0).all()
+
+
+@pytest.mark.parametrize("tokens,rows", [(3, 40), (40, 300), (1100, 1501), (3900, 3900)])
+def test_product_with_a_block_that_is_not_finite(i4s, tokens, rows):
+    """Its token, or its weight row, gets NaN; nothing else changes."""
+    rng = np.random.default_rng(tokens)
+    x, w = draw(rng, tokens, 96, F16, 0.3), draw(rng, rows, 96, F16, 0.3)
+    x[0, 5], x[tokens - 1, 95], w[rows - 2, 40] = float("nan"), float("inf"), float("-inf")
+    xc, wc = x.clone(), w.clone()
+    xc[0, 5], xc[tokens - 1, 95], wc[rows - 2, 40] = 0, 0, 0
+    y = i4s.mx_product(x, i4s.mx_quantize(w), dtype=F32)
+    want = i4s.mx_product(xc, i4s.mx_quantize(wc), dtype=F32)
+    want[0], want[tokens - 1], want[:, rows - 2] = float("nan"), float("nan"), float("nan")
+    assert torch.equal(y.isnan(), want.isnan()) and torch.equal(y.nan_to_num(3.0), want.nan_to_num(3.0))
+
+
+def test_product_long_offsets(i4s):
+    """A weight past 4 GB, and tokens and outputs whose strides pass it."""
+    say("long offsets")
+    rows, cols = 1 << 17, 65568
+    sizes = ((rows // 16, 2 * -(-cols // 256), 1024), (rows // 16, -(-cols // 512), 256))
+    w = i4s.MXTensor(rows, cols, torch.randint(256, sizes[0], dtype=torch.uint8, device="cuda"),
+                     torch.full(sizes[1], 120, dtype=torch.uint8, device="cuda"))
+    assert w.vals.numel() > 1 << 32
+    w.vals[:, -1], w.scales[:, -1] = 0, 0  # past the columns
+    w.vals[:, 512, 256:], w.scales[:, 128] = 0, 0
+    w.scales[:, 128, 0:64:4] = 120  # the last block of 32
+    rng = np.random.default_rng(1)
+    for tokens in (3, 80, 300):
+        x, out = (torch.empty(tokens, 1 << 24, dtype=F16, device="cuda")[:, 64:64 + n] for n in (cols, rows))
+        x.copy_(draw(rng, tokens, cols, F16, 0.2))
+        i4s.mx_product(x, w, out=out)
+        # the last tiles by themselves
+        tail = i4s.MXTensor(48, cols, w.vals[-3:].clone(), w.scales[-3:].clone())
+        check_product(i4s, i4s.mx_quantize(x), tail, out[:, -48:], F16)
+        del x, out
 
 
 # ---------------------------------------------------------------------------
@@ -398,3 +447,178 @@ def test_attention_without_tokens_or_keys(i4s):
     lse = torch.zeros(3, 2, device="cuda")
     out = i4s.prompt_attention(z(3, 2) + 1, z(0, 1), z(0, 1), lse=lse)
     assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, F16), (128, BF16)])
+def test_attention_of_many_pairs(i4s, dim, dtype):
+    """More pairs of sequence and KV head than run together, rows of very different lengths among them."""
+    say("pairs", dim, dtype)
+    rng = np.random.default_rng(dim)
+    lengths = [(610, 610)] + [(n, n) for n in (1, 40, 33, 128, 129, 7, 64, 65, 2)] + [(30, 300)]
+    q, k, v, starts = packed(rng, lengths, 8, 4, dim, dtype)
+    out = i4s.prompt_attention(q, k, v, *starts, max_q=610, max_k=610)
+    check_attention(q, k, v, starts, out, None, True, dim ** -0.5, dtype)
+
+
+@pytest.mark.parametrize("max_k", [0, 1, 1000, 3001])
+@pytest.mark.parametrize("tokens", [1, 20, 100])
+def test_attention_split_over_blocks(i4s, tokens, max_k):
+    """Long keys in pieces, and a largest length that is not given, or too small: the same within the tolerance."""
+    rng = np.random.default_rng(tokens)
+    q, k, v, starts = packed(rng, [(tokens, 3001), (tokens, tokens), (2, 0)], 1, 2, 128, F16)
+    for causal in (True, False):
+        lse = torch.empty(q.shape[:2], device="cuda")
+        out = i4s.prompt_attention(q, k, v, *starts, max_q=max(tokens, 2), max_k=max_k, causal=causal, lse=lse)
+        check_attention(q, k, v, starts, out, lse, causal, 128 ** -0.5, F16)
+
+
+def test_attention_long_offsets(i4s):
+    """Keys, values and queries whose strides pass 4 GB."""
+    say("long offsets")
+    rng = np.random.default_rng(8)
+    q, k, v, starts = packed(rng, [(5, 5), (290, 290)], 1, 2, 64, BF16)
+    step = 1 << 23
+    big = torch.empty(295, step, dtype=BF16, device="cuda")
+    far = [big[:, at:at + n * 64].unflatten(1, (n, 64)) for at, n in ((0, 2), (step // 2, 1), (step - 64, 1))]
+    for a, b in zip(far, (q, k, v)):
+        a.copy_(b)
+    assert big.numel() * 2 > 1 << 32
+    out = i4s.prompt_attention(*far, *starts, max_q=290, max_k=290)
+    assert torch.equal(out, i4s.prompt_attention(q, k, v, *starts, max_q=290, max_k=290))
+    check_attention(q, k, v, starts, out, None, True, 64 ** -0.5, BF16)
+    token = i4s.prompt_attention(far[0][-1:], far[1], far[2])
+    want = [torch.tensor(x, dtype=torch.int32) for x in ([0, 1], [0, 295])]
+    check_attention(q[-1:], k, v, want, token, None, True, 64 ** -0.5, BF16)
+
+
+# ---------------------------------------------------------------------------
+# calls together
+
+
+def prompt_step(i4s, lengths, seed=0):
+    import bench
+    return bench.PromptStep(i4s, lengths, seed=seed, hidden=512, heads=8, kv_heads=2, mlp=1408, vocab=1000)
+
+
+def test_prompt_step_then_a_decode_step(i4s):
+    """The step that ``bench.py --prompt-step`` times, on a small layer and three requests, each part against the oracle on
+    its own inputs; then each request's next token over the cache that the prompts left."""
+    say("prompt step")
+    s = prompt_step(i4s, [70, 1, 33])
+    a, y, scores = s.run()
+    torch.cuda.synchronize()
+    q, k, v = s.project()
+    check_product(i4s, i4s.mx_quantize(s.x), s.qkv, torch.cat([t.flatten(1) for t in (q, k, v)], 1), F16)
+    r = s.extend()
+    assert int(r.flags) == 0 and r.q_start.tolist() == [0, 70, 71, 104]
+    starts = [r.q_start.cpu()] * 2
+    check_attention(q, k, v, starts, a.unflatten(1, (8, 64)), None, True, 0.125, F16)
+    gate_up = i4s.mx_product(i4s.mx_product(a, s.o), s.gate_up)
+    check_product(i4s, i4s.mx_quantize(i4s.mx_product(a, s.o)), s.gate_up, gate_up, F16)
+    check_product(i4s, i4s.mx_quantize(gate_up[:, :1408] * gate_up[:, 1408:]), s.down, y, F16)
+    logits = i4s.mx_product(y[[69, 70, 103]], s.head)
+    lp, ent, ids, top = S.token_logprobs(f64(logits), s.given.cpu().numpy(), 8)
+    np.testing.assert_array_equal(scores.top_ids.cpu().numpy(), ids)
+    np.testing.assert_allclose(f64(scores.logprobs), lp, rtol=2.0**-20)  # sums of 1000 terms
+    # the cache holds what the attention read, in 4 bits
+    keys, values = i4s.kv_read(s.cache, r.slots, dtype=F32)
+    for got, x in ((keys, k), (values, v)):
+        n, f = S.quantize(f64(x), 64)
+        np.testing.assert_array_equal(f64(got), n * f.repeat(64, -1))
+    # the next token of each
+    new = torch.ones(3, dtype=torch.int32, device="cuda")
+    q, k, v = s.project(s.x[:3])
+    n = i4s.kv_extend(s.table, r.lens, new, s.free, r.free_count, s.PAGE, 3)
+    assert int(n.flags) == 0 and n.lens.tolist() == [71, 2, 34]
+    i4s.kv_append(s.cache, k, v, n.slots)
+    out = i4s.kv_attention(s.cache, q, s.table, n.lens, q_start=n.q_start, max_q=1)
+    slots = r.slots.tolist()
+    for i, (b, e) in enumerate(((0, 70), (70, 71), (71, 104))):
+        held = torch.tensor(slots[b:e] + [n.slots.tolist()[i]], dtype=torch.int32).cuda()
+        keys, values = i4s.kv_read(s.cache, held, dtype=F32)
+        want, _, spread = S.attention(f64(q[i:i + 1]), f64(keys), f64(values), e - b, 0.125)
+        assert (np.abs(f64(out[i:i + 1]) - want) <= half_step(F16) * np.abs(want) + 2.0**-10 * spread).all()
+
+
+def test_captured_steps_replay(i4s):
+    """Two steps in two graphs, replayed in turn with other inputs and eager work in between, against the eager calls."""
+    say("captured")
+    steps = [prompt_step(i4s, lengths, seed) for seed, lengths in ((1, [300, 20]), (2, [1, 17, 600]))]
+    # and a token behind long keys, whose call has a workspace
+    q, k, v = (torch.randn(n, h, 128, device="cuda").half() for n, h in ((1, 4), (5000, 1), (5000, 1)))
+    graphs, outs = [], []
+    for s in steps:
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            s.run(), i4s.prompt_attention(q, k, v)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append((*s.run()[:2], i4s.prompt_attention(q, k, v)))
+        graphs.append(graph)
+    for turn in range(4):
+        for s in steps:
+            s.x.normal_()
+        q.normal_(), k.normal_()
+        want = [[t.clone() for t in (*s.run()[:2], i4s.prompt_attention(q, k, v))] for s in steps]
+        for graph in graphs:
+            graph.replay()
+        torch.randn(1000, device="cuda").sum()
+        torch.cuda.synchronize()
+        for w, o in zip(want, outs):
+            assert all(torch.equal(a, b) for a, b in zip(w, o)), turn
+
+
+def test_two_streams_at_once(i4s):
+    """Calls with workspaces on two streams at the same time."""
+    say("two streams")
+    torch.manual_seed(3)
+    qs = [torch.randn(1, 4, 128, device="cuda").half() for _ in range(2)]
+    k, v = (torch.randn(6000, 1, 128, device="cuda").half() for _ in range(2))
+    xs = [torch.randn(200, 1024, device="cuda").half() for _ in range(2)]
+    w = i4s.mx_quantize(torch.randn(1000, 1024, device="cuda").half())
+    want = [(i4s.prompt_attention(q, k, v), i4s.mx_product(x, w)) for q, x in zip(qs, xs)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for s, q, x, g in zip(streams, qs, xs, got):
+            with torch.cuda.stream(s):
+                g.append((i4s.prompt_attention(q, k, v), i4s.mx_product(x, w)))
+    torch.cuda.synchronize()
+    for (a, y), g in zip(want, got):
+        assert all(torch.equal(a, b) and torch.equal(y, z) for b, z in g)
+
+
+def test_python_refusals(i4s):
+    x, w = torch.zeros(3, 64, dtype=F16, device="cuda"), i4s.mx_quantize(torch.zeros(20, 64, dtype=F16, device="cuda"))
+    q = torch.zeros(5, 4, 64, dtype=F16, device="cuda")
+    k = q[:, :2]
+    i32 = lambda *s: torch.tensor(s, dtype=torch.int32).cuda()  # noqa: E731
+    for call in (lambda: i4s.mx_quantize(x.float()), lambda: i4s.mx_quantize(x.cpu()), lambda: i4s.mx_quantize(x[0]),
+                 lambda: i4s.mx_quantize(x[:, ::2]), lambda: i4s.mx_quantize(x, out=w), lambda: i4s.mx_read(w, torch.int8),
+                 lambda: i4s.mx_product(x.float(), w), lambda: i4s.mx_product(x[:, :32], w), lambda: i4s.mx_product(x.cpu(), w),
+                 lambda: i4s.mx_product(x, w, dtype=torch.int32), lambda: i4s.mx_product(x, w, out=x),
+                 lambda: i4s.mx_product(x, w, out=torch.zeros(20, 3, dtype=F16, device="cuda").t()),
+                 lambda: i4s.mx_product(x, w, dtype=F32, out=torch.zeros(3, 20, dtype=F16, device="cuda")),
+                 lambda: i4s.MXTensor(20, 64, w.vals, w.scales[:1]), lambda: i4s.MXTensor(20, 64, w.vals.cpu(), w.scales.cpu()),
+                 lambda: i4s.prompt_attention(q.float(), k, k), lambda: i4s.prompt_attention(q, k.bfloat16(), k),
+                 lambda: i4s.prompt_attention(q.cpu(), k, k), lambda: i4s.prompt_attention(q, k.cpu(), k),
+                 lambda: i4s.prompt_attention(q[0], k, k), lambda: i4s.prompt_attention(q, k, k[:4]),
+                 lambda: i4s.prompt_attention(q, k[..., :32], k[..., :32]), lambda: i4s.prompt_attention(q.transpose(1, 2), k, k),
+                 lambda: i4s.prompt_attention(q, k, k, k_start=i32(0, 5)), lambda: i4s.prompt_attention(q, k, k, i32(0, 5).long()),
+                 lambda: i4s.prompt_attention(q, k, k, i32(0, 5), i32(0, 2, 5)), lambda: i4s.prompt_attention(q, k, k, i32()),
+                 lambda: i4s.prompt_attention(q, k, k, out=q.float()), lambda: i4s.prompt_attention(q, k, k, out=q[:4]),
+                 lambda: i4s.prompt_attention(q, k, k, lse=torch.zeros(5, device="cuda"))):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: i4s.mx_quantize(x[:, :40]), lambda: i4s.mx_quantize(x.flatten()[4:68].view(1, 64)),
+                 lambda: i4s.mx_product(x, w, out=x.expand(3, 64)[:, :20]), lambda: i4s.mx_product(x[:1].expand(3, 64), w),
+                 lambda: i4s.prompt_attention(q[:, :3], k, k), lambda: i4s.prompt_attention(q[..., :32], k[..., :32], k[..., :32]),
+                 lambda: i4s.prompt_attention(q, k, k, out=q), lambda: i4s.prompt_attention(q, k, k, scale=0.0),
+                 lambda: i4s.prompt_attention(q, k, k, scale=float("nan")), lambda: i4s.prompt_attention(q, k, k, max_q=0),
+                 lambda: i4s.prompt_attention(q, k, k, max_k=-1)):
+        with pytest.raises(i4s.I4SError):
+            call()
