@@ -178,9 +178,18 @@ __global__ __launch_bounds__(WAVES * 64) void mx_few_kernel(MxProductKernelArgs 
 // A block of WR x WC waves takes WR*RT weight tiles x WC*NT token tiles; a
 // wave RT x NT of them.  Tiles go to LDS directly (global_load_lds), a step of
 // 128 columns at a time, into a ring of kRing steps; scales a group of four
-// steps at a time, into two areas.  One barrier a step: behind it every wave
-// has its step's tiles, and no wave reads the step before any more, whose place
-// the next load takes.
+// steps at a time, into two areas.  A barrier before a step's loads sees to it
+// that every wave has read the step whose place they take, and the waits before
+// it that every wave's part of the step that is read next is there.
+//
+// 8191 x 13824 x 5120: 284 us = 4.1 PFLOP/s; 8192^3 4.4.  Bound by power: matrix
+// instructions alone on the same data run at 6.2 PFLOP/s and 1.5 GHz, and here
+// too the clock falls to 1.5 GHz, with the matrix cores busy 64 % of the cycles.
+// The stores take 5 us of a round of 256 blocks of 256 x 256.  All eight waves in
+// step, reading and then multiplying: 7 to 14 % slower (8192^3: 292 us, half a
+// step apart 257, with the loads among the products 250).  Four waves with
+// 128 x 128 outputs each: the same as that.  128 neighbouring bytes of a token
+// in a store instead of 64, or non-temporal ones: no faster.
 
 constexpr int kRing = 4;
 
@@ -379,17 +388,18 @@ __global__ __launch_bounds__(64 * WR *WC, 2) void mx_tile_kernel(MxProductKernel
       }
     });
   } else {
+    // A SIMD has two waves, one of either half of the rows, and the halves are half a
+    // step apart: while one multiplies, the other reads its operands from LDS.
+    static_assert(WR == 2 && S::kWaves == 8, "wave and wave + 4 share a SIMD");
     load_scales(0);
 #pragma unroll
     for (int i = 0; i < kRing - 1; ++i) load_step(i);
     uint32_t sa[RT], sb[NT];
+    wait_loads<2 * S::kLoads>();
+    meet();
+    if (wr) meet();
     run([&](int s, auto C) {
       constexpr int c = decltype(C)::value;
-      // two more steps (and scales) are on their way behind this one
-      wait_loads<2 * S::kLoads>();
-      meet();  // nobody reads the step before this one any more
-      if (c == 0) load_scales(s / 4 + 1);
-      load_step(s + kRing - 1);
       const char *base = ring + (s & (kRing - 1)) * S::kStep + lane * 16;
       if (c == 0) {
         const char *p = scale_area + (s / 4 & 1) * S::kScales + lane * 4;
@@ -403,11 +413,21 @@ __global__ __launch_bounds__(64 * WR *WC, 2) void mx_tile_kernel(MxProductKernel
       for (int n = 0; n < NT; ++n) vb[n] = load16(base + (S::kA + wc * NT + n) * kMxTileBytes);
 #pragma unroll
       for (int r = 0; r < RT; ++r) va[r] = load16(base + (wr * RT + r) * kMxTileBytes);
+      // the next step's loads (and scales) are done behind this, one more step's on their way
+      wait_loads<S::kLoads>();
+      meet();  // the operands are in registers, and so are the other half's of the step before
+      if (c == 0) load_scales(s / 4 + 1);
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
+      for (int r = 0; r < RT; ++r) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[r][n] = mx_mfma<c>(va[r], sa[r], vb[n], sb[n], acc[r][n]);
+#pragma unroll
+        for (int i = r * S::kLoads / RT; i < (r + 1) * S::kLoads / RT; ++i) load_tile(s + kRing - 1, i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      meet();
     });
+    if (!wr) meet();
   }
   wait_loads<0>();
 

@@ -15,6 +15,7 @@ with torch, never synchronise, and can be captured into a graph.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -44,15 +45,18 @@ class MXTensor:
             if (t.dtype != torch.uint8 or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous()
                     or t.device != vals.device):
                 raise ValueError(f"{name} must be a contiguous uint8 {list(shape)} tensor on one GPU")
-        self.rows, self.cols, self.vals, self.scales = rows, cols, vals, scales
-        self.device = vals.device
-        self.index = self.device.index
+        self._hold(rows, cols, vals, scales, vals.get_device())
+
+    def _hold(self, rows, cols, vals, scales, index):
+        self.rows, self.cols, self.vals, self.scales, self.index = rows, cols, vals, scales, index
+        self.shape = rows, cols
         self.descriptor = P.i4s_mx(rows, cols, vals.data_ptr(), scales.data_ptr())
         self.address = ctypes.addressof(self.descriptor)
+        return self
 
     @property
-    def shape(self):
-        return self.rows, self.cols
+    def device(self):
+        return self.vals.device
 
     def nbytes(self) -> int:
         return self.vals.numel() + self.scales.numel()
@@ -77,11 +81,10 @@ def mx_quantize(x, out: Optional[MXTensor] = None) -> MXTensor:
     rows, cols = x.shape
     _fit(rows, cols)
     if out is None:
-        sz = P.i4s_mx_buffers()
-        B.check(P.i4s_mx_sizes(rows, cols, sz), "i4s_mx_sizes")
+        # the constructor's checks would find what is made here; the call checks rows and cols
         tiles = (rows + 15) // 16
-        out = MXTensor(rows, cols, x.new_empty((tiles, 2 * ((cols + 255) // 256), 1024), dtype=torch.uint8),
-                       x.new_empty((tiles, (cols + 511) // 512, 256), dtype=torch.uint8))
+        vals = x.new_empty((tiles, 2 * ((cols + 255) // 256), 1024), dtype=torch.uint8)
+        out = MXTensor.__new__(MXTensor)._hold(rows, cols, vals, vals.new_empty((tiles, (cols + 511) // 512, 256)), x.get_device())
     elif out.shape != (rows, cols) or out.index != x.get_device():
         raise ValueError(f"out must be [{rows}, {cols}] on {x.device}, not {list(out.shape)} on {out.device}")
     st = _call(P.i4s_mx_quantize, out.index, x.data_ptr(), dtype, stride, out.descriptor)
@@ -102,22 +105,33 @@ def mx_read(m: MXTensor, dtype=torch.float16):
     return out
 
 
+@functools.lru_cache(maxsize=4096)
+def _product_workspace(tokens: int, rows: int, cols: int, given: bool) -> int:
+    """Bytes that a product of these sizes needs."""
+    w = P.i4s_mx(rows, cols)
+    x = P.i4s_mx(tokens, cols)
+    a = P.i4s_mx_product_args(ctypes.addressof(w), ctypes.addressof(x) if given else None, None, 0, 0, tokens)
+    n = ctypes.c_uint64()
+    B.check(P.i4s_mx_product_workspace_size(a, n), "i4s_mx_product_workspace_size")
+    return n.value
+
+
 def mx_product(x, w: MXTensor, dtype=None, out=None):
     """y = x w^T: [tokens, rows of w] for tokens ``x``, an ``MXTensor`` or fp16
     or bf16 [tokens, cols of w] (quantized within the call, with the same
     result; tokens may be strided).  Sums are held in fp32 and rounded once to
     ``dtype`` (float16, bfloat16 or float32; x's, or ``out``'s, or float16).
     ``out`` may have strided tokens."""
-    index = w.index
-    a = P.i4s_mx_product_args()
-    if isinstance(x, MXTensor):
+    index, rows = w.index, w.rows
+    given = isinstance(x, MXTensor)
+    if given:
         tokens, cols, where = x.rows, x.cols, x.index
-        a.x = x.address
+        address, values, x_stride, x_dtype = x.address, None, 0, 0
     else:
-        a.x_dtype, a.x_stride = _rows_of(x, "x")
+        x_dtype, x_stride = _rows_of(x, "x")
         (tokens, cols), where = x.shape, x.get_device()
         _fit(tokens)
-        a.x_values = x.data_ptr()
+        address, values = None, x.data_ptr()
         if dtype is None and out is None:
             dtype = x.dtype
     if cols != w.cols or where != index:
@@ -127,25 +141,22 @@ def mx_product(x, w: MXTensor, dtype=None, out=None):
     number = _DTYPES.get(dtype)
     if number is None:
         raise ValueError("dtype must be float16, bfloat16 or float32")
-    shape = (tokens, w.rows)
+    y_stride = rows
     if out is None:
-        out = w.vals.new_empty(shape, dtype=dtype)
-        a.y_stride = w.rows
+        out = w.vals.new_empty((tokens, rows), dtype=dtype)
     else:
-        if out.dtype is not dtype or out.shape != shape or out.get_device() != index or (w.rows > 1 and out.stride(1) != 1):
-            raise ValueError(f"out must be {dtype} {list(shape)} on GPU {index} with adjacent columns, "
+        if (out.dtype is not dtype or out.shape != (tokens, rows) or out.get_device() != index
+                or (rows > 1 and out.stride(1) != 1)):
+            raise ValueError(f"out must be {dtype} {[tokens, rows]} on GPU {index} with adjacent columns, "
                              f"not {out.dtype} {list(out.shape)} on {out.device}")
-        a.y_stride = out.stride(0) if tokens > 1 else w.rows
-    a.w, a.tokens, a.y, a.y_dtype = w.address, tokens, out.data_ptr(), number
-    nbytes = ctypes.c_uint64()
-    st = P.i4s_mx_product_workspace_size(a, nbytes)
-    if st:
-        B.check(st, "i4s_mx_product_workspace_size")
-    if nbytes.value:
-        # of this call alone: calls on other streams and captured graphs have their own
-        ws = w.vals.new_empty(nbytes.value)
-        a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes.value
-    st = _call(P.i4s_mx_product, index, a)
+        if tokens > 1:
+            y_stride = out.stride(0)
+    nbytes = _product_workspace(tokens, rows, cols, given)
+    # a workspace of this call alone: calls on other streams and captured graphs have their own
+    ws = w.vals.new_empty(nbytes) if nbytes else None
+    st = _call(P.i4s_mx_product, index, P.i4s_mx_product_args(
+        w.address, address, values, x_stride, x_dtype, tokens, out.data_ptr(), y_stride, number, 0,
+        None if ws is None else ws.data_ptr(), nbytes))
     if st:
         B.check(st, "i4s_mx_product")
     return out
@@ -156,6 +167,17 @@ def _whole(n, device):
     if n == 0:
         return torch.zeros(2, dtype=torch.int32, device=device)
     return torch.arange(0, n + 1, n, dtype=torch.int32, device=device)
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention_workspace(dtype, dim, heads, kv_heads, tokens, keys, n, max_q, max_k) -> int:
+    """Bytes that a call of these sizes needs."""
+    _fit(tokens, heads, keys, kv_heads, n, max_q, max_k)
+    a = P.i4s_prompt_args(dtype=dtype, head_dim=dim, q_heads=heads, kv_heads=kv_heads, num_tokens=tokens, num_keys=keys,
+                          num_seqs=n, max_q=max_q, max_k=max_k, scale=1.0)
+    nbytes = ctypes.c_uint64()
+    B.check(P.i4s_prompt_attention_workspace_size(a, nbytes), "i4s_prompt_attention_workspace_size")
+    return nbytes.value
 
 
 def prompt_attention(q, k, v, q_start=None, k_start=None, max_q: Optional[int] = None, max_k: int = 0, causal: bool = True,
@@ -178,15 +200,16 @@ def prompt_attention(q, k, v, q_start=None, k_start=None, max_q: Optional[int] =
     [tokens, q_heads]) receives the logarithm of the sum of exponentials.
     Returns [tokens, q_heads, head_dim] like q.
     """
-    shape, dtype, index = q.shape, _HALVES.get(q.dtype), q.get_device()
+    shape, kind, index = q.shape, q.dtype, q.get_device()
+    dtype = _HALVES.get(kind)
     if dtype is None or len(shape) != 3 or index < 0:
         raise ValueError("q must be a float16 or bfloat16 [tokens, q_heads, head_dim] tensor on a GPU")
     tokens, heads, dim = shape
-    if (k.dim() != 3 or k.shape != v.shape or k.shape[2] != dim or k.dtype is not q.dtype or v.dtype is not q.dtype
+    held = k.shape
+    if (len(held) != 3 or held != v.shape or held[2] != dim or k.dtype is not kind or v.dtype is not kind
             or k.get_device() != index or v.get_device() != index):
-        raise ValueError(f"k and v must be {q.dtype} [keys, kv_heads, {dim}] tensors on {q.device}")
-    keys, kv_heads = k.shape[0], k.shape[1]
-    qs, ks, vs = _strides(q, "q"), _strides(k, "k"), _strides(v, "v")
+        raise ValueError(f"k and v must be {kind} [keys, kv_heads, {dim}] tensors on {q.device}")
+    keys, kv_heads, _ = held
     if q_start is None:
         if k_start is not None:
             raise ValueError("k_start needs q_start")
@@ -201,26 +224,20 @@ def prompt_attention(q, k, v, q_start=None, k_start=None, max_q: Optional[int] =
     _check(k_start, torch.int32, (n + 1,), index, "k_start")
     if max_q is None:
         max_q = max(tokens, 1)
-    _fit(tokens, heads, keys, kv_heads, n, max_q, max_k)
     if out is None:
         out = q.new_empty(shape)
     else:
-        _check(out, q.dtype, shape, index, "out")
+        _check(out, kind, shape, index, "out")
     if lse is not None:
         _check(lse, torch.float32, (tokens, heads), index, "lse")
-    a = P.i4s_prompt_args(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], dtype, dim, heads, kv_heads,
-        tokens, keys, n, max_q, max_k, int(bool(causal)), dim ** -0.5 if scale is None else scale, 0, q_start.data_ptr(),
-        k_start.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), None, 0)
-    nbytes = ctypes.c_uint64()
-    st = P.i4s_prompt_attention_workspace_size(a, nbytes)
-    if st:
-        B.check(st, "i4s_prompt_attention_workspace_size")
-    if nbytes.value:
-        # of this call alone: calls on other streams and captured graphs have their own
-        ws = q.new_empty(nbytes.value, dtype=torch.uint8)
-        a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes.value
-    st = _call(P.i4s_prompt_attention, index, a)
+    nbytes = _attention_workspace(dtype, dim, heads, kv_heads, tokens, keys, n, max_q, max_k)
+    # a workspace of this call alone: calls on other streams and captured graphs have their own
+    ws = q.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+    st = _call(P.i4s_prompt_attention, index, P.i4s_prompt_args(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), *_strides(q, "q"), *_strides(k, "k"), *_strides(v, "v"), dtype, dim, heads,
+        kv_heads, tokens, keys, n, max_q, max_k, 1 if causal else 0, dim ** -0.5 if scale is None else scale, 0,
+        q_start.data_ptr(), k_start.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+        None if ws is None else ws.data_ptr(), nbytes))
     if st:
         B.check(st, "i4s_prompt_attention")
     return out
