@@ -57,6 +57,15 @@ struct YFloat {
 // neighbouring lanes hold a block, and codes and scales pass through the wave's
 // own LDS into the matrix instruction's order.  Their loads go out first: they
 // come from L2, and loads return in order.
+//
+// ONCE: no other block reads the same weights, which then pass by the caches.
+// Us, so / through them: 50257 x 4096, 16 tokens 22.0 / 24.0, 37 tokens 29.1 / 30.6;
+// 13824 x 5120, 48 tokens 11.9 / 12.8; 4096 x 4096, 16 tokens 3.8 / 3.7 (from the
+// last-level cache); 200 tokens in four blocks, 9.8 / 9.2.
+// Bound by memory: 50257 x 4096 with 16 tokens reads 5.8 TB/s behind 2.5 us of
+// launch and first loads; more tokens cost their reads from L2 by every block, which
+// for 48 are more than the weights (more weight tiles a block: registers do not
+// reach; one and two waves a block: 33 to 36 us for 37 tokens).
 
 // One group's tiles in registers.
 template <int N>
@@ -65,24 +74,30 @@ struct Operand {
   uint32_t s[N];
 };
 
-template <int N>
+template <int N, bool STREAM>
 __device__ inline void load_operand(Operand<N> &o, const uint8_t *vals, const uint8_t *scales, int first, int tiles, int steps,
                                     int groups, int group, int lane) {
   const int left = steps - 4 * group;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int64_t tile = first + i < tiles ? first + i : tiles - 1;
-    o.s[i] = load4(scales + (tile * groups + group) * kMxGroupBytes + lane * 4);
+    const uint8_t *sp = scales + (tile * groups + group) * kMxGroupBytes + lane * 4;
+    o.s[i] = STREAM ? __builtin_nontemporal_load(reinterpret_cast<const uint32_t *>(sp)) : load4(sp);
     const uint8_t *p = vals + (tile * steps + 4 * group) * kMxTileBytes + lane * 16;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-      if (c < 2 || left > 2) o.v[i][c] = load16(p + c * kMxTileBytes);
+      if (c < 2 || left > 2) {
+        if constexpr (STREAM)
+          o.v[i][c] = __builtin_nontemporal_load(reinterpret_cast<const u4_t *>(p + c * kMxTileBytes));
+        else
+          o.v[i][c] = load16(p + c * kMxTileBytes);
+      }
   }
 }
 
 struct NoX {};  // tokens in the format
 
-template <typename X, typename Y, int RT, int NT, int WAVES>
+template <typename X, typename Y, int RT, int NT, int WAVES, bool ONCE>
 __global__ __launch_bounds__(WAVES * 64) void mx_few_kernel(MxProductKernelArgs a) {
   constexpr bool kFused = !std::is_same<X, NoX>::value;
   constexpr int kBatch = 4;  // tokens whose loads are on their way together
@@ -111,8 +126,8 @@ __global__ __launch_bounds__(WAVES * 64) void mx_few_kernel(MxProductKernelArgs 
   Operand<NT> x;
   auto load = [&](int g) {
     if constexpr (kFused) load_tokens(g, 0);
-    load_operand<RT>(w, a.w_vals, a.w_scales, first, tiles, steps, groups, g, lane);
-    if constexpr (!kFused) load_operand<NT>(x, a.x_vals, a.x_scales, blockIdx.y * NT, mx_row_tiles(a.tokens), steps, groups, g, lane);
+    load_operand<RT, ONCE>(w, a.w_vals, a.w_scales, first, tiles, steps, groups, g, lane);
+    if constexpr (!kFused) load_operand<NT, false>(x, a.x_vals, a.x_scales, blockIdx.y * NT, mx_row_tiles(a.tokens), steps, groups, g, lane);
   };
   if (wave < groups) load(wave);
   for (int g = wave; g < groups; g += WAVES) {
@@ -460,10 +475,10 @@ __global__ __launch_bounds__(64 * WR *WC, 2) void mx_tile_kernel(MxProductKernel
     }
 }
 
-template <typename X, typename Y, int RT, int NT, int WAVES>
+template <typename X, typename Y, int RT, int NT, int WAVES, bool ONCE = true>
 hipError_t launch_few_shape(const MxProductKernelArgs &a, hipStream_t stream) {
   const dim3 grid((mx_row_tiles(a.rows) + RT - 1) / RT, (mx_row_tiles(a.tokens) + NT - 1) / NT);
-  hipLaunchKernelGGL((mx_few_kernel<X, Y, RT, NT, WAVES>), grid, dim3(64 * WAVES), 0, stream, a);
+  hipLaunchKernelGGL((mx_few_kernel<X, Y, RT, NT, WAVES, ONCE>), grid, dim3(64 * WAVES), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -482,7 +497,8 @@ hipError_t launch_few(const MxProductKernelArgs &a, const MxProductPlan &p, hipS
     case 1: return launch_few_tokens<NoX, Y, 1>(a, p, stream);
     case 2: return launch_few_tokens<NoX, Y, 2>(a, p, stream);
     case 3: return launch_few_tokens<NoX, Y, 3>(a, p, stream);
-    default: return launch_few_tokens<NoX, Y, 4>(a, p, stream);
+    case 4: return launch_few_tokens<NoX, Y, 4>(a, p, stream);
+    default: return launch_few_shape<NoX, Y, 2, 4, 4, false>(a, stream);
   }
 }
 

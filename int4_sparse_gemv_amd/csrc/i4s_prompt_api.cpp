@@ -157,12 +157,14 @@ MxProductPlan mx_product_plan(int32_t tokens, int32_t rows, int32_t cols, bool x
   // 11008 x 4096: 64: 11 / 13, 128: 14.4 / 12.9; 13824 x 5120: 64: 13.6 / 15, 128: 20 / 17.
   p.few = p.token_tiles <= 4 || (int64_t)tiles * p.token_tiles <= 5120;
   if (p.token_tiles > 4) p.row_tiles = 2, p.waves = 4;
-  // 256 x 256 outputs, one block a compute unit, where they fill whole rounds of
-  // them; else 128 x 128, two blocks.  Us, 256 / 128: 4096^3 39 / 41 (256 blocks); 8191
-  // x 13824 x 5120 327 / 357 (6.75 rounds); 3000 x 13824 x 5120 127 / 125 (2.5 of 3);
-  // 4096 x 5120 x 13824 197 / 147 (1.25 of 2); 2048 x 4096 x 4096 34 / 23 (half of one).
+  // 256 x 256 outputs, one block a compute unit, where they fill more than three
+  // quarters of whole rounds of them; else 128 x 128, two blocks.  Us, 256 / 128:
+  // 4096^3 37 / 41 (256 blocks); 9000 x 13824 x 5120 348 / 402 (7.6 rounds of 8); 3000 x
+  // 13824 x 5120 114 / 125 (2.5 of 3); 5000 x 5120 x 5120 74 / 80 (400 blocks); 6000 x
+  // 4096 x 4096 61 / 59 (384); 4096 x 5120 x 13824 162 / 148 (320); 2048 x 4096 x 4096
+  // 34 / 23 (half of one).
   const int64_t large = ((int64_t)tokens + 255) / 256 * (((int64_t)rows + 255) / 256);
-  p.tile = 10 * large >= 9 * ((large + 255) / 256 * 256) ? 256 : 128;
+  p.tile = 4 * large > 3 * ((large + 255) / 256 * 256) ? 256 : 128;
   if (p.quantize) {
     p.x_vals = mx_vals_bytes(tokens, cols);
     p.x_scales = mx_scales_bytes(tokens, cols);

@@ -34,10 +34,11 @@
 // 32 rows or fewer of a sequence and KV head (a token behind long keys) are bound
 // by memory: there each wave of a block has tiles of 32 keys of its own, two of
 // them, in its own time with no barrier, and all join in LDS; long keys are
-// split over blocks, joined by a second launch.  65536 keys of 8 KV heads of 128,
-// 32 query heads: 59 us = 4.6 TB/s.  Us, waves x tiles ahead 3x3 / 4x2 / 5x2: 60.2 /
-// 59.5 / 61.8, D = 64 38.1 / 36.8 / 39.6; blocks of four waves sharing tiles of
-// 64 keys took 115.
+// split over blocks, joined by a second launch.  Keys and values are read once,
+// past the caches.  65536 keys of 8 KV heads of 128, 32 query heads: 49 us = 5.4
+// TB/s (through the caches 64), 64 such sequences of 4096 keys 164 us = 6.6 (186).
+// Us through the caches, waves x tiles ahead 3x3 / 4x2 / 5x2: 60.2 / 59.5 / 61.8, D =
+// 64 38.1 / 36.8 / 39.6; blocks of four waves sharing tiles of 64 keys took 115.
 
 #include <float.h>
 
@@ -104,8 +105,9 @@ __device__ inline float lse_of(float reference, float sum, float scale_log2, flo
 
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(1))) const void global_void;
+template <int AUX>  // 2: past the caches
 __device__ inline void copy16(const void *from, char *to) {
-  __builtin_amdgcn_global_load_lds((global_void *)from, (lds_void *)to, 16, 0, 0);
+  __builtin_amdgcn_global_load_lds((global_void *)from, (lds_void *)to, 16, 0, AUX);
 }
 template <int N>
 __device__ inline void wait_loads() {
@@ -236,13 +238,13 @@ __global__ __launch_bounds__((64 * Shape<T, D, FEW>::kWaves), (D == 256 || FEW ?
     for (int i = 0; i < S::kLoads; ++i) {
       const int at = loader * S::kLoads + i, r = at * kRowsPerLoad + lane / L::kPieces, p = lane % L::kPieces;
       const int from = r < left ? r : left;
-      copy16(k0 + (uint32_t)(from * k_step + L::k_piece(r, p) * 16), to + at * 1024);
+      copy16<FEW ? 2 : 0>(k0 + (uint32_t)(from * k_step + L::k_piece(r, p) * 16), to + at * 1024);
     }
 #pragma unroll
     for (int i = 0; i < S::kLoads; ++i) {
       const int at = loader * S::kLoads + i, r = at * kRowsPerLoad + lane / L::kPieces, p = lane % L::kPieces;
       const int from = r < left ? r : left;
-      copy16(v0 + (uint32_t)(from * v_step + L::v_piece(r, p) * 16), to + L::kBytes + at * 1024);
+      copy16<FEW ? 2 : 0>(v0 + (uint32_t)(from * v_step + L::v_piece(r, p) * 16), to + L::kBytes + at * 1024);
     }
   };
 
