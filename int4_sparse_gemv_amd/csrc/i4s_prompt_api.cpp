@@ -176,10 +176,17 @@ MxProductPlan mx_product_plan(int32_t tokens, int32_t rows, int32_t cols, bool x
 PromptPlan prompt_plan(const i4s_prompt_args &a) {
   PromptPlan p{};
   const int64_t rows = (int64_t)a.max_q * (a.q_heads / a.kv_heads);
-  p.few = rows <= kPromptRows;
-  p.row_blocks = p.few ? 1 : (int32_t)((rows + 4 * kPromptRows - 1) / (4 * kPromptRows));
+  const int64_t pairs = (int64_t)a.kv_heads * (a.num_seqs > 0 ? a.num_seqs : 1), large = (rows + 255) / 256;
+  // Blocks of 32 rows where those are all; of 256 (head dimension 128) where a pair
+  // has many and all of them are some rounds of the 256 compute units; else of 128.
+  // Us, 256 / 128: 8191 tokens x 40 heads 689 / 706, x 32 553 / 595; 4096 x 56 (896
+  // blocks of 256) 290 / 296, x 40 (640) 219 / 210; 16 x 1024 x 40 (four a pair) 402 /
+  // 382; head dimension 64, 4096 x 40 133 / 120.
+  p.rows = rows <= kPromptRows ? kPromptRows
+           : a.head_dim == 128 && large >= 16 && pairs * large >= 896 ? 8 * kPromptRows : 4 * kPromptRows;
+  p.row_blocks = (int32_t)((rows + p.rows - 1) / p.rows);
   const int64_t len = a.max_k > 0 && a.max_k < a.num_keys ? a.max_k : a.num_keys;
-  const int64_t units = (int64_t)p.row_blocks * a.kv_heads * (a.num_seqs > 0 ? a.num_seqs : 1);
+  const int64_t units = p.row_blocks * pairs;
   // Pairs of sequence and KV head that run together: as many as keep their keys in
   // the L2s, but enough that long rows of one are done next to short ones of others.
   // Us, groups of 1 / 20 / 40 / all pairs: 16 x up to 2047 tokens, 8 x 4 heads (128
@@ -190,7 +197,7 @@ PromptPlan prompt_plan(const i4s_prompt_args &a) {
   // launch.  Us, for 256 / 512 / 1024 blocks: 65536 keys, 8 x 4 rows 60 / 60 / 76;
   // 128 tokens behind 32767, 8 x 4 heads 110 / 102 / 117.  512 tokens, 40 heads in one
   // piece / two of 256 keys 25 / 52.
-  const int64_t want = clamp_to<int64_t>((p.few ? 256 : 512) / units, 1, len > 512 ? (len + 511) / 512 : 1);
+  const int64_t want = clamp_to<int64_t>((p.rows == kPromptRows ? 256 : 512) / units, 1, len > 512 ? (len + 511) / 512 : 1);
   const int64_t per = clamp_to<int64_t>((len + want * kPromptKeys - 1) / (want * kPromptKeys), 1, (1 << 30) / kPromptKeys);
   p.chunk = (int32_t)(per * kPromptKeys);
   p.splits = (int32_t)clamp_to<int64_t>((len + p.chunk - 1) / p.chunk, 1, kMaxPromptSplits);

@@ -1,11 +1,10 @@
 // Attention of packed sequences over their own 16-bit keys and values
 // (include/i4s_prompt.h), for gfx950.
 //
-// A block takes 128 query rows (tokens x query heads) of one sequence that
-// read one KV head, 32 a wave; its waves share tiles of keys and values in
-// LDS, filled with direct 16-byte loads one step ahead of their use.  Scores
-// and outputs are computed transposed, so that no value moves between lanes
-// on the way:
+// A block takes 128 or 256 query rows (tokens x query heads) of one sequence
+// that read one KV head, 32 a wave; its waves share tiles of keys and values in
+// LDS, filled with direct 16-byte loads ahead of their use.  Scores and outputs
+// are computed transposed, so that no value moves between lanes on the way:
 //   S^T = K Q^T: v_mfma_f32_32x32x16 with 32 keys as rows, 32 query rows as
 //     columns and 16 channels.  Lane l = i + 32 h holds query row i and the
 //     keys 8 x + 4 h + 0..3, x = 0..3, of a tile: its softmax is a loop over
@@ -24,12 +23,17 @@
 // the values' type for its matrix instruction (at most 2^-8 of itself for
 // bf16, 2^-11 for fp16), the sum takes it unrounded; the output is rounded once.
 //
-// Long prompts are bound by the matrix cores and the power they may take: 8191
-// tokens, 40 heads of 128, causal, 725 us = 0.95 PFLOP/s with the masked halves
-// of tiles, without the causal mask 1460 us = 0.94; matrix instructions alone
-// reach 1.9, and are busy half of the cycles, the softmax's vector instructions
-// the other half.  Tried and no faster: 32-key tiles with the next scores ahead of
-// this softmax (the same time, D = 256 slower), 64 rows a wave (spills).
+// Long prompts are bound by the matrix cores, the LDS that feeds them (every wave
+// reads all keys and values for its 32 rows: half of the LDS's cycles) and power.
+// 8191 tokens, 40 heads of 128: 1231 us without the causal mask = 1.12 PFLOP/s, 689
+// with it; a large matrix product of the library reaches 1.15, matrix instructions
+// alone 1.9.  Us without the mask, step by step: operands read by the instruction that
+// uses them 1400; four instructions ahead, V's first ones before the softmax, 1300
+// (head dimension 256: 224, 178; two ahead 204; six the same as four); blocks of 256
+// rows in two halves, one in its softmax while the other multiplies, 1275, with the
+// loads' issue in the softmax 1231.  Tried and no faster: wave priorities for either
+// part, waits between matrix instructions, 32-key tiles with the next scores ahead
+// of this softmax; 64 rows a wave spill.
 //
 // 32 rows or fewer of a sequence and KV head (a token behind long keys) are bound
 // by memory: there each wave of a block has tiles of 32 keys of its own, two of
@@ -165,27 +169,33 @@ struct Tile {
 
 constexpr float kSlack = 8.0f;  // log2: how far a probability may pass 2^kHeadroom
 
-// FEW: all query rows of a sequence and KV head fit a wave.  Then the waves of a
-// block take the same rows and tiles of their own in turn, and join at the end.
+// ROWS of a block.  32: all query rows of a sequence and KV head fit a wave; the
+// waves of a block take the same rows and tiles of their own in turn, and join
+// at the end.  128: four waves, two blocks a compute unit.  256: eight, in two
+// halves half a step apart.
 // D = 256: 32 keys a tile, for 64 the registers do not reach.
-template <typename T, int D, bool FEW>
+template <typename T, int D, int ROWS>
 struct Shape {
-  static constexpr int kWaves = FEW && D == 256 ? 2 : 4;
-  static constexpr int kBlockRows = FEW ? kPromptRows : kWaves * kPromptRows;
-  typedef Tile<D, FEW || D == 256 ? 32 : 64> L;
-  static constexpr int kLoaders = FEW ? 1 : kWaves;             // waves that share a tile's loads
+  static constexpr bool kFew = ROWS == kPromptRows, kPaired = ROWS == 8 * kPromptRows;
+  static constexpr int kWaves = kFew ? (D == 256 ? 2 : 4) : ROWS / kPromptRows;
+  typedef Tile<D, kFew || D == 256 ? 32 : 64> L;
+  static constexpr int kLoaders = kFew ? 1 : kWaves;            // waves that share a tile's loads
   static constexpr int kLoads = L::kBytes / 1024 / kLoaders;    // load instructions of a wave for K, and for V
-  static constexpr int kLds = (FEW ? kWaves : 1) * 4 * L::kBytes;
+  static constexpr int kStages = kPaired ? 4 : 2;               // tiles of K, and of V
+    static constexpr int kLds = (kFew ? kWaves : 1) * 2 * kStages * L::kBytes;
   static constexpr int kRowFloats = D + 4;                      // of an output row where waves join
-  static_assert(!FEW || kWaves * kPromptRows * kRowFloats * 4 + kWaves * kPromptRows * 8 <= kLds, "joined in the tiles' LDS");
+  static_assert(!kFew || kWaves * kPromptRows * kRowFloats * 4 + kWaves * kPromptRows * 8 <= kLds, "joined in the tiles' LDS");
+  static_assert(kLds <= 160 * 1024, "a compute unit has 160 KB");
 };
 
-template <typename T, int D, bool FEW>
-__global__ __launch_bounds__((64 * Shape<T, D, FEW>::kWaves), (D == 256 || FEW ? 1 : 2)) void prompt_kernel(PromptKernelArgs a) {
-  typedef Shape<T, D, FEW> S;
+template <typename T, int D, int ROWS>
+__global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPromptRows || D == 256 ? 1 : 2)) void prompt_kernel(
+    PromptKernelArgs a) {
+  typedef Shape<T, D, ROWS> S;
+  constexpr bool FEW = S::kFew, PAIRED = S::kPaired;
   typedef typename S::L L;
   constexpr int NK = L::kKeys / 32, NC = D / 32, NQ = D / 16, kWaves = S::kWaves;
-  constexpr int kRowsPerLoad = 64 / L::kPieces;
+  constexpr int kRowsPerLoad = 64 / L::kPieces, kAhead = 4;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
   const int li = lane & 31, lh = lane >> 5;
@@ -198,11 +208,11 @@ __global__ __launch_bounds__((64 * Shape<T, D, FEW>::kWaves), (D == 256 || FEW ?
   const int seq = pair / a.kv_heads, head = pair % a.kv_heads;
   const Sequence s = sequence_of(a, seq);
   const int tokens = s.nq < a.max_q ? s.nq : a.max_q;
-  const int rows = tokens * a.share, block_row = rb * S::kBlockRows;
+  const int rows = tokens * a.share, block_row = rb * ROWS;
   if (block_row >= rows) return;
 
   // keys of this piece that any row of the block sees
-  const int last_row = block_row + S::kBlockRows < rows ? block_row + S::kBlockRows - 1 : rows - 1;
+  const int last_row = block_row + ROWS < rows ? block_row + ROWS - 1 : rows - 1;
   const int most = keys_seen(a, s, last_row / a.share);
   const int piece0 = blockIdx.y * a.chunk;
   const int piece1 = (int)blockIdx.y + 1 < a.splits && most - piece0 > a.chunk ? piece0 + a.chunk : most;
@@ -228,23 +238,28 @@ __global__ __launch_bounds__((64 * Shape<T, D, FEW>::kWaves), (D == 256 || FEW ?
   const char *vb = static_cast<const char *>(a.v) + 2 * (s.k0 * a.v_token + head * a.v_head);
   const uint32_t k_step = 2 * (uint32_t)a.k_token, v_step = 2 * (uint32_t)a.v_token;
   // this wave's pieces of 1024 bytes of K and of V
-  char *const tiles = lds + (FEW ? wave * 4 * L::kBytes : 0);
+  char *const tiles = lds + (FEW ? wave * 2 * S::kStages * L::kBytes : 0);
   const int loader = FEW ? 0 : wave;
-  auto load_step = [&](int key, int stage) {
-    char *to = tiles + stage * 2 * L::kBytes;
-    const char *k0 = kb + (int64_t)key * k_step, *v0 = vb + (int64_t)key * v_step;
-    const int left = s.nk - 1 - key;  // rows past it repeat the last: their scores are masked
+  char *const v_tiles = tiles + S::kStages * L::kBytes;
+  // rows past the keys repeat the last: their scores are masked
+  auto load_k = [&](int key, int stage) {
+    const int first = key < s.nk ? key : s.nk - 1, left = s.nk - 1 - first;
+    const char *k0 = kb + (int64_t)first * k_step;
 #pragma unroll
     for (int i = 0; i < S::kLoads; ++i) {
       const int at = loader * S::kLoads + i, r = at * kRowsPerLoad + lane / L::kPieces, p = lane % L::kPieces;
       const int from = r < left ? r : left;
-      copy16<FEW ? 2 : 0>(k0 + (uint32_t)(from * k_step + L::k_piece(r, p) * 16), to + at * 1024);
+      copy16<FEW ? 2 : 0>(k0 + (uint32_t)(from * k_step + L::k_piece(r, p) * 16), tiles + stage * L::kBytes + at * 1024);
     }
+  };
+  auto load_v = [&](int key, int stage) {
+    const int first = key < s.nk ? key : s.nk - 1, left = s.nk - 1 - first;
+    const char *v0 = vb + (int64_t)first * v_step;
 #pragma unroll
     for (int i = 0; i < S::kLoads; ++i) {
       const int at = loader * S::kLoads + i, r = at * kRowsPerLoad + lane / L::kPieces, p = lane % L::kPieces;
       const int from = r < left ? r : left;
-      copy16<FEW ? 2 : 0>(v0 + (uint32_t)(from * v_step + L::v_piece(r, p) * 16), to + L::kBytes + at * 1024);
+      copy16<FEW ? 2 : 0>(v0 + (uint32_t)(from * v_step + L::v_piece(r, p) * 16), v_tiles + stage * L::kBytes + at * 1024);
     }
   };
 
@@ -272,19 +287,34 @@ __global__ __launch_bounds__((64 * Shape<T, D, FEW>::kWaves), (D == 256 || FEW ?
     return r;
   };
 
-  auto step = [&](int key, const char *stage, auto MASKED) {
+  auto step = [&](int key, int stage, auto MASKED, auto &&load) {
     constexpr bool masked = decltype(MASKED)::value;
+    // Operands are read kAhead instructions ahead of the one that uses them, V's
+    // first ones before the softmax.
+    constexpr int kScores = NK * NQ, kValues = 2 * NK * NC;
     f16_t p[NK];
+    u4_t ahead[kAhead];
+    auto read_k = [&](int i) {  // neighbouring products have sums of their own
+      return *reinterpret_cast<const u4_t *>(tiles + stage * L::kBytes + (32 * (i % NK) + li) * 2 * D + L::k_piece(li, 2 * (i / NK) + lh) * 16);
+    };
+    const char *const tile = v_tiles + stage * L::kBytes;
 #pragma unroll
-    for (int n = 0; n < NK; ++n) {
-      const char *tile = stage + (32 * n + li) * 2 * D;
-      u4_t k = *reinterpret_cast<const u4_t *>(tile + L::k_piece(li, lh) * 16);
-      p[n] = T::mfma(k, q[0], less);
+    for (int i = 0; i < kAhead; ++i) ahead[i] = read_k(i);
+    issue_fence();
 #pragma unroll
-      for (int c = 1; c < NQ; ++c) {
-        k = *reinterpret_cast<const u4_t *>(tile + L::k_piece(li, 2 * c + lh) * 16);
-        p[n] = T::mfma(k, q[c], p[n]);
-      }
+    for (int i = 0; i < kScores; ++i) {
+      p[i % NK] = T::mfma(ahead[i % kAhead], q[i / NK], i < NK ? less : p[i % NK]);
+      if (i + kAhead < kScores) ahead[i % kAhead] = read_k(i + kAhead);
+      issue_fence();
+    }
+    if constexpr (PAIRED) {
+      meet();  // the other half has its softmax behind it
+      load();
+    }
+    if constexpr (!masked) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) ahead[i] = read_v(tile, i % NC, i / NC);
+      issue_fence();
     }
     if constexpr (masked) {
       const int limit = seen - key - 4 * lh;
@@ -327,7 +357,7 @@ __global__ __launch_bounds__((64 * Shape<T, D, FEW>::kWaves), (D == 256 || FEW ?
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[n][e / 4][e % 4] = two<T>(p[n][2 * e], p[n][2 * e + 1]);
     }
-    const char *tile = stage + L::kBytes;
+    if constexpr (PAIRED) wait_loads<2 * S::kLoads>(), meet();
     bool strange = false;  // values that are not finite may lie where a row does not see them
     if constexpr (masked) {
       float test = 0;
@@ -342,10 +372,17 @@ __global__ __launch_bounds__((64 * Shape<T, D, FEW>::kWaves), (D == 256 || FEW ?
       strange = __builtin_amdgcn_ballot_w64(!(test == 0.0f)) != 0;
     }
     if (!strange) {
+      if constexpr (masked) {
 #pragma unroll
-      for (int x = 0; x < 2 * NK; ++x)
+        for (int i = 0; i < kAhead; ++i) ahead[i] = read_v(tile, i % NC, i / NC);
+        issue_fence();
+      }
 #pragma unroll
-        for (int c = 0; c < NC; ++c) o[c] = T::mfma(read_v(tile, c, x), w[x / 2][x % 2], o[c]);
+      for (int i = 0; i < kValues; ++i) {
+        o[i % NC] = T::mfma(ahead[i % kAhead], w[i / NC / 2][i / NC % 2], o[i % NC]);
+        if (i + kAhead < kValues) ahead[i % kAhead] = read_v(tile, (i + kAhead) % NC, (i + kAhead) / NC);
+        issue_fence();
+      }
       return;
     }
     // the finite ones as usual; then whether the row sees a +inf (-inf, either
@@ -394,29 +431,66 @@ __global__ __launch_bounds__((64 * Shape<T, D, FEW>::kWaves), (D == 256 || FEW ?
   const int plain = (all_see < piece1 ? all_see : piece1) - L::kKeys;
   constexpr int kStride = FEW ? kWaves * L::kKeys : L::kKeys;
   int key = piece0 + (FEW ? wave * L::kKeys : 0), stage = 0;
-  if (key < piece1) load_step(key, 0);
-  auto next = [&]() {
-    wait_loads<0>();
-    if constexpr (FEW) {
-      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the other stage is read
-      issue_fence();
-    } else {
-      meet();  // everybody's part of this step's tiles is here, and nobody reads the other stage
+  if constexpr (PAIRED) {
+    // While one half multiplies (a tile's probabilities with V, the next one's keys
+    // with Q), the other works on its softmax, on the same four SIMDs.  Loads run
+    // three tiles ahead of the keys' use, two of the values'.
+    auto load = [&]() {
+      load_k(key + 3 * kStride, (stage + 3) & 3);
+      load_v(key + 2 * kStride, stage ^ 2);
+    };
+    auto turn = [&]() { key += kStride, stage = (stage + 1) & 3; };
+    if (key < piece1) {
+      load_k(key, 0), load_k(key + kStride, 1), load_v(key, 0);
+      load_k(key + 2 * kStride, 2), load_v(key + kStride, 1);
+      wait_loads<2 * S::kLoads>();
+      meet();
+      if (wave >= kWaves / 2) meet();
     }
-    if (key + kStride < piece1) load_step(key + kStride, stage ^ 1);
-  };
-  auto turn = [&]() { key += kStride, stage ^= 1; };
 #pragma unroll 1
-  while (key <= plain) {
-    next();
-    step(key, tiles + stage * 2 * L::kBytes, std::false_type());
-    turn();
-  }
+    while (key <= plain) {
+      step(key, stage, std::false_type(), load);
+      turn();
+    }
 #pragma unroll 1
-  while (key < piece1) {
-    next();
-    if (key < any_sees) step(key, tiles + stage * 2 * L::kBytes, std::true_type());
-    turn();
+    while (key < piece1) {
+      if (key < any_sees) {
+        step(key, stage, std::true_type(), load);
+      } else {
+        meet();
+        load();
+        wait_loads<2 * S::kLoads>();
+        meet();
+      }
+      turn();
+    }
+    if (piece0 < piece1 && wave < kWaves / 2) meet();
+    wait_loads<0>();
+  } else {
+    if (key < piece1) load_k(key, 0), load_v(key, 0);
+    auto next = [&]() {
+      wait_loads<0>();
+      if constexpr (FEW) {
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the other stage is read
+        issue_fence();
+      } else {
+        meet();  // everybody's part of this step's tiles is here, and nobody reads the other stage
+      }
+      if (key + kStride < piece1) load_k(key + kStride, stage ^ 1), load_v(key + kStride, stage ^ 1);
+    };
+    auto turn = [&]() { key += kStride, stage ^= 1; };
+#pragma unroll 1
+    while (key <= plain) {
+      next();
+      step(key, stage, std::false_type(), [] {});
+      turn();
+    }
+#pragma unroll 1
+    while (key < piece1) {
+      next();
+      if (key < any_sees) step(key, stage, std::true_type(), [] {});
+      turn();
+    }
   }
 
   sum += other_half(sum, lane);
@@ -548,11 +622,11 @@ __global__ __launch_bounds__(kJoinThreads) void prompt_join_kernel(PromptKernelA
   if (a.lse && threadIdx.x == 0) a.lse[row] = lse_of(top, sum, a.scale_log2, T::kHeadroom);
 }
 
-template <typename T, int D, bool FEW>
+template <typename T, int D, int ROWS>
 hipError_t launch_shape(const PromptKernelArgs &a, hipStream_t stream) {
-  typedef Shape<T, D, FEW> S;
+  typedef Shape<T, D, ROWS> S;
   const unsigned blocks = (unsigned)((int64_t)a.num_seqs * a.kv_heads * a.row_blocks);
-  hipLaunchKernelGGL((prompt_kernel<T, D, FEW>), dim3(blocks, a.splits), dim3(64 * S::kWaves), S::kLds, stream, a);
+  hipLaunchKernelGGL((prompt_kernel<T, D, ROWS>), dim3(blocks, a.splits), dim3(64 * S::kWaves), S::kLds, stream, a);
   if (a.splits > 1) {
     const int64_t rows = (int64_t)a.max_q * a.kv_heads * a.share;
     hipLaunchKernelGGL((prompt_join_kernel<T, D>), dim3((unsigned)rows, a.num_seqs), dim3(kJoinThreads), 0, stream, a);
@@ -562,7 +636,9 @@ hipError_t launch_shape(const PromptKernelArgs &a, hipStream_t stream) {
 
 template <typename T, int D>
 hipError_t launch_dim(const PromptKernelArgs &a, const PromptPlan &p, hipStream_t stream) {
-  return p.few ? launch_shape<T, D, true>(a, stream) : launch_shape<T, D, false>(a, stream);
+  if constexpr (D == 128)
+    if (p.rows == 8 * kPromptRows) return launch_shape<T, D, 8 * kPromptRows>(a, stream);
+  return p.rows == kPromptRows ? launch_shape<T, D, kPromptRows>(a, stream) : launch_shape<T, D, 4 * kPromptRows>(a, stream);
 }
 
 template <typename T>

@@ -77,12 +77,12 @@ hipError_t launch_mx_product(const MxProductKernelArgs &a, const MxProductPlan &
 // ---------------------------------------------------------------------------
 // attention of whole prompts (i4s_prompt_attention.hip)
 
-// Launch shape: blocks of 128 query rows (tokens x query heads of one KV head),
-// or, `few`, of up to 32 that a sequence and KV head has in all, row_blocks such
+// Launch shape: blocks of 128 or 256 query rows (tokens x query heads of one KV
+// head), or of up to 32 that a sequence and KV head has in all, row_blocks such
 // blocks a sequence and KV head, the keys in `splits` pieces of `chunk` keys (the
 // last takes what is left).
 struct PromptPlan {
-  bool few;
+  int32_t rows;  // of a block
   int32_t row_blocks;
   int32_t group;  // pairs of sequence and KV head that run together
   int32_t splits, chunk;

@@ -122,9 +122,10 @@ void attention(i4s_status expect) {
                 const i4s::PromptPlan &p = prompt_stub_plan();
                 const i4s::PromptKernelArgs &k = prompt_stub_attention();
                 const int64_t len = max_k > 0 && max_k < keys ? max_k : keys;
-                CHECK(p.few == ((int64_t)max_q * share <= i4s::kPromptRows));
-                CHECK((int64_t)p.row_blocks * (p.few ? 32 : 128) >= (int64_t)max_q * share);
-                CHECK((int64_t)p.row_blocks * heads * seqs * 256 < (int64_t(1) << 31));  // threads of the grid
+                CHECK((p.rows == 32) == ((int64_t)max_q * share <= 32));
+                CHECK(p.rows == 32 || p.rows == 128 || (p.rows == 256 && dim == 128));  // what is instantiated
+                CHECK((int64_t)p.row_blocks * p.rows >= (int64_t)max_q * share);
+                CHECK((int64_t)p.row_blocks * heads * seqs * 2 * p.rows < (int64_t(1) << 31));  // threads of the grid, at most
                 CHECK(p.group >= 8 && (int64_t)p.group * p.row_blocks < (int64_t(1) << 30));
                 CHECK(p.chunk > 0 && p.chunk % i4s::kPromptKeys == 0);
                 CHECK(p.splits >= 1 && p.splits <= i4s::kMaxPromptSplits);

@@ -460,6 +460,30 @@ def test_attention_of_many_pairs(i4s, dim, dtype):
     check_attention(q, k, v, starts, out, None, True, dim ** -0.5, dtype)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_attention_of_large_blocks(i4s, dtype):
+    """Enough long rows for the largest blocks, and short, empty and odd sequences beside them; then values that are not
+    finite where tokens do not see them."""
+    say("large blocks", dtype)
+    rng = np.random.default_rng(16)
+    lengths = [(1100, 1100), (3, 0), (40, 7), (300, 900), (1, 1), (256, 256), (257, 300)]
+    q, k, v, starts = packed(rng, lengths, 8, 4, 128, dtype)
+    outs = []
+    for causal in (True, False):
+        lse = torch.empty(q.shape[:2], device="cuda")
+        outs.append(i4s.prompt_attention(q, k, v, *starts, max_q=1100, max_k=1100, causal=causal, lse=lse))
+        check_attention(q, k, v, starts, outs[-1], lse, causal, 128 ** -0.5, dtype)
+    again = i4s.prompt_attention(q, k, v, *starts, max_q=1100, max_k=1100)
+    assert torch.equal(again, outs[0])
+    k[1090, 3], v[700, 5], v[1099, 2, 60:] = float("nan"), float("inf"), float("nan")
+    out = i4s.prompt_attention(q, k, v, *starts, max_q=1100, max_k=1100)
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+    hit[1090:1100, 12:16], hit[700:1100, 20:24], hit[1099, 8:12] = True, True, True
+    assert torch.equal(out[~hit], outs[0][~hit])
+    assert out[1090:1100, 12:16].isnan().all() and (out[700:1100, 20:24] == float("inf")).all()
+    assert out[1099, 8:12, 60:].isnan().all() and torch.equal(out[1099, 8:12, :60], outs[0][1099, 8:12, :60])
+
+
 @pytest.mark.parametrize("max_k", [0, 1, 1000, 3001])
 @pytest.mark.parametrize("tokens", [1, 20, 100])
 def test_attention_split_over_blocks(i4s, tokens, max_k):
