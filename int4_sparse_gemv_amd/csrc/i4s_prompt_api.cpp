@@ -177,26 +177,28 @@ PromptPlan prompt_plan(const i4s_prompt_args &a) {
   PromptPlan p{};
   const int64_t rows = (int64_t)a.max_q * (a.q_heads / a.kv_heads);
   const int64_t pairs = (int64_t)a.kv_heads * (a.num_seqs > 0 ? a.num_seqs : 1), large = (rows + 255) / 256;
-  // Blocks of 32 rows where those are all; of 256 (head dimension 128) where a pair
-  // has many and all of them are some rounds of the 256 compute units; else of 128.
-  // Us, 256 / 128: 8191 tokens x 40 heads 689 / 706, x 32 553 / 595; 4096 x 56 (896
-  // blocks of 256) 290 / 296, x 40 (640) 219 / 210; 16 x 1024 x 40 (four a pair) 402 /
-  // 382; head dimension 64, 4096 x 40 133 / 120.
-  p.rows = rows <= kPromptRows ? kPromptRows
-           : a.head_dim == 128 && large >= 16 && pairs * large >= 896 ? 8 * kPromptRows : 4 * kPromptRows;
-  p.row_blocks = (int32_t)((rows + p.rows - 1) / p.rows);
+  // Blocks of 32 rows where those are all; of 256 (head dimension 128) for long keys,
+  // where their ends weigh little, and some rounds of the 256 compute units; else 128.
+  // Us, 256 / 128: 8191 tokens x 40 heads 670 / 695, x 16 (512 blocks of 256) 269 / 298;
+  // 16384 x 16 1001 / 1045; 4096 x 64 297 / 306, x 40 205 / 195; 16 x up to 2047 tokens,
+  // 8 x 4 heads 347 / 332, x up to 1023 151 / 123; head dimension 64, 4096 x 40 133 / 117.
   const int64_t len = a.max_k > 0 && a.max_k < a.num_keys ? a.max_k : a.num_keys;
+  p.rows = rows <= kPromptRows ? kPromptRows
+           : a.head_dim == 128 && len >= 6144 && pairs * large >= 448 ? 8 * kPromptRows : 4 * kPromptRows;
+  p.row_blocks = (int32_t)((rows + p.rows - 1) / p.rows);
   const int64_t units = p.row_blocks * pairs;
   // Pairs of sequence and KV head that run together: as many as keep their keys in
   // the L2s, but enough that long rows of one are done next to short ones of others.
-  // Us, groups of 1 / 20 / 40 / all pairs: 16 x up to 2047 tokens, 8 x 4 heads (128
-  // pairs of 64 blocks) 395 / 385 / 387 / 494; 8191 tokens, 40 heads 821 / 789 / 783 / 803.
+  // Us, for 8 / 160 / 320 blocks of an XCD and all: 16 x up to 2047 tokens, 8 x 4 heads
+  // (blocks of 256) 359 / 369 / 446 / 496; 8191 tokens, 40 heads 761 / 697 / 698 / 698; 16 x 1024 tokens,
+  // 40 heads 429 / 385 / 397 / 442.
   p.group = 8 * ((160 + p.row_blocks - 1) / p.row_blocks);
   // The keys in pieces for about two blocks of 128 rows a compute unit, or one of
   // 32, but none shorter than 512 keys: partial results are fp32 and need a second
-  // launch.  Us, for 256 / 512 / 1024 blocks: 65536 keys, 8 x 4 rows 60 / 60 / 76;
-  // 128 tokens behind 32767, 8 x 4 heads 110 / 102 / 117.  512 tokens, 40 heads in one
-  // piece / two of 256 keys 25 / 52.
+  // launch.  Us, for half as many / these / twice as many: 65536 keys, 8 x 4 rows 63 /
+  // 50 / 53; 128 tokens behind 32767, 8 x 4 heads 101 / 95 / 108; 4 x 16 behind 8191
+  // 43 / 46 / 47.  512 tokens, 40 heads in one piece / two of 256 keys 26 / 53; 1024
+  // tokens, 8 heads in pieces of 512 / 256 35 / 30.
   const int64_t want = clamp_to<int64_t>((p.rows == kPromptRows ? 256 : 512) / units, 1, len > 512 ? (len + 511) / 512 : 1);
   const int64_t per = clamp_to<int64_t>((len + want * kPromptKeys - 1) / (want * kPromptKeys), 1, (1 << 30) / kPromptKeys);
   p.chunk = (int32_t)(per * kPromptKeys);

@@ -25,13 +25,14 @@
 //
 // Long prompts are bound by the matrix cores, the LDS that feeds them (every wave
 // reads all keys and values for its 32 rows: half of the LDS's cycles) and power.
-// 8191 tokens, 40 heads of 128: 1231 us without the causal mask = 1.12 PFLOP/s, 689
+// 8191 tokens, 40 heads of 128: 1231 us without the causal mask = 1.12 PFLOP/s, 665
 // with it; a large matrix product of the library reaches 1.15, matrix instructions
 // alone 1.9.  Us without the mask, step by step: operands read by the instruction that
 // uses them 1400; four instructions ahead, V's first ones before the softmax, 1300
 // (head dimension 256: 224, 178; two ahead 204; six the same as four); blocks of 256
 // rows in two halves, one in its softmax while the other multiplies, 1275, with the
-// loads' issue in the softmax 1231.  Tried and no faster: wave priorities for either
+// loads' issue in the softmax 1231.  The tiles that a mask cuts, 512 tokens x 40 heads
+// x 40 prompts: with registers that spill 405, with less held from one to the next 326.  Tried and no faster: wave priorities for either
 // part, waits between matrix instructions, 32-key tiles with the next scores ahead
 // of this softmax; 64 rows a wave spill.
 //
@@ -263,32 +264,43 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
     }
   };
 
-  f16_t o[NC], less;  // less: minus the row's reference, in every register
+  f16_t o[NC], every;  // every: `less` in each register
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[c][e] = 0;
 #pragma unroll
-  for (int e = 0; e < 16; ++e) less[e] = 0;
-  float sum = 0;
+  for (int e = 0; e < 16; ++e) every[e] = 0;
+  float sum = 0, less = 0;  // less: minus the row's reference
   bool fresh = true;
-
-  // V's operand: channels 32 c + li of the keys 16 x + 4 lh + 0..3 and + 8
-  const int tr_row = (lane & 15) / 4 + 4 * lh, tr_piece = (lane >> 4 & 1) * 2 + (lane & 3) / 2;
-  auto read_v = [&](const char *tile, int c, int x) {
-    u4_t r;
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const int key = 16 * x + 8 * y + tr_row;
-      const char *p = tile + key * 2 * D + L::v_piece(tr_row, 4 * c + tr_piece) * 16 + (lane & 1) * 8;
-      const u2_t w = read_transposed((lds_s4)p);
-      r[2 * y] = w.x, r[2 * y + 1] = w.y;
-    }
-    return r;
-  };
 
   auto step = [&](int key, int stage, auto MASKED, auto &&load) {
     constexpr bool masked = decltype(MASKED)::value;
+    // In the masked tiles addresses are worked out anew: kept from one to the next they
+    // would not fit the registers.
+    int own = lane;
+    if constexpr (masked) asm volatile("" : "+v"(own));
+    const int li = own & 31, lh = own >> 5;
+    // V's operand: channels 32 c + li of the keys 16 x + 4 lh + 0..3 and + 8
+    const int tr_row = (own & 15) / 4 + 4 * lh, tr_piece = (own >> 4 & 1) * 2 + (own & 3) / 2;
+    auto read_v = [&](const char *tile, int c, int x) {
+      u4_t r;
+  #pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int key = 16 * x + 8 * y + tr_row;
+        const char *p = tile + key * 2 * D + L::v_piece(tr_row, 4 * c + tr_piece) * 16 + (own & 1) * 8;
+        const u2_t w = read_transposed((lds_s4)p);
+        r[2 * y] = w.x, r[2 * y + 1] = w.y;
+      }
+      return r;
+    };
+    f16_t start = every;
+    if constexpr (masked) {
+      float one = less;
+      asm volatile("" : "+v"(one));
+#pragma unroll
+      for (int e = 0; e < 16; ++e) start[e] = one;
+    }
     // Operands are read kAhead instructions ahead of the one that uses them, V's
     // first ones before the softmax.
     constexpr int kScores = NK * NQ, kValues = 2 * NK * NC;
@@ -303,7 +315,7 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
     issue_fence();
 #pragma unroll
     for (int i = 0; i < kScores; ++i) {
-      p[i % NK] = T::mfma(ahead[i % kAhead], q[i / NK], i < NK ? less : p[i % NK]);
+      p[i % NK] = T::mfma(ahead[i % kAhead], q[i / NK], i < NK ? start : p[i % NK]);
       if (i + kAhead < kScores) ahead[i % kAhead] = read_k(i + kAhead);
       issue_fence();
     }
@@ -335,8 +347,11 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
       const float f = grown && fresh ? 0.0f : __builtin_amdgcn_exp2f(-by * a.scale_log2);
       fresh = fresh && !grown;
       sum *= f;
+      less -= by;
+      if constexpr (!masked) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) less[e] -= by;
+        for (int e = 0; e < 16; ++e) every[e] -= by;
+      }
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -413,15 +428,20 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
           v[e] = keep, plus[e] = up, minus[e] = down;
         }
         o[c] = T::mfma(v, weight, o[c]);
+        issue_fence();
         f16_t zero;
 #pragma unroll
         for (int e = 0; e < 16; ++e) zero[e] = 0;
-        const f16_t ups = T::mfma(plus, sees, zero), downs = T::mfma(minus, sees, zero);
+        f16_t sum = T::mfma(plus, sees, zero);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          if (ups[e] > 0) o[c][e] += INFINITY;
-          if (downs[e] > 0) o[c][e] -= INFINITY;
-        }
+        for (int e = 0; e < 16; ++e)
+          if (sum[e] > 0) o[c][e] += INFINITY;
+        issue_fence();
+        sum = T::mfma(minus, sees, zero);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (sum[e] > 0) o[c][e] -= INFINITY;
+        issue_fence();
       }
     }
   };
@@ -500,7 +520,7 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
     __syncthreads();
     float *const ml = reinterpret_cast<float *>(lds), *const rows_at = ml + kWaves * kPromptRows * 2;
     if (lh == 0) {
-      ml[(wave * kPromptRows + li) * 2] = fresh ? -FLT_MAX : -less[0];
+      ml[(wave * kPromptRows + li) * 2] = fresh ? -FLT_MAX : -less;
       ml[(wave * kPromptRows + li) * 2 + 1] = sum;
     }
 #pragma unroll
@@ -551,7 +571,7 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
         *reinterpret_cast<f4_t *>(to + 32 * c + 8 * e) =
             f4_t{o[c][4 * e], o[c][4 * e + 1], o[c][4 * e + 2], o[c][4 * e + 3]};
     if (lh == 0) {
-      a.part_ml[2 * at] = fresh ? -FLT_MAX : -less[0];
+      a.part_ml[2 * at] = fresh ? -FLT_MAX : -less;
       a.part_ml[2 * at + 1] = sum;
     }
     return;
@@ -564,7 +584,7 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
     for (int e = 0; e < 4; ++e)
       *reinterpret_cast<u2_t *>(to + 32 * c + 8 * e) =
           u2_t{two<T>(o[c][4 * e] * f, o[c][4 * e + 1] * f), two<T>(o[c][4 * e + 2] * f, o[c][4 * e + 3] * f)};
-  if (a.lse && lh == 0) a.lse[out_row] = lse_of(-less[0], sum, a.scale_log2, T::kHeadroom);
+  if (a.lse && lh == 0) a.lse[out_row] = lse_of(-less, sum, a.scale_log2, T::kHeadroom);
 }
 
 // Joins the pieces of a row: a block a row.  Its threads take the pieces'

@@ -466,22 +466,24 @@ def test_attention_of_large_blocks(i4s, dtype):
     finite where tokens do not see them."""
     say("large blocks", dtype)
     rng = np.random.default_rng(16)
-    lengths = [(1100, 1100), (3, 0), (40, 7), (300, 900), (1, 1), (256, 256), (257, 300)]
-    q, k, v, starts = packed(rng, lengths, 8, 4, 128, dtype)
+    lengths = [(300, 6200), (3, 0), (40, 7), (33, 900), (1, 1), (256, 256), (257, 300)] + [(n, n) for n in range(38)]
+    q, k, v, starts = packed(rng, lengths, 2, 4, 128, dtype)
     outs = []
     for causal in (True, False):
         lse = torch.empty(q.shape[:2], device="cuda")
-        outs.append(i4s.prompt_attention(q, k, v, *starts, max_q=1100, max_k=1100, causal=causal, lse=lse))
+        outs.append(i4s.prompt_attention(q, k, v, *starts, max_q=300, max_k=6200, causal=causal, lse=lse))
         check_attention(q, k, v, starts, outs[-1], lse, causal, 128 ** -0.5, dtype)
-    again = i4s.prompt_attention(q, k, v, *starts, max_q=1100, max_k=1100)
+    again = i4s.prompt_attention(q, k, v, *starts, max_q=300, max_k=6200)
     assert torch.equal(again, outs[0])
-    k[1090, 3], v[700, 5], v[1099, 2, 60:] = float("nan"), float("inf"), float("nan")
-    out = i4s.prompt_attention(q, k, v, *starts, max_q=1100, max_k=1100)
+    k[6190, 1], v[6100, 0], v[6199, 1, 60:] = float("nan"), float("inf"), float("nan")
+    out = i4s.prompt_attention(q, k, v, *starts, max_q=300, max_k=6200)
     hit = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
-    hit[1090:1100, 12:16], hit[700:1100, 20:24], hit[1099, 8:12] = True, True, True
+    hit[290:300, 4:], hit[200:300, :4] = True, True
     assert torch.equal(out[~hit], outs[0][~hit])
-    assert out[1090:1100, 12:16].isnan().all() and (out[700:1100, 20:24] == float("inf")).all()
-    assert out[1099, 8:12, 60:].isnan().all() and torch.equal(out[1099, 8:12, :60], outs[0][1099, 8:12, :60])
+    assert out[290:300, 4:].isnan().all() and (out[200:300, :4] == float("inf")).all()
+    k[6190, 1] = 0
+    plain = i4s.prompt_attention(q, k, v, *starts, max_q=300, max_k=6200)
+    assert plain[299, 4:, 60:].isnan().all() and plain[299, 4:, :60].isfinite().all() and plain[:299, 4:].isfinite().all()
 
 
 @pytest.mark.parametrize("max_k", [0, 1, 1000, 3001])
