@@ -152,8 +152,8 @@ typedef struct i4s_prompt_args {
   int32_t causal;            /* 0 or 1                                       */
   float scale;               /* > 0, finite                                  */
   int32_t reserved;          /* 0                                            */
-  const int32_t *q_start;    /* [num_seqs+1], non-decreasing                 */
-  const int32_t *k_start;    /* [num_seqs+1], non-decreasing                 */
+  const int32_t *q_start;    /* [num_seqs+1], non-decreasing; both NULL: one */
+  const int32_t *k_start;    /* sequence of all tokens and keys, num_seqs 1  */
   void *out;                 /* [num_tokens][q_heads][D] contiguous, 16-byte */
                              /* aligned                                      */
   float *lse;                /* [num_tokens][q_heads], natural logarithm of  */

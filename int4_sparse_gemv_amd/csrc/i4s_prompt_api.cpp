@@ -352,8 +352,10 @@ i4s_status i4s_prompt_attention(const i4s_prompt_args *a, void *stream) {
     return fail(I4S_ERR_INVALID_ARGUMENT, "q or out is NULL or not 16-byte aligned");
   if (a->num_keys && (!a->k || !aligned(a->k, 16) || !a->v || !aligned(a->v, 16)))
     return fail(I4S_ERR_INVALID_ARGUMENT, "k or v is NULL or not 16-byte aligned");
-  if (!a->q_start || !aligned(a->q_start, 4) || !a->k_start || !aligned(a->k_start, 4) || !aligned(a->lse, 4))
-    return fail(I4S_ERR_INVALID_ARGUMENT, "q_start or k_start is NULL, or one of them or lse is not 4-byte aligned");
+  if (!a->q_start != !a->k_start || (!a->q_start && a->num_seqs != 1))
+    return fail(I4S_ERR_INVALID_ARGUMENT, "q_start or k_start is NULL; both may be for num_seqs=1, not %d", a->num_seqs);
+  if (!aligned(a->q_start, 4) || !aligned(a->k_start, 4) || !aligned(a->lse, 4))
+    return fail(I4S_ERR_INVALID_ARGUMENT, "q_start, k_start or lse is not 4-byte aligned");
   const i4s::PromptPlan p = i4s::prompt_plan(*a);
   if (p.workspace_bytes) {
     if (!a->workspace || !aligned(a->workspace, 16))
@@ -370,8 +372,8 @@ i4s_status i4s_prompt_attention(const i4s_prompt_args *a, void *stream) {
       {a->q, extent(a->num_tokens, a->q_token_stride, a->q_heads, a->q_head_stride, a->head_dim), "q"},
       {a->k, extent(a->num_keys, a->k_token_stride, a->kv_heads, a->k_head_stride, a->head_dim), "k"},
       {a->v, extent(a->num_keys, a->v_token_stride, a->kv_heads, a->v_head_stride, a->head_dim), "v"},
-      {a->q_start, 4ull * (a->num_seqs + 1), "q_start"},
-      {a->k_start, 4ull * (a->num_seqs + 1), "k_start"}};
+      {a->q_start, a->q_start ? 4ull * (a->num_seqs + 1) : 0, "q_start"},
+      {a->k_start, a->k_start ? 4ull * (a->num_seqs + 1) : 0, "k_start"}};
   st = check_spans(outs, ins);
   if (st != I4S_OK) return st;
   st = check_device();

@@ -142,6 +142,7 @@ struct Sequence {
   int q0, nq, k0, nk;
 };
 __device__ inline Sequence sequence_of(const PromptKernelArgs &a, int seq) {
+  if (!a.q_start) return {0, a.num_tokens, 0, a.num_keys};
   Sequence s;
   s.q0 = clamp_to(a.q_start[seq], 0, a.num_tokens);
   s.nq = clamp_to(a.q_start[seq + 1], s.q0, a.num_tokens) - s.q0;

@@ -101,7 +101,7 @@ struct PromptKernelArgs {
   int32_t num_tokens, num_keys, num_seqs, max_q, causal;
   int32_t row_blocks, group, splits, chunk;
   float scale_log2;
-  const int32_t *q_start, *k_start;
+  const int32_t *q_start, *k_start;  // null: one sequence
   void *out;
   float *lse;
   float *part_o;   // [splits][num_tokens * q_heads][D]

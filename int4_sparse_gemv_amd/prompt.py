@@ -162,13 +162,6 @@ def mx_product(x, w: MXTensor, dtype=None, out=None):
     return out
 
 
-def _whole(n, device):
-    """[0, n]: where the one sequence begins and ends."""
-    if n == 0:
-        return torch.zeros(2, dtype=torch.int32, device=device)
-    return torch.arange(0, n + 1, n, dtype=torch.int32, device=device)
-
-
 @functools.lru_cache(maxsize=4096)
 def _attention_workspace(dtype, dim, heads, kv_heads, tokens, keys, n, max_q, max_k) -> int:
     """Bytes that a call of these sizes needs."""
@@ -213,15 +206,16 @@ def prompt_attention(q, k, v, q_start=None, k_start=None, max_q: Optional[int] =
     if q_start is None:
         if k_start is not None:
             raise ValueError("k_start needs q_start")
-        q_start = _whole(tokens, q.device)
-        k_start = q_start if keys == tokens else _whole(keys, q.device)
-    if k_start is None:
-        k_start = q_start
-    n = q_start.numel() - 1
-    if n < 0:
-        raise ValueError("q_start must be int32 [sequences + 1]")
-    _check(q_start, torch.int32, (n + 1,), index, "q_start")
-    _check(k_start, torch.int32, (n + 1,), index, "k_start")
+        n, q_at, k_at = 1, None, None
+    else:
+        n = q_start.numel() - 1
+        if n < 0:
+            raise ValueError("q_start must be int32 [sequences + 1]")
+        if k_start is None:
+            k_start = q_start
+        _check(q_start, torch.int32, (n + 1,), index, "q_start")
+        _check(k_start, torch.int32, (n + 1,), index, "k_start")
+        q_at, k_at = q_start.data_ptr(), k_start.data_ptr()
     if max_q is None:
         max_q = max(tokens, 1)
     if out is None:
@@ -236,7 +230,7 @@ def prompt_attention(q, k, v, q_start=None, k_start=None, max_q: Optional[int] =
     st = _call(P.i4s_prompt_attention, index, P.i4s_prompt_args(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), *_strides(q, "q"), *_strides(k, "k"), *_strides(v, "v"), dtype, dim, heads,
         kv_heads, tokens, keys, n, max_q, max_k, 1 if causal else 0, dim ** -0.5 if scale is None else scale, 0,
-        q_start.data_ptr(), k_start.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+        q_at, k_at, out.data_ptr(), None if lse is None else lse.data_ptr(),
         None if ws is None else ws.data_ptr(), nbytes))
     if st:
         B.check(st, "i4s_prompt_attention")

@@ -143,6 +143,16 @@ void attention(i4s_status expect) {
               }
 }
 
+void one_sequence(i4s_status expect) {  // needs no starts
+  i4s_prompt_args a{};
+  a.q = fake<void>(100), a.k = fake<void>(200), a.v = fake<void>(300), a.out = fake<void>(400);
+  a.head_dim = 64, a.q_heads = a.kv_heads = 1, a.num_tokens = a.num_keys = 9, a.max_q = 9, a.num_seqs = 1, a.scale = 1;
+  CHECK(i4s_prompt_attention(&a, nullptr) == expect);
+  if (expect == I4S_OK) CHECK(!prompt_stub_attention().q_start && !prompt_stub_attention().k_start);
+  a.num_seqs = 2;
+  CHECK(i4s_prompt_attention(&a, nullptr) == I4S_ERR_INVALID_ARGUMENT);
+}
+
 void nothing_to_do() {
   const int before = prompt_stub_launches();
   const i4s_mx none = {0, 64, nullptr, nullptr}, w = mx_of(20, 64, 1);
@@ -157,7 +167,7 @@ void nothing_to_do() {
   a.head_dim = 64, a.q_heads = a.kv_heads = 1, a.max_q = 1, a.scale = 1;
   CHECK(i4s_prompt_attention(&a, nullptr) == I4S_OK);
   a.num_tokens = 5;
-  CHECK(i4s_prompt_attention(&a, nullptr) == I4S_OK);
+  CHECK(i4s_prompt_attention(&a, nullptr) == I4S_OK);  // no sequences
   CHECK(prompt_stub_launches() == before);
 }
 
@@ -172,6 +182,7 @@ int main(int argc, char **argv) {
   format(expect);
   products(expect);
   attention(expect);
+  one_sequence(expect);
   nothing_to_do();
   if (g_fails) return 1;
   std::printf("ok %d checks\n", g_checks);

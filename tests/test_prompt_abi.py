@@ -172,7 +172,7 @@ def attention(**kw):
     dict(num_tokens=(1 << 30) + 1), dict(num_keys=-1), dict(num_keys=(1 << 30) + 1), dict(num_seqs=-1), dict(num_seqs=65536),
     dict(max_q=0), dict(max_q=(1 << 24) + 1), dict(max_k=-1), dict(causal=2), dict(causal=-1), dict(scale=0.0), dict(scale=-1.0),
     dict(scale=float("nan")), dict(scale=float("inf")), dict(reserved=1), dict(q_start=None), dict(q_start=4 * GIB + 2),
-    dict(k_start=None), dict(k_start=5 * GIB + 1), dict(out=None), dict(out=6 * GIB + 8), dict(lse=7 * GIB + 2), dict(out=GIB),
+    dict(k_start=None), dict(k_start=5 * GIB + 1), dict(q_start=None, k_start=None), dict(out=None), dict(out=6 * GIB + 8), dict(lse=7 * GIB + 2), dict(out=GIB),
     dict(out=2 * GIB), dict(out=3 * GIB), dict(out=4 * GIB), dict(lse=6 * GIB), dict(lse=5 * GIB), dict(workspace=None),
     dict(workspace=8 * GIB + 4), dict(workspace=6 * GIB), dict(workspace=GIB), dict(num_seqs=65535, max_q=1 << 13)])
 def test_attention_refuses(lib, change):
