@@ -134,10 +134,10 @@ namespace i4s {
 MxProductPlan mx_product_plan(int32_t tokens, int32_t rows, int32_t cols, bool x_given) {
   MxProductPlan p{};
   // 16-bit tokens: quantized by every block of the product while they are few,
-  // else by a launch of its own.  Us in graphs, on the way / before (13824 x 5120): 4
-  // tokens 9.6 / 12.7, 8: 10.9 / 12.8, 16: 15.3 / 13.0; 4096 x 4096, 16 tokens: 7.3 / 7.0;
-  // 4096 x 11008: 4: 7.8 / 10.2, 8: 11.4 / 10.3.
-  p.quantize = !x_given && (tokens > 16 || (int64_t)tokens * cols >= 1 << 16);
+  // else by a launch of its own.  Us in graphs, on the way / before: 13824 x 5120, 8
+  // tokens 9.6 / 13.5, 16: 13.1 / 14.0; 4096 x 4096, 16: 6.7 / 8.7; 22016 x 4096, 16: 16.2 /
+  // 15.8; 4096 x 11008, 8: 9.3 / 11.0, 16: 15.0 / 11.7.
+  p.quantize = !x_given && (tokens > 16 || (int64_t)tokens * cols >= 3 << 15);
   p.token_tiles = (tokens + 15) / 16;
   // Blocks of eight waves and 1, 2 or (where each quantizes the tokens) 4 weight
   // tiles, about one or two for each of the 256 compute units; beyond, and for
@@ -145,8 +145,8 @@ MxProductPlan mx_product_plan(int32_t tokens, int32_t rows, int32_t cols, bool x
   // sums and so must not depend on how the tokens are given.
   // Us, 16 quantized tokens, tiles x waves 1x8 / 2x8 / 2x4: 4096 x 4096 3.7 / 4.1 / 4.3;
   // 5120 x 13824 11.9 / 10.6 / 10.8; 13824 x 5120 10.5 / 9.8 / 9.7, 64 tokens 21.4 / 17.8
-  // / 13.5; 50257 x 4096, 48 tokens 45 / 42 / 30.  8 tokens quantized on the way,
-  // 2x8 / 4x8 / 2x4: 13824 x 5120 14.5 / 10.9 / 12.8; 50257 x 4096 32 / 31 / 26.
+  // / 13.5; 50257 x 4096, 48 tokens 45 / 42 / 30.  8 tokens quantized on the way, four at
+  // a time, 2x8 / 4x8 / 2x4: 13824 x 5120 14.5 / 10.9 / 12.8; 50257 x 4096 32 / 31 / 26.
   const int32_t tiles = mx_row_tiles(rows);
   p.row_tiles = tiles <= 256 ? 1 : 2;
   p.waves = tiles <= (p.token_tiles == 1 ? 1024 : 512) ? 8 : 4;

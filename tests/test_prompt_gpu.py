@@ -182,7 +182,8 @@ def check_product(i4s, x, w, y, dtype):
 SIZES = [(1, 16, 32), (1, 4096, 4096), (2, 33, 96), (5, 1000, 512), (15, 77, 1056), (16, 256, 4096), (17, 100, 288),
          (31, 513, 768), (33, 48, 1024), (50, 300, 2080), (64, 129, 512), (65, 127, 256), (65, 1, 64), (100, 257, 544),
          (128, 128, 128), (129, 400, 1312), (257, 640, 992), (300, 31, 4096), (511, 513, 800), (3, 8300, 512), (15, 16400, 224),
-         (16, 9000, 4096)]
+         (16, 9000, 4096),
+         (16, 500, 8224), (11, 129, 8192), (9, 4100, 5120)]
 
 
 @pytest.mark.parametrize("tokens,rows,cols", SIZES)
