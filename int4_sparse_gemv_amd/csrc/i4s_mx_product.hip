@@ -110,7 +110,7 @@ template <typename X, typename Y, int RT, int NT, int WAVES, bool ONCE>
 __global__ __launch_bounds__(WAVES * 64) void mx_few_kernel(MxProductKernelArgs a) {
   constexpr bool kFused = !std::is_same<X, Given>::value;
   constexpr int kBatch = X::kBatch;
-  __shared__ float sums[WAVES][RT * NT][64][4];
+  __shared__ float sums[WAVES][RT * NT][72][4];  // 16 lanes and two empty places: rows read together lie in other banks
   __shared__ uint32_t own[kFused ? WAVES : 1][kFused ? 5 : 1][64][4];  // four tiles, and in the fifth place the scales
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
   const int steps = mx_steps(a.cols), groups = mx_groups(a.cols), tiles = mx_row_tiles(a.rows);
@@ -181,13 +181,13 @@ __global__ __launch_bounds__(WAVES * 64) void mx_few_kernel(MxProductKernelArgs 
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) *reinterpret_cast<f4_t *>(sums[wave][r * NT + n][lane]) = acc[r][n];
+    for (int n = 0; n < NT; ++n) *reinterpret_cast<f4_t *>(sums[wave][r * NT + n][lane + lane / 16 * 2]) = acc[r][n];
   __syncthreads();
   // neighbouring rows of a token go out together
   typename Y::type *y = static_cast<typename Y::type *>(a.y);
   for (int at = threadIdx.x; at < RT * NT * 256; at += WAVES * 64) {
     const int row = at % (16 * RT), token = at / (16 * RT);
-    const int r = row / 16, n = token / 16, from = row % 16 / 4 * 16 + token % 16;
+    const int r = row / 16, n = token / 16, from = row % 16 / 4 * 18 + token % 16;
     float s = 0;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) s += sums[w][r * NT + n][from][row % 4];
