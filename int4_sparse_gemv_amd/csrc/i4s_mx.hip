@@ -12,23 +12,21 @@
 // written where they are read back, past the caches (non-temporal): they are used
 // once.  Quantizing and reading back 13824 x 5120: 67 us for 358 MB = 5.4 TB/s
 // (through the caches 79), 2000 x 11008 22 us (31); a large copy runs at 4.8 TB/s.
+// Us for blocks of one / two / four waves, 64 x 11008: 9.1 / 9.6 / 10.3, large ones alike.
 
 #include "i4s_mx_common.h"
 
 namespace i4s {
 namespace {
 
-constexpr int kMxThreads = 256;
-constexpr int kMxWavesPerBlock = kMxThreads / 64;
+constexpr int kMxThreads = 64;  // blocks of a wave: few rows reach more compute units
 
 template <typename X>
 __global__ __launch_bounds__(kMxThreads) void mx_quantize_kernel(MxQuantizeArgs a) {
   const int groups = mx_groups(a.cols), steps = mx_steps(a.cols);
-  const int64_t unit = (int64_t)blockIdx.x * kMxWavesPerBlock + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int64_t tile = unit / groups;
-  const int group = (int)(unit - tile * groups);
-  if (tile >= mx_row_tiles(a.rows)) return;
-  const int lane = threadIdx.x & 63, col = lane % 16 * 8, sub = lane / 16, quad = lane % 4, block = lane % 16 / 4;
+  const int64_t tile = blockIdx.x / (unsigned)groups;
+  const int group = blockIdx.x % (unsigned)groups;
+  const int lane = threadIdx.x, col = lane % 16 * 8, sub = lane / 16, quad = lane % 4, block = lane % 16 / 4;
   const int left = steps - 4 * group < 4 ? steps - 4 * group : 4;  // tiles of this group
   const uint16_t *x = static_cast<const uint16_t *>(a.x);
   u4_t v[4][4];
@@ -87,11 +85,9 @@ template <typename Y>
 __global__ __launch_bounds__(kMxThreads) void mx_read_kernel(MxReadArgs a) {
   typedef typename Y::type T;
   const int groups = mx_groups(a.cols), steps = mx_steps(a.cols);
-  const int64_t unit = (int64_t)blockIdx.x * kMxWavesPerBlock + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int64_t tile = unit / groups;
-  const int group = (int)(unit - tile * groups);
-  if (tile >= mx_row_tiles(a.rows)) return;
-  const int lane = threadIdx.x & 63, col = lane % 16 * 8, sub = lane / 16, quad = lane % 4, block = lane % 16 / 4;
+  const int64_t tile = blockIdx.x / (unsigned)groups;
+  const int group = blockIdx.x % (unsigned)groups;
+  const int lane = threadIdx.x, col = lane % 16 * 8, sub = lane / 16, quad = lane % 4, block = lane % 16 / 4;
   const uint8_t *vals = a.vals + (tile * steps + 4 * group) * kMxTileBytes + block * 256 + quad * 4;
   const uint8_t *scales = a.scales + (tile * groups + group) * kMxGroupBytes + block * 64;
   T *out = static_cast<T *>(a.out);
@@ -119,12 +115,10 @@ __global__ __launch_bounds__(kMxThreads) void mx_read_kernel(MxReadArgs a) {
 
 }  // namespace
 
-static int64_t mx_blocks(int32_t rows, int32_t cols) {
-  return ((int64_t)mx_row_tiles(rows) * mx_groups(cols) + kMxWavesPerBlock - 1) / kMxWavesPerBlock;
-}
+static dim3 mx_blocks(int32_t rows, int32_t cols) { return dim3((unsigned)((int64_t)mx_row_tiles(rows) * mx_groups(cols))); }
 
 hipError_t launch_mx_quantize(const MxQuantizeArgs &a, int32_t dtype, hipStream_t stream) {
-  const dim3 grid((unsigned)mx_blocks(a.rows, a.cols));
+  const dim3 grid = mx_blocks(a.rows, a.cols);
   if (dtype == I4S_F16)
     hipLaunchKernelGGL(mx_quantize_kernel<HalfX>, grid, dim3(kMxThreads), 0, stream, a);
   else
@@ -133,7 +127,7 @@ hipError_t launch_mx_quantize(const MxQuantizeArgs &a, int32_t dtype, hipStream_
 }
 
 hipError_t launch_mx_read(const MxReadArgs &a, int32_t dtype, hipStream_t stream) {
-  const dim3 grid((unsigned)mx_blocks(a.rows, a.cols));
+  const dim3 grid = mx_blocks(a.rows, a.cols);
   if (dtype == I4S_F16)
     hipLaunchKernelGGL(mx_read_kernel<AsHalf>, grid, dim3(kMxThreads), 0, stream, a);
   else if (dtype == I4S_BF16)

@@ -28,7 +28,7 @@ i4s_status check_mx_shape(int32_t rows, int32_t cols) {
   if (rows < 0 || rows > kMxMaxRows) return fail(I4S_ERR_INVALID_ARGUMENT, "rows=%d must be in [0, 2^24]", rows);
   if (cols < 32 || cols > kMxMaxCols || cols % 32)
     return fail(I4S_ERR_INVALID_ARGUMENT, "cols=%d must be a multiple of 32 in [32, 2^20]", cols);
-  // four waves a block, each 16 rows x 512 columns
+  // a block of 64 threads takes 16 rows x 512 columns
   if ((int64_t)i4s::mx_row_tiles(rows) * i4s::mx_groups(cols) > 4 * kMaxBlocks)
     return fail(I4S_ERR_INVALID_ARGUMENT, "rows=%d times cols=%d must be below 2^38", rows, cols);
   return I4S_OK;

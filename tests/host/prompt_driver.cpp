@@ -37,8 +37,8 @@ void format(i4s_status expect) {
       CHECK(i4s_mx_sizes(rows, cols, &sz) == (fits ? I4S_OK : I4S_ERR_INVALID_ARGUMENT));
       if (!fits) continue;
       CHECK(sz.vals >= (uint64_t)rows * cols / 2 && sz.scales >= (uint64_t)rows * cols / 32);
-      // a block of four waves for each four groups: 32-bit grids of 256 threads
-      CHECK((int64_t)((rows + 15) / 16) * ((cols + 511) / 512) / 4 * 256 < (int64_t(1) << 32));
+      // a block of a wave for each: 32-bit grids
+      CHECK((int64_t)((rows + 15) / 16) * ((cols + 511) / 512) * 64 < (int64_t(1) << 32));
       const i4s_mx m = mx_of(rows, cols, 1);
       const int before = prompt_stub_launches();
       CHECK(i4s_mx_quantize(fake<void>(100), I4S_BF16, cols, &m, nullptr) == expect);
