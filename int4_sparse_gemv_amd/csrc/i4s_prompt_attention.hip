@@ -25,16 +25,17 @@
 //
 // Long prompts are bound by the matrix cores, the LDS that feeds them (every wave
 // reads all keys and values for its 32 rows: half of the LDS's cycles) and power.
-// 8191 tokens, 40 heads of 128: 1231 us without the causal mask = 1.12 PFLOP/s, 665
+// 8191 tokens, 40 heads of 128: 1231 us without the causal mask = 1.12 PFLOP/s, 670
 // with it; a large matrix product of the library reaches 1.15, matrix instructions
 // alone 1.9.  Us without the mask, step by step: operands read by the instruction that
 // uses them 1400; four instructions ahead, V's first ones before the softmax, 1300
 // (head dimension 256: 224, 178; two ahead 204; six the same as four); blocks of 256
 // rows in two halves, one in its softmax while the other multiplies, 1275, with the
-// loads' issue in the softmax 1231.  The tiles that a mask cuts, 512 tokens x 40 heads
-// x 40 prompts: with registers that spill 405, with less held from one to the next 326.  Tried and no faster: wave priorities for either
-// part, waits between matrix instructions, 32-key tiles with the next scores ahead
-// of this softmax; 64 rows a wave spill.
+// loads' issue in the softmax 1231.  The tiles that a mask cuts, 40 prompts of 512
+// tokens, 40 heads: with registers that spill 405, with less held from one to the next
+// 288.  Tried and no faster: wave priorities for either part, waits between matrix
+// instructions, 32-key tiles with the next scores ahead of this softmax, V's operands
+// ahead in masked tiles, their finite check shared among the waves; 64 rows a wave spill.
 //
 // 32 rows or fewer of a sequence and KV head (a token behind long keys) are bound
 // by memory: there each wave of a block has tiles of 32 keys of its own, two of
@@ -244,7 +245,7 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
   const int loader = FEW ? 0 : wave;
   char *const v_tiles = tiles + S::kStages * L::kBytes;
   // rows past the keys repeat the last: their scores are masked
-  auto load_k = [&](int key, int stage) {
+  auto load_k = [&](int key, int stage, int lane) {
     const int first = key < s.nk ? key : s.nk - 1, left = s.nk - 1 - first;
     const char *k0 = kb + (int64_t)first * k_step;
 #pragma unroll
@@ -254,7 +255,7 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
       copy16<FEW ? 2 : 0>(k0 + (uint32_t)(from * k_step + L::k_piece(r, p) * 16), tiles + stage * L::kBytes + at * 1024);
     }
   };
-  auto load_v = [&](int key, int stage) {
+  auto load_v = [&](int key, int stage, int lane) {
     const int first = key < s.nk ? key : s.nk - 1, left = s.nk - 1 - first;
     const char *v0 = vb + (int64_t)first * v_step;
 #pragma unroll
@@ -322,7 +323,7 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
     }
     if constexpr (PAIRED) {
       meet();  // the other half has its softmax behind it
-      load();
+      load(own);
     }
     if constexpr (!masked) {
 #pragma unroll
@@ -456,14 +457,14 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
     // While one half multiplies (a tile's probabilities with V, the next one's keys
     // with Q), the other works on its softmax, on the same four SIMDs.  Loads run
     // three tiles ahead of the keys' use, two of the values'.
-    auto load = [&]() {
-      load_k(key + 3 * kStride, (stage + 3) & 3);
-      load_v(key + 2 * kStride, stage ^ 2);
+    auto load = [&](int own) {
+      load_k(key + 3 * kStride, (stage + 3) & 3, own);
+      load_v(key + 2 * kStride, stage ^ 2, own);
     };
     auto turn = [&]() { key += kStride, stage = (stage + 1) & 3; };
     if (key < piece1) {
-      load_k(key, 0), load_k(key + kStride, 1), load_v(key, 0);
-      load_k(key + 2 * kStride, 2), load_v(key + kStride, 1);
+      load_k(key, 0, lane), load_k(key + kStride, 1, lane), load_v(key, 0, lane);
+      load_k(key + 2 * kStride, 2, lane), load_v(key + kStride, 1, lane);
       wait_loads<2 * S::kLoads>();
       meet();
       if (wave >= kWaves / 2) meet();
@@ -479,7 +480,7 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
         step(key, stage, std::true_type(), load);
       } else {
         meet();
-        load();
+        load(lane);
         wait_loads<2 * S::kLoads>();
         meet();
       }
@@ -488,8 +489,8 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
     if (piece0 < piece1 && wave < kWaves / 2) meet();
     wait_loads<0>();
   } else {
-    if (key < piece1) load_k(key, 0), load_v(key, 0);
-    auto next = [&]() {
+    if (key < piece1) load_k(key, 0, lane), load_v(key, 0, lane);
+    auto next = [&](int own) {
       wait_loads<0>();
       if constexpr (FEW) {
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the other stage is read
@@ -497,19 +498,21 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
       } else {
         meet();  // everybody's part of this step's tiles is here, and nobody reads the other stage
       }
-      if (key + kStride < piece1) load_k(key + kStride, stage ^ 1), load_v(key + kStride, stage ^ 1);
+      if (key + kStride < piece1) load_k(key + kStride, stage ^ 1, own), load_v(key + kStride, stage ^ 1, own);
     };
     auto turn = [&]() { key += kStride, stage ^= 1; };
 #pragma unroll 1
     while (key <= plain) {
-      next();
-      step(key, stage, std::false_type(), [] {});
+      next(lane);
+      step(key, stage, std::false_type(), [](int) {});
       turn();
     }
 #pragma unroll 1
     while (key < piece1) {
-      next();
-      if (key < any_sees) step(key, stage, std::true_type(), [] {});
+      int own = lane;
+      asm volatile("" : "+v"(own));
+      next(own);
+      if (key < any_sees) step(key, stage, std::true_type(), [](int) {});
       turn();
     }
   }
