@@ -170,7 +170,8 @@ i4s_status i4s_prompt_attention_workspace_size(const i4s_prompt_args *a /* host 
 /* The call.  Every row of out (and lse) that belongs to a sequence is written;
  * rows before q_start[0] and from q_start[num_seqs] on, and tokens of a
  * sequence past max_q, are left as they were.  A start outside [0, num_tokens]
- * (num_keys) is moved into it; a sequence that ends before it begins is empty.
+ * (num_keys) is moved into it; a sequence that ends before it begins is empty,
+ * and a row that two sequences claim then holds values of either.
  * max_k below a number of keys costs time, not correctness.  One kernel
  * launch, or two where the keys are split; results do not depend on the order
  * of blocks.  Calls that share a workspace must not overlap.  out, lse and

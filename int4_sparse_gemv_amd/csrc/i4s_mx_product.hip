@@ -136,7 +136,8 @@ __global__ __launch_bounds__(WAVES * 64) void mx_few_kernel(MxProductKernelArgs 
   auto load = [&](int g) {
     if constexpr (kFused) load_tokens(g, 0);
     load_operand<RT, ONCE>(w, a.w_vals, a.w_scales, first, tiles, steps, groups, g, lane);
-    if constexpr (!kFused) load_operand<NT, false>(x, a.x_vals, a.x_scales, blockIdx.y * NT, mx_row_tiles(a.tokens), steps, groups, g, lane);
+    if constexpr (!kFused)
+      load_operand<NT, false>(x, a.x_vals, a.x_scales, blockIdx.y * NT, mx_row_tiles(a.tokens), steps, groups, g, lane);
   };
   if (wave < groups) load(wave);
   for (int g = wave; g < groups; g += WAVES) {
@@ -460,7 +461,8 @@ __global__ __launch_bounds__(64 * WR *WC, 2) void mx_tile_kernel(MxProductKernel
   typedef typename Y::type T;
   typedef typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type W;
   constexpr int kMany = 16 / sizeof(T), kTiles = kMany / 4;
-  const int64_t row_at = (int64_t)(row0 + wr * RT) * 16 + lane / 16 * kMany, token_at = (int64_t)(token0 + wc * NT) * 16 + lane % 16;
+  const int64_t row_at = (int64_t)(row0 + wr * RT) * 16 + lane / 16 * kMany;
+  const int64_t token_at = (int64_t)(token0 + wc * NT) * 16 + lane % 16;
   T *const to = static_cast<T *>(a.y) + token_at * a.y_stride + row_at;
 #pragma unroll
   for (int n = 0; n < NT; ++n)

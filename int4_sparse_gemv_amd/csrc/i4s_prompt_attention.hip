@@ -309,7 +309,8 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
     f16_t p[NK];
     u4_t ahead[kAhead];
     auto read_k = [&](int i) {  // neighbouring products have sums of their own
-      return *reinterpret_cast<const u4_t *>(tiles + stage * L::kBytes + (32 * (i % NK) + li) * 2 * D + L::k_piece(li, 2 * (i / NK) + lh) * 16);
+      const char *row = tiles + stage * L::kBytes + (32 * (i % NK) + li) * 2 * D;
+      return *reinterpret_cast<const u4_t *>(row + L::k_piece(li, 2 * (i / NK) + lh) * 16);
     };
     const char *const tile = v_tiles + stage * L::kBytes;
 #pragma unroll

@@ -430,14 +430,15 @@ def test_attention_scales_and_far_scores(i4s, scale):
 
 
 def test_starts_outside_the_tensors(i4s):
-    """Moved into range; a sequence that ends before it begins is empty."""
+    """Moved into range; a sequence that ends before it begins is empty; a row that two claim has values of either."""
     rng = np.random.default_rng(2)
     q, k, v, _ = packed(rng, [(60, 60)], 2, 1, 64, F16)
     i32 = lambda *x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
     out = torch.full(q.shape, 3.0, dtype=F16, device="cuda")
     i4s.prompt_attention(q, k, v, i32(-5, 20, 10, 100), max_q=60, out=out)
     a, b = i4s.prompt_attention(q[:20], k[:20], v[:20]), i4s.prompt_attention(q[10:], k[10:], v[10:])
-    assert torch.equal(out[:10], a[:10]) and torch.equal(out[10:], b)
+    assert torch.equal(out[:10], a[:10]) and torch.equal(out[20:], b[10:])
+    assert ((out[10:20] == a[10:]) | (out[10:20] == b[:10])).all()
     none = i4s.prompt_attention(q, k, v, i32(0, 60), i32(2 ** 31 - 1, -2 ** 31))
     assert (none == 0).all()
 
