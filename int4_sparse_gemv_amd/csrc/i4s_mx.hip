@@ -1,7 +1,7 @@
 // Quantization to the microscaled 4-bit format and reading it back (format:
 // include/i4s_prompt.h), for gfx950.
 //
-// A wave takes 16 rows x 512 columns: the scales of a tile group.  Sixteen
+// A wave takes 16 rows x 512 columns, the scales of a tile group, or 4 rows of it.  Sixteen
 // neighbouring lanes hold 128 neighbouring columns of a row, eight each (16
 // bytes), so four lanes hold a block, whose largest magnitude two DPP steps
 // find as whole-number bits.  A lane's eight codes are four bytes of the
@@ -12,7 +12,6 @@
 // written where they are read back, past the caches (non-temporal): they are used
 // once.  Quantizing and reading back 13824 x 5120: 67 us for 358 MB = 5.4 TB/s
 // (through the caches 79), 2000 x 11008 22 us (31); a large copy runs at 4.8 TB/s.
-// Us for blocks of one / two / four waves, 64 x 11008: 9.1 / 9.6 / 10.3, large ones alike.
 
 #include "i4s_mx_common.h"
 
@@ -20,8 +19,12 @@ namespace i4s {
 namespace {
 
 constexpr int kMxThreads = 64;  // blocks of a wave: few rows reach more compute units
+// Up to so many tile groups take four waves each, of four rows.  Us of quantizing and
+// reading back, four waves / one, x 11008: 64 rows 5.1 / 9.2, 500 (704 groups) 7.8 / 11.5;
+// quantizing alone in four, 1000 (1386) 16.9 / 15.1, 2000 25.2 / 22.9.  1 x 4096 4.2 / 6.0.
+constexpr unsigned kFewUnits = 1024;
 
-template <typename X>
+template <typename X, int PARTS>  // PARTS of four rows by this wave, of the tile's four
 __global__ __launch_bounds__(kMxThreads) void mx_quantize_kernel(MxQuantizeArgs a) {
   const int groups = mx_groups(a.cols), steps = mx_steps(a.cols);
   const int64_t tile = blockIdx.x / (unsigned)groups;
@@ -29,35 +32,39 @@ __global__ __launch_bounds__(kMxThreads) void mx_quantize_kernel(MxQuantizeArgs 
   const int lane = threadIdx.x, col = lane % 16 * 8, sub = lane / 16, quad = lane % 4, block = lane % 16 / 4;
   const int left = steps - 4 * group < 4 ? steps - 4 * group : 4;  // tiles of this group
   const uint16_t *x = static_cast<const uint16_t *>(a.x);
-  u4_t v[4][4];
+  const int first = PARTS == 4 ? 0 : blockIdx.y * PARTS;
+  u4_t v[4][PARTS];
 #pragma unroll
   for (int c = 0; c < 4; ++c)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t row = tile * kMxRows + 4 * i + sub;
+    for (int i = 0; i < PARTS; ++i) {
+      const int64_t row = tile * kMxRows + 4 * (first + i) + sub;
       const int at = group * kMxGroup + c * kMxStep + col;
       v[c][i] = u4_t{0, 0, 0, 0};
       if (row < a.rows && at < a.cols)
         v[c][i] = __builtin_nontemporal_load(reinterpret_cast<const u4_t *>(x + row * a.stride + at));
     }
-  uint32_t scales[4] = {0, 0, 0, 0};
+  uint32_t scales[PARTS] = {};
   uint8_t *vals = a.vals + (tile * steps + 4 * group) * kMxTileBytes + block * 256 + quad * 4;
 #pragma unroll
   for (int c = 0; c < 4; ++c)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < PARTS; ++i) {
       const uint32_t pair = quad_max(top_bits(v[c][i]));
       const uint32_t top = (pair & 0xFFFFu) > pair >> 16 ? pair & 0xFFFFu : pair >> 16;
       const uint32_t byte = scale_byte<X>(top);
       scales[i] |= byte << (8 * c);
       const uint32_t word = byte == kMxNaN ? 0u : codes<X>(v[c][i], scale_value(byte));
-      if (c < left && tile * kMxRows + 4 * i + sub < a.rows)
-        *reinterpret_cast<uint32_t *>(vals + c * kMxTileBytes + (4 * i + sub) * 16) = word;
+      const int row = 4 * (first + i) + sub;
+      if (c < left && tile * kMxRows + row < a.rows)
+        *reinterpret_cast<uint32_t *>(vals + c * kMxTileBytes + row * 16) = word;
     }
-  // the quad's lanes hold the same four scale words: each stores one
-  const uint32_t word = quad < 2 ? (quad ? scales[1] : scales[0]) : (quad == 3 ? scales[3] : scales[2]);
-  const int row = 4 * quad + sub;
-  if (tile * kMxRows + row < a.rows)
+  // the quad's lanes hold the same scale words: each stores one
+  uint32_t word = scales[0];
+#pragma unroll
+  for (int i = 1; i < PARTS; ++i) word = quad == i ? scales[i] : word;
+  const int row = 4 * (first + quad) + sub;
+  if (quad < PARTS && tile * kMxRows + row < a.rows)
     *reinterpret_cast<uint32_t *>(a.scales + (tile * groups + group) * kMxGroupBytes + (block * 16 + row) * 4) = word;
 }
 
@@ -81,7 +88,7 @@ struct AsFloat {
   static __device__ float of(float f) { return f; }
 };
 
-template <typename Y>
+template <typename Y, int PARTS>
 __global__ __launch_bounds__(kMxThreads) void mx_read_kernel(MxReadArgs a) {
   typedef typename Y::type T;
   const int groups = mx_groups(a.cols), steps = mx_steps(a.cols);
@@ -91,16 +98,18 @@ __global__ __launch_bounds__(kMxThreads) void mx_read_kernel(MxReadArgs a) {
   const uint8_t *vals = a.vals + (tile * steps + 4 * group) * kMxTileBytes + block * 256 + quad * 4;
   const uint8_t *scales = a.scales + (tile * groups + group) * kMxGroupBytes + block * 64;
   T *out = static_cast<T *>(a.out);
+  const int first = PARTS == 4 ? 0 : blockIdx.y * PARTS;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t row = tile * kMxRows + 4 * i + sub;
+  for (int i = 0; i < PARTS; ++i) {
+    const int in = 4 * (first + i) + sub;
+    const int64_t row = tile * kMxRows + in;
     if (row >= a.rows) continue;
-    const uint32_t four = *reinterpret_cast<const uint32_t *>(scales + (4 * i + sub) * 4);
+    const uint32_t four = *reinterpret_cast<const uint32_t *>(scales + in * 4);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int at = group * kMxGroup + c * kMxStep + col;
       if (at >= a.cols) continue;
-      const uint32_t word = *reinterpret_cast<const uint32_t *>(vals + c * kMxTileBytes + (4 * i + sub) * 16);
+      const uint32_t word = *reinterpret_cast<const uint32_t *>(vals + c * kMxTileBytes + in * 16);
       const uint32_t byte = four >> (8 * c) & 255u;
       const float scale = byte == kMxNaN ? __builtin_nanf("") : scale_value(byte);
       const f2_t p[4] = {two_values<0>(word), two_values<1>(word), two_values<2>(word), two_values<3>(word)};
@@ -117,24 +126,37 @@ __global__ __launch_bounds__(kMxThreads) void mx_read_kernel(MxReadArgs a) {
 
 static dim3 mx_blocks(int32_t rows, int32_t cols) { return dim3((unsigned)((int64_t)mx_row_tiles(rows) * mx_groups(cols))); }
 
+template <typename X>
+static hipError_t launch_quantize(const MxQuantizeArgs &a, hipStream_t stream) {
+  dim3 grid = mx_blocks(a.rows, a.cols);
+  if (grid.x <= kFewUnits) {
+    grid.y = 4;
+    hipLaunchKernelGGL((mx_quantize_kernel<X, 1>), grid, dim3(kMxThreads), 0, stream, a);
+  } else {
+    hipLaunchKernelGGL((mx_quantize_kernel<X, 4>), grid, dim3(kMxThreads), 0, stream, a);
+  }
+  return hipGetLastError();
+}
+
 hipError_t launch_mx_quantize(const MxQuantizeArgs &a, int32_t dtype, hipStream_t stream) {
-  const dim3 grid = mx_blocks(a.rows, a.cols);
-  if (dtype == I4S_F16)
-    hipLaunchKernelGGL(mx_quantize_kernel<HalfX>, grid, dim3(kMxThreads), 0, stream, a);
-  else
-    hipLaunchKernelGGL(mx_quantize_kernel<BrainX>, grid, dim3(kMxThreads), 0, stream, a);
+  return dtype == I4S_F16 ? launch_quantize<HalfX>(a, stream) : launch_quantize<BrainX>(a, stream);
+}
+
+template <typename Y>
+static hipError_t launch_read(const MxReadArgs &a, hipStream_t stream) {
+  dim3 grid = mx_blocks(a.rows, a.cols);
+  if (grid.x <= kFewUnits) {
+    grid.y = 4;
+    hipLaunchKernelGGL((mx_read_kernel<Y, 1>), grid, dim3(kMxThreads), 0, stream, a);
+  } else {
+    hipLaunchKernelGGL((mx_read_kernel<Y, 4>), grid, dim3(kMxThreads), 0, stream, a);
+  }
   return hipGetLastError();
 }
 
 hipError_t launch_mx_read(const MxReadArgs &a, int32_t dtype, hipStream_t stream) {
-  const dim3 grid = mx_blocks(a.rows, a.cols);
-  if (dtype == I4S_F16)
-    hipLaunchKernelGGL(mx_read_kernel<AsHalf>, grid, dim3(kMxThreads), 0, stream, a);
-  else if (dtype == I4S_BF16)
-    hipLaunchKernelGGL(mx_read_kernel<AsBrain>, grid, dim3(kMxThreads), 0, stream, a);
-  else
-    hipLaunchKernelGGL(mx_read_kernel<AsFloat>, grid, dim3(kMxThreads), 0, stream, a);
-  return hipGetLastError();
+  if (dtype == I4S_F16) return launch_read<AsHalf>(a, stream);
+  return dtype == I4S_BF16 ? launch_read<AsBrain>(a, stream) : launch_read<AsFloat>(a, stream);
 }
 
 }  // namespace i4s

@@ -135,9 +135,10 @@ MxProductPlan mx_product_plan(int32_t tokens, int32_t rows, int32_t cols, bool x
   MxProductPlan p{};
   // 16-bit tokens: quantized by every block of the product while they are few,
   // else by a launch of its own.  Us in graphs, on the way / before: 13824 x 5120, 8
-  // tokens 9.6 / 13.5, 16: 13.1 / 14.0; 4096 x 4096, 16: 6.7 / 8.7; 22016 x 4096, 16: 16.2 /
-  // 15.8; 4096 x 11008, 8: 9.3 / 11.0, 16: 15.0 / 11.7.
-  p.quantize = !x_given && (tokens > 16 || (int64_t)tokens * cols >= 3 << 15);
+  // tokens 9.3 / 11.5, 12: 11.1 / 11.5, 16: 12.6 / 11.5; 4096 x 4096, 8: 4.9 / 6.3, 16: 6.7 /
+  // 6.4; 22016 x 4096, 8: 12.4 / 13.1, 16: 16.1 / 13.4; 4096 x 11008, 8: 9.3 / 9.2, 16: 14.9 /
+  // 9.5.
+  p.quantize = !x_given && (tokens > 16 || (int64_t)tokens * cols >= 1 << 16);
   p.token_tiles = (tokens + 15) / 16;
   // Blocks of eight waves and 1, 2 or (where each quantizes the tokens) 4 weight
   // tiles, about one or two for each of the 256 compute units; beyond, and for
@@ -190,8 +191,8 @@ PromptPlan prompt_plan(const i4s_prompt_args &a) {
   // Pairs of sequence and KV head that run together: as many as keep their keys in
   // the L2s, but enough that long rows of one are done next to short ones of others.
   // Us, for 8 / 160 / 320 blocks of an XCD and all: 16 x up to 2047 tokens, 8 x 4 heads
-  // (blocks of 256) 359 / 369 / 446 / 496; 8191 tokens, 40 heads 761 / 697 / 698 / 698; 16 x 1024 tokens,
-  // 40 heads 429 / 385 / 397 / 442.
+  // (blocks of 256) 359 / 369 / 446 / 496; 8191 tokens, 40 heads 761 / 697 / 698 / 698; 16 x
+  // 1024 tokens, 40 heads 429 / 385 / 397 / 442.
   p.group = 8 * ((160 + p.row_blocks - 1) / p.row_blocks);
   // The keys in pieces for about two blocks of 128 rows a compute unit, or one of
   // 32, but none shorter than 512 keys: partial results are fp32 and need a second

@@ -138,7 +138,7 @@ def test_product_workspace(lib):
     n = ctypes.c_uint64()
     size = lambda **kw: (P.i4s_mx_product_workspace_size(product(**kw), n), n.value)[1]  # noqa: E731
     assert size() == 4 * 2048 + 4 * 256 and size(**GIVEN) == 0 and size(tokens=16) == 0 and size(tokens=0) == 0
-    assert size(w=mx(20, 8192), tokens=12) == 64 * 1024 + 16 * 256 and size(w=mx(20, 8192), tokens=11) == 0
+    assert size(w=mx(20, 8192), tokens=8) == 64 * 1024 + 16 * 256 and size(w=mx(20, 8192), tokens=7) == 0
     assert P.i4s_mx_product(product(workspace_bytes=4 * 2048 + 4 * 256 - 1), None) == SMALL
     assert P.i4s_mx_product_workspace_size(product(), None) == BAD
     assert P.i4s_mx_product_workspace_size(None, n) == BAD and P.i4s_mx_product(None, None) == BAD
