@@ -531,6 +531,7 @@ template <typename Y>
 hipError_t launch_product(const MxProductKernelArgs &a, const MxProductPlan &p, hipStream_t stream) {
   if (p.few) return launch_few<Y>(a, p, stream);
   if (p.tile == 256) return launch_tiles<Y, 8, 4, 2, 4>(a, stream);
+  if (p.tile == 64) return launch_tiles<Y, 2, 4, 2, 2>(a, stream);
   return launch_tiles<Y, 4, 4, 2, 2>(a, stream);
 }
 

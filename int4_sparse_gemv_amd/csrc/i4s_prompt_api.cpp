@@ -152,20 +152,25 @@ MxProductPlan mx_product_plan(int32_t tokens, int32_t rows, int32_t cols, bool x
   p.row_tiles = tiles <= 256 ? 1 : 2;
   p.waves = tiles <= (p.token_tiles == 1 ? 1024 : 512) ? 8 : 4;
   if (!x_given && !p.quantize && tiles > 512 && p.waves == 8) p.row_tiles = 4;
-  // Few tokens' blocks (more than 64 tokens: several of them, 2x4) while they fill
-  // the chip better than 128 x 128 outputs.  Us, few / 128 x 128: 4096 x 4096: 128 tokens
-  // 6.8 / 11.5, 256: 8.9 / 11.7, 384: 12.1 / 12; 5120 x 13824: 128: 20 / 31, 256: 29 / 31;
-  // 11008 x 4096: 64: 11 / 13, 128: 14.4 / 12.9; 13824 x 5120: 64: 13.6 / 15, 128: 20 / 17.
-  p.few = p.token_tiles <= 4 || (int64_t)tiles * p.token_tiles <= 5120;
+  // Few tokens' blocks (more than 64 tokens: several of them, 2x4) while they are few
+  // enough to be on the chip together.  Us, few / 64 x 128 outputs: 4096 x 4096, 128 tokens
+  // 6.5 / 9.5, 256 (512 blocks) 8.6 / 10.4, 320 (640) 11.1 / 10.7; 5120 x 13824, 256 (640) 28 / 30,
+  // 320 (800) 34 / 30; 11008 x 4096, 80 (688) 13.0 / 11.5; 2048 x 2048, 512 (512) 5.9 / 6.5, 768
+  // (768) 8.3 / 6.7.  11008 x 4096, 64 tokens 11 / 13 (128 x 128).
+  p.few = p.token_tiles <= 4 || ((int64_t)tiles + 1) / 2 * ((p.token_tiles + 3) / 4) <= 640;
   if (p.token_tiles > 4) p.row_tiles = 2, p.waves = 4;
+  // 64 x 128 outputs while there is a compute unit for each block.  Us, 64 x 128 / 128 x
+  // 128: 4096 x 4096, 512 tokens 11.3 / 13.4; 11008 x 4096, 128 (172 blocks) 12.0 / 14.2, 192
+  // (344) 15.2 / 14.0; 13824 x 5120, 128 (216) 15.7 / 18.2, 160 (432) 18.8 / 17.4.
   // 256 x 256 outputs, one block a compute unit, where they fill more than three
   // quarters of whole rounds of them; else 128 x 128, two blocks.  Us, 256 / 128:
   // 4096^3 37 / 41 (256 blocks); 9000 x 13824 x 5120 348 / 402 (7.6 rounds of 8); 3000 x
   // 13824 x 5120 114 / 125 (2.5 of 3); 5000 x 5120 x 5120 74 / 80 (400 blocks); 6000 x
   // 4096 x 4096 61 / 59 (384); 4096 x 5120 x 13824 162 / 148 (320); 2048 x 4096 x 4096
   // 34 / 23 (half of one).
+  const int64_t small = ((int64_t)tokens + 127) / 128 * (((int64_t)rows + 63) / 64);
   const int64_t large = ((int64_t)tokens + 255) / 256 * (((int64_t)rows + 255) / 256);
-  p.tile = 4 * large > 3 * ((large + 255) / 256 * 256) ? 256 : 128;
+  p.tile = small <= 256 ? 64 : 4 * large > 3 * ((large + 255) / 256 * 256) ? 256 : 128;
   if (p.quantize) {
     p.x_vals = mx_vals_bytes(tokens, cols);
     p.x_scales = mx_scales_bytes(tokens, cols);

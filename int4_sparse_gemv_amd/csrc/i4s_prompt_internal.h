@@ -49,13 +49,13 @@ hipError_t launch_mx_read(const MxReadArgs &a, int32_t dtype, hipStream_t stream
 // How a product runs.  `quantize`: the 16-bit tokens are quantized into the
 // workspace first (otherwise the kernel does it on the way).  Few: blocks of
 // `waves` waves that split the columns of `row_tiles` weight tiles and up to
-// four token tiles.  Else blocks of `tile` x `tile` outputs.  The order of the
+// four token tiles.  Else blocks of `tile` x `tile` outputs, or 64 x 128.  The order of the
 // sums follows `few` and `waves`, which do not depend on how the tokens are given.
 struct MxProductPlan {
   bool quantize, few;
   int32_t token_tiles;       // 16-token tiles
   int32_t row_tiles, waves;  // few: (1, 8), (2, 8), (2, 4), or (4, 8) for 16-bit tokens
-  int32_t tile;
+  int32_t tile;              // 64, 128 or 256
   uint64_t x_vals, x_scales;  // workspace bytes of the quantized tokens
   uint64_t workspace_bytes;
 };

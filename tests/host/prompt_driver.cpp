@@ -85,7 +85,7 @@ void products(i4s_status expect) {
             CHECK(p.token_tiles <= 4 || (p.row_tiles == 2 && p.waves == 4));
             CHECK((p.token_tiles + 3) / 4 <= 65535);  // grid.y
           } else {
-            CHECK(p.tile == 128 || p.tile == 256);
+            CHECK(p.tile == 64 || p.tile == 128 || p.tile == 256);
           }
           if (fused) CHECK(p.few && tokens <= 16);
           // the order of the sums does not depend on how the tokens are given

@@ -202,7 +202,7 @@ def test_product(i4s, tokens, rows, cols, dtype):
 
 
 @pytest.mark.parametrize("tokens,rows,cols", [(4096, 4096, 1024), (2049, 8200, 544), (1100, 1501, 288), (1023, 1399, 1312),
-                                              (3897, 3801, 288), (3900, 3900, 96)])
+                                              (3897, 3801, 288), (3900, 3900, 96), (511, 4033, 1312), (383, 5003, 288), (100, 16300, 96)])
 def test_product_many(i4s, tokens, rows, cols):
     """The largest blocks, whole and ragged."""
     say("product", tokens, rows, cols)
@@ -228,7 +228,7 @@ def test_product_strides(i4s, tokens):
     assert (keep == 7.0).all()
 
 
-@pytest.mark.parametrize("tokens,rows,wide", [(1100, 1501, 1511), (3897, 3801, 3805)])
+@pytest.mark.parametrize("tokens,rows,wide", [(1100, 1501, 1511), (3897, 3801, 3805), (401, 4001, 4005), (1200, 4401, 4405)])
 @pytest.mark.parametrize("dtype", [F16, F32])
 def test_product_many_at_odd_places(i4s, tokens, rows, wide, dtype):
     """Outputs of the largest blocks at odd offsets and strides: the same values, and what lies between stays."""
@@ -240,7 +240,7 @@ def test_product_many_at_odd_places(i4s, tokens, rows, wide, dtype):
     assert (buf[:, :3] == 7.0).all() and (buf[:, 3 + rows:] == 7.0).all()
 
 
-@pytest.mark.parametrize("tokens,rows", [(3, 40), (40, 300), (1100, 1501), (3900, 3900)])
+@pytest.mark.parametrize("tokens,rows", [(3, 40), (40, 300), (400, 4000), (1100, 1501), (1200, 4400), (3900, 3900)])
 def test_product_with_a_block_that_is_not_finite(i4s, tokens, rows):
     """Its token, or its weight row, gets NaN; nothing else changes."""
     rng = np.random.default_rng(tokens)
