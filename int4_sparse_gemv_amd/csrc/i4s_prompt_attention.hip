@@ -545,8 +545,8 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
         const float lw = ml[(w * kPromptRows + r) * 2 + 1];
-        if (lw == 0.0f) continue;  // saw no key
-        const float f = __builtin_amdgcn_exp2f((ml[(w * kPromptRows + r) * 2] - top) * a.scale_log2);
+        // a wave of weight 0 counts: a value that its rows see may be a NaN
+        const float f = lw == 0.0f ? 0.0f : __builtin_amdgcn_exp2f((ml[(w * kPromptRows + r) * 2] - top) * a.scale_log2);
         l += f * lw;
         y += f * *reinterpret_cast<const f4_t *>(rows_at + (w * kPromptRows + r) * S::kRowFloats + x);
       }
@@ -635,7 +635,7 @@ __global__ __launch_bounds__(kJoinThreads) void prompt_join_kernel(PromptKernelA
   f4_t o = {0, 0, 0, 0};
 #pragma unroll 4
   for (int p = group; p < used; p += kGroups)
-    if (weight[p] != 0.0f) o += weight[p] * *reinterpret_cast<const f4_t *>(a.part_o + (p * all + row) * D + x);
+    o += weight[p] * *reinterpret_cast<const f4_t *>(a.part_o + (p * all + row) * D + x);  // of weight 0 too: it may be a NaN
   part[threadIdx.x] = o;
   __syncthreads();
   if (group) return;
