@@ -119,13 +119,17 @@ i4s_status i4s_mx_product(const i4s_mx_product_args *a /* host */, void *stream)
  * j <= nk - nq + t of its nk (the last token sees all; where nq > nk the first
  * ones see none); without it every token sees all keys:
  *   out = sum_j p_j v_j, p = softmax(scale * q . k_j).
- * A token that sees no key, or only scores of -inf, gets out = 0 and lse =
- * -inf.  Query head h reads KV head h / (q_heads / kv_heads).  What is in keys
- * and values that a token does not see does not matter to it, infinities and
- * NaN included; a NaN that it sees makes its output NaN.  Scores, softmax
- * statistics and sums are held in fp32; probabilities are rounded to the type
- * of v before they multiply it (2^-8 of a probability for bf16; 2^-11 for fp16,
- * or 2^-32 of the row's largest where that is more). */
+ * A token that sees no key, or only scores of -inf, gets lse = -inf and, where
+ * the values that it sees are finite, out = 0.  Query head h reads KV head
+ * h / (q_heads / kv_heads).  What is in keys and values that a token does not
+ * see does not matter to it, infinities and NaN included.  What it sees does,
+ * whatever its probability: a NaN among the values, or infinities of both
+ * signs, make that channel of its output NaN, other infinities make it that
+ * infinity; a NaN among q . k_j, or one (or the difference of two) above fp32's
+ * range, makes all of its output and lse NaN.  Scores, softmax statistics and
+ * sums are held in fp32; probabilities are rounded to the type of v before they
+ * multiply it (2^-8 of a probability for bf16; 2^-11 for fp16, or 2^-32 of the
+ * row's largest where that is more). */
 typedef struct i4s_prompt_args {
   const void *q;             /* [num_tokens][q_heads][D]; k, v               */
   const void *k;             /* [num_keys][kv_heads][D]: channels adjacent,  */

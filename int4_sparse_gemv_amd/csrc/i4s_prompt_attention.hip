@@ -23,6 +23,12 @@
 // the values' type for its matrix instruction (at most 2^-8 of itself for
 // bf16, 2^-11 for fp16), the sum takes it unrounded; the output is rounded once.
 //
+// Values that are not finite cost the usual call nothing: 0 times one is a NaN, in the
+// rows that do not see it as in those whose probability of it is 0, and a block whose
+// rows have a NaN at the end that is not their scores' goes through its keys again with
+// such values apart.  Us, 8191 tokens, 40 heads: 803 back to back, with a NaN in the first
+// key 2271, with nothing but infinities 6444.
+//
 // Long prompts are bound by the matrix cores, the LDS that feeds them (every wave
 // reads all keys and values for its 32 rows: half of the LDS's cycles) and power.
 // 8191 tokens, 40 heads of 128: 1231 us without the causal mask = 1.12 PFLOP/s, 670
@@ -33,9 +39,9 @@
 // rows in two halves, one in its softmax while the other multiplies, 1275, with the
 // loads' issue in the softmax 1231.  The tiles that a mask cuts, 40 prompts of 512
 // tokens, 40 heads: with registers that spill 405, with less held from one to the next
-// 288.  Tried and no faster: wave priorities for either part, waits between matrix
-// instructions, 32-key tiles with the next scores ahead of this softmax, V's operands
-// ahead in masked tiles, their finite check shared among the waves; 64 rows a wave spill.
+// 285, without a look at each one's V for values that are not finite 263.  Tried and no
+// faster: wave priorities for either part, waits between matrix instructions, 32-key
+// tiles with the next scores ahead of this softmax; 64 rows a wave spill.
 //
 // 32 rows or fewer of a sequence and KV head (a token behind long keys) are bound
 // by memory: there each wave of a block has tiles of 32 keys of its own, two of
@@ -172,6 +178,17 @@ struct Tile {
 
 constexpr float kSlack = 8.0f;  // log2: how far a probability may pass 2^kHeadroom
 
+// How a tile is worked on: every row sees all of it; a mask cuts it; and, in the pass
+// for values that are not finite, each value by what it is.
+constexpr int kPlain = 0, kMasked = 1, kCareful = 2;
+
+// A sum of values at another reference: infinities stay where their weight is 0.
+__device__ inline float weigh(float f, float v) { return __builtin_fabsf(v) == INFINITY ? v : f * v; }
+__device__ inline f4_t weigh(float f, f4_t v) { return {weigh(f, v.x), weigh(f, v.y), weigh(f, v.z), weigh(f, v.w)}; }
+
+// The factor of an output row.  Where all probabilities are 0 the row is 0 already, or an infinity or a NaN that it sees.
+__device__ inline float over(float sum) { return sum == 0.0f ? 1.0f : 1.0f / sum; }
+
 // ROWS of a block.  32: all query rows of a sequence and KV head fit a wave; the
 // waves of a block take the same rows and tiles of their own in turn, and join
 // at the end.  128: four waves, two blocks a compute unit.  256: eight, in two
@@ -185,9 +202,10 @@ struct Shape {
   static constexpr int kLoaders = kFew ? 1 : kWaves;            // waves that share a tile's loads
   static constexpr int kLoads = L::kBytes / 1024 / kLoaders;    // load instructions of a wave for K, and for V
   static constexpr int kStages = kPaired ? 4 : 2;               // tiles of K, and of V
-    static constexpr int kLds = (kFew ? kWaves : 1) * 2 * kStages * L::kBytes;
+  static constexpr int kTiles = (kFew ? kWaves : 1) * 2 * kStages * L::kBytes;
+  static constexpr int kLds = kTiles + (kFew ? 0 : 64);         // and a word of each wave
   static constexpr int kRowFloats = D + 4;                      // of an output row where waves join
-  static_assert(!kFew || kWaves * kPromptRows * kRowFloats * 4 + kWaves * kPromptRows * 8 <= kLds, "joined in the tiles' LDS");
+  static_assert(!kFew || kWaves * kPromptRows * kRowFloats * 4 + kWaves * kPromptRows * 8 <= kTiles, "joined in the tiles' LDS");
   static_assert(kLds <= 160 * 1024, "a compute unit has 160 KB");
 };
 
@@ -276,8 +294,8 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
   float sum = 0, less = 0;  // less: minus the row's reference
   bool fresh = true;
 
-  auto step = [&](int key, int stage, auto MASKED, auto &&load) {
-    constexpr bool masked = decltype(MASKED)::value;
+  auto step = [&](int key, int stage, auto MODE, auto &&load) {
+    constexpr bool masked = decltype(MODE)::value != kPlain, careful = decltype(MODE)::value == kCareful;
     // In the masked tiles addresses are worked out anew: kept from one to the next they
     // would not fit the registers.
     int own = lane;
@@ -287,7 +305,7 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
     const int tr_row = (own & 15) / 4 + 4 * lh, tr_piece = (own >> 4 & 1) * 2 + (own & 3) / 2;
     auto read_v = [&](const char *tile, int c, int x) {
       u4_t r;
-  #pragma unroll
+#pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int key = 16 * x + 8 * y + tr_row;
         const char *p = tile + key * 2 * D + L::v_piece(tr_row, 4 * c + tr_piece) * 16 + (own & 1) * 8;
@@ -322,7 +340,7 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
       if (i + kAhead < kScores) ahead[i % kAhead] = read_k(i + kAhead);
       issue_fence();
     }
-    if constexpr (PAIRED) {
+    if constexpr (PAIRED && !careful) {
       meet();  // the other half has its softmax behind it
       load(own);
     }
@@ -358,7 +376,7 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[c][e] *= f;
+        for (int e = 0; e < 16; ++e) o[c][e] = careful ? weigh(f, o[c][e]) : o[c][e] * f;
 #pragma unroll
       for (int n = 0; n < NK; ++n)
 #pragma unroll
@@ -375,21 +393,8 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[n][e / 4][e % 4] = two<T>(p[n][2 * e], p[n][2 * e + 1]);
     }
-    if constexpr (PAIRED) wait_loads<2 * S::kLoads>(), meet();
-    bool strange = false;  // values that are not finite may lie where a row does not see them
-    if constexpr (masked) {
-      float test = 0;
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int x = 0; x < 2 * NK; ++x) {
-          const u4_t v = read_v(tile, c, x);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) test = T::dot(v[e], 0u, test);
-        }
-      strange = __builtin_amdgcn_ballot_w64(!(test == 0.0f)) != 0;
-    }
-    if (!strange) {
+    if constexpr (!careful) {
+      if constexpr (PAIRED) wait_loads<2 * S::kLoads>(), meet();
       if constexpr (masked) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) ahead[i] = read_v(tile, i % NC, i / NC);
@@ -403,47 +408,51 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
       }
       return;
     }
-    // the finite ones as usual; then whether the row sees a +inf (-inf, either
-    // for a NaN) in the channel
+    // finite values as usual, in the same order; of others, whether the row sees a +inf
+    // (-inf, either for a NaN) in the channel
     const int limit = seen - key - 4 * lh;
 #pragma unroll 1
     for (int x = 0; x < 2 * NK; ++x) {
-      u4_t sees, weight;
+      u4_t weight;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int at = 16 * x + 8 * (e / 2) + 2 * (e % 2);
-        sees[e] = (at < limit ? T::kOne : 0u) | (at + 1 < limit ? T::kOne << 16 : 0u);
+      for (int e = 0; e < 4; ++e)
         weight[e] = x == 0 ? w[0][0][e] : (x == 1 ? w[0][1][e] : (x == 2 ? w[NK - 1][0][e] : w[NK - 1][1][e]));
-      }
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        u4_t v = read_v(tile, c, x), plus, minus;
+        u4_t v = read_v(tile, c, x);
+        float test = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t keep = 0, up = 0, down = 0;
+        for (int e = 0; e < 4; ++e) test = T::dot(v[e], 0u, test);
+        if (__builtin_amdgcn_ballot_w64(test != 0.0f)) {
+          u4_t sees, plus, minus;
 #pragma unroll
-          for (int b = 0; b < 32; b += 16) {
-            const uint32_t bits = v[e] >> b & 0xFFFFu, size = bits & 0x7FFFu;
-            if (size < T::kInf) keep |= bits << b;
-            if (size > T::kInf || bits == T::kInf) up |= T::kOne << b;
-            if (size > T::kInf || bits == (T::kInf | 0x8000u)) down |= T::kOne << b;
+          for (int e = 0; e < 4; ++e) {
+            const int at = 16 * x + 8 * (e / 2) + 2 * (e % 2);
+            sees[e] = (at < limit ? T::kOne : 0u) | (at + 1 < limit ? T::kOne << 16 : 0u);
+            uint32_t keep = 0, up = 0, down = 0;
+#pragma unroll
+            for (int b = 0; b < 32; b += 16) {
+              const uint32_t bits = v[e] >> b & 0xFFFFu, size = bits & 0x7FFFu;
+              if (size < T::kInf) keep |= bits << b;
+              if (size > T::kInf || bits == T::kInf) up |= T::kOne << b;
+              if (size > T::kInf || bits == (T::kInf | 0x8000u)) down |= T::kOne << b;
+            }
+            v[e] = keep, plus[e] = up, minus[e] = down;
           }
-          v[e] = keep, plus[e] = up, minus[e] = down;
+          f16_t zero;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) zero[e] = 0;
+          f16_t count = T::mfma(plus, sees, zero);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (count[e] > 0) o[c][e] += INFINITY;
+          issue_fence();
+          count = T::mfma(minus, sees, zero);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (count[e] > 0) o[c][e] -= INFINITY;
         }
         o[c] = T::mfma(v, weight, o[c]);
-        issue_fence();
-        f16_t zero;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) zero[e] = 0;
-        f16_t sum = T::mfma(plus, sees, zero);
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (sum[e] > 0) o[c][e] += INFINITY;
-        issue_fence();
-        sum = T::mfma(minus, sees, zero);
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (sum[e] > 0) o[c][e] -= INFINITY;
         issue_fence();
       }
     }
@@ -453,7 +462,23 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
   const int all_see = keys_seen(a, s, block_row / a.share);
   const int plain = (all_see < piece1 ? all_see : piece1) - L::kKeys;
   constexpr int kStride = FEW ? kWaves * L::kKeys : L::kKeys;
-  int key = piece0 + (FEW ? wave * L::kKeys : 0), stage = 0;
+  const int first_key = piece0 + (FEW ? wave * L::kKeys : 0);
+  int key = first_key, stage = 0;
+  // tiles of the next step on their way while one is worked on
+  auto next = [&](int own) {
+    wait_loads<0>();
+    if constexpr (FEW) {
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the other stage is read
+      issue_fence();
+    } else {
+      meet();  // everybody's part of this step's tiles is here, and nobody reads the other stage
+    }
+    if (key + kStride < piece1) load_k(key + kStride, stage ^ 1, own), load_v(key + kStride, stage ^ 1, own);
+  };
+  auto begin = [&](int own) {
+    if (key < piece1) load_k(key, 0, own), load_v(key, 0, own);
+  };
+  const auto no_load = [](int) {};
   if constexpr (PAIRED) {
     // While one half multiplies (a tile's probabilities with V, the next one's keys
     // with Q), the other works on its softmax, on the same four SIMDs.  Loads run
@@ -472,13 +497,13 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
     }
 #pragma unroll 1
     while (key <= plain) {
-      step(key, stage, std::false_type(), load);
+      step(key, stage, std::integral_constant<int, kPlain>(), load);
       turn();
     }
 #pragma unroll 1
     while (key < piece1) {
       if (key < any_sees) {
-        step(key, stage, std::true_type(), load);
+        step(key, stage, std::integral_constant<int, kMasked>(), load);
       } else {
         meet();
         load(lane);
@@ -490,22 +515,18 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
     if (piece0 < piece1 && wave < kWaves / 2) meet();
     wait_loads<0>();
   } else {
-    if (key < piece1) load_k(key, 0, lane), load_v(key, 0, lane);
-    auto next = [&](int own) {
-      wait_loads<0>();
-      if constexpr (FEW) {
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the other stage is read
-        issue_fence();
-      } else {
-        meet();  // everybody's part of this step's tiles is here, and nobody reads the other stage
-      }
-      if (key + kStride < piece1) load_k(key + kStride, stage ^ 1, own), load_v(key + kStride, stage ^ 1, own);
-    };
+    begin(lane);
+    if constexpr (D == 256) {
+      // In the other half of the registers, which matrix instructions read as they are: left
+      // to itself the compiler copied some of it in every step (4096 tokens, 16 heads: 182 us, so 171).
+#pragma unroll
+      for (int c = 0; c < NQ; ++c) asm volatile("" : "+a"(q[c]));
+    }
     auto turn = [&]() { key += kStride, stage ^= 1; };
 #pragma unroll 1
     while (key <= plain) {
       next(lane);
-      step(key, stage, std::false_type(), [](int) {});
+      step(key, stage, std::integral_constant<int, kPlain>(), no_load);
       turn();
     }
 #pragma unroll 1
@@ -513,12 +534,51 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
       int own = lane;
       asm volatile("" : "+v"(own));
       next(own);
-      if (key < any_sees) step(key, stage, std::true_type(), [](int) {});
+      if (key < any_sees) step(key, stage, std::integral_constant<int, kMasked>(), no_load);
       turn();
     }
   }
 
-  sum += other_half(sum, lane);
+  // 0 times a value that is not finite is a NaN: a row has one where it does not see
+  // such a value, or sees it at a probability that is 0 in fp32.  If any row has (and
+  // not by its scores, which make its sum a NaN too), the keys are gone through again,
+  // with care.  Blocks decide together, since they share tiles.
+  float all = sum + other_half(sum, lane);
+  bool lost = false;
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) lost |= o[c][e] != o[c][e];
+  bool again = __builtin_amdgcn_ballot_w64(lost && all == all) != 0;
+  if constexpr (!FEW) {
+    uint32_t *const votes = reinterpret_cast<uint32_t *>(lds + S::kTiles);
+    if (lane == 0) votes[wave] = again;
+    __syncthreads();
+    uint32_t any = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) any |= votes[w];
+    again = __builtin_amdgcn_readfirstlane(any) != 0;
+  }
+  if (__builtin_expect(again, 0)) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[c][e] = 0;
+    sum = 0, less = 0, fresh = true;
+    key = first_key, stage = 0;
+    int own = lane;
+    asm volatile("" : "+v"(own));
+    begin(own);
+#pragma unroll 1
+    while (key < piece1) {
+      asm volatile("" : "+v"(own));
+      next(own);
+      if (key < any_sees) step(key, stage, std::integral_constant<int, kCareful>(), no_load);
+      key += kStride, stage ^= 1;
+    }
+    all = sum + other_half(sum, lane);
+  }
+  sum = all;
   if constexpr (FEW) {
     // the waves join: references and sums first, then outputs at a common reference
     wait_loads<0>();
@@ -545,10 +605,10 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
         const float lw = ml[(w * kPromptRows + r) * 2 + 1];
-        // a wave of weight 0 counts: a value that its rows see may be a NaN
+        // a wave of weight 0 counts: values that its rows see may not be finite
         const float f = lw == 0.0f ? 0.0f : __builtin_amdgcn_exp2f((ml[(w * kPromptRows + r) * 2] - top) * a.scale_log2);
         l += f * lw;
-        y += f * *reinterpret_cast<const f4_t *>(rows_at + (w * kPromptRows + r) * S::kRowFloats + x);
+        y += weigh(f, *reinterpret_cast<const f4_t *>(rows_at + (w * kPromptRows + r) * S::kRowFloats + x));
       }
       const int64_t out_row = ((int64_t)(s.q0 + tr) * a.kv_heads + head) * a.share + (r - tr * a.share);
       if (a.splits > 1) {
@@ -556,7 +616,7 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
         *reinterpret_cast<f4_t *>(a.part_o + to * D + x) = y;
         if (x == 0) a.part_ml[2 * to] = top, a.part_ml[2 * to + 1] = l;
       } else {
-        const float f = l == 0.0f ? 0.0f : 1.0f / l;
+        const float f = over(l);
         *reinterpret_cast<u2_t *>(static_cast<uint16_t *>(a.out) + out_row * D + x) =
             u2_t{two<T>(y.x * f, y.y * f), two<T>(y.z * f, y.w * f)};
         if (a.lse && x == 0) a.lse[out_row] = lse_of(top, l, a.scale_log2, T::kHeadroom);
@@ -581,7 +641,7 @@ __global__ __launch_bounds__((64 * Shape<T, D, ROWS>::kWaves), (ROWS != 4 * kPro
     }
     return;
   }
-  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const float f = over(sum);
   uint16_t *to = static_cast<uint16_t *>(a.out) + out_row * D + 4 * lh;
 #pragma unroll
   for (int c = 0; c < NC; ++c)
@@ -635,13 +695,13 @@ __global__ __launch_bounds__(kJoinThreads) void prompt_join_kernel(PromptKernelA
   f4_t o = {0, 0, 0, 0};
 #pragma unroll 4
   for (int p = group; p < used; p += kGroups)
-    o += weight[p] * *reinterpret_cast<const f4_t *>(a.part_o + (p * all + row) * D + x);  // of weight 0 too: it may be a NaN
+    o += weigh(weight[p], *reinterpret_cast<const f4_t *>(a.part_o + (p * all + row) * D + x));  // pieces of weight 0 too
   part[threadIdx.x] = o;
   __syncthreads();
   if (group) return;
 #pragma unroll
   for (int g = 1; g < kGroups; ++g) o += part[g * kLanes + threadIdx.x];
-  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const float f = over(sum);
   *reinterpret_cast<u2_t *>(static_cast<uint16_t *>(a.out) + row * D + x) =
       u2_t{two<T>(o.x * f, o.y * f), two<T>(o.z * f, o.w * f)};
   if (a.lse && threadIdx.x == 0) a.lse[row] = lse_of(top, sum, a.scale_log2, T::kHeadroom);

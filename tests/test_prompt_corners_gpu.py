@@ -1,5 +1,11 @@
-"""Attention of whole prompts where values are not finite, on the GPU: what a
-token sees counts, whatever its probability and wherever the keys are split."""
+"""Attention of whole prompts where values are not finite, on the GPU.
+
+The rule: every key that a token sees counts, whatever its probability.  A NaN
+among their values, or infinities of both signs, make the channel NaN, another
+infinity makes it that infinity.  So the answer depends neither on the launch's
+shape, nor on the tile that a key lies in, nor on where the keys are split;
+channels whose values are finite keep their bits.
+"""
 
 import numpy as np
 import pytest
@@ -67,3 +73,142 @@ def test_a_nan_of_no_weight_counts(i4s, shape, dim, dtype, where, below):
     assert out[hit, :, 3].isnan().all()
     out[hit, :, 3] = clean[hit, :, 3]
     assert torch.equal(out, clean)
+
+
+# ---------------------------------------------------------------------------
+# the rule for all values that are not finite, at every place of the keys
+
+
+def sees(starts, lengths, key, tokens, causal):
+    """Which query tokens see key number ``key`` of the first sequence."""
+    nq, nk = lengths[0]
+    hit = torch.zeros(tokens, dtype=torch.bool, device="cuda")
+    hit[max(0, key - (nk - nq)) if causal else 0:nq] = True
+    return hit
+
+
+def poison(i4s, q, k, v, starts, lengths, key, causal, scale=1.0):
+    """One key's values in three channels, NaN and both infinities: the rows that see it get those, all else stays."""
+    clean, clean_lse = attend(i4s, q, k, v, starts, lengths, causal, scale)
+    v = v.clone()
+    for channel, bad in ((3, NAN), (17, INF), (40, -INF)):
+        v[key, :, channel] = bad
+    out, lse = attend(i4s, q, k, v, starts, lengths, causal, scale)
+    hit = sees(starts, lengths, key, q.shape[0], causal)
+    assert hit.any() and torch.equal(lse, clean_lse)
+    got = out[hit].float()
+    assert got[..., 3].isnan().all(), "NaN"
+    assert (got[..., 17] == INF).all(), "inf"
+    assert (got[..., 40] == -INF).all(), "-inf"
+    out = out.clone()
+    for channel in (3, 17, 40):
+        out[hit, :, channel] = clean[hit, :, channel]
+    assert torch.equal(out, clean)
+
+
+KEYS = ("first", 40, "middle", "block", "last")
+
+
+def key_of(where, lengths):
+    nq, nk = lengths[0]
+    return {"first": 0, "middle": nk // 2, "block": nk - nq, "last": nk - 1}.get(where, where)
+
+
+@pytest.mark.parametrize("shape,dim,dtype", CASES)
+@pytest.mark.parametrize("where", KEYS)
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_key_of_no_weight_counts(i4s, shape, dim, dtype, where, causal):
+    """Its score lies 300 below the others: its probability is less than fp32 holds."""
+    say(shape, dim, dtype, where, causal)
+    q, k, v, starts, lengths = make(shape, dim, dtype)
+    key = key_of(where, lengths)
+    q[..., 0], k[..., 0], k[key, :, 0] = 1, 0, -300 * dim ** 0.5
+    poison(i4s, q, k, v, starts, lengths, key, causal, dim ** -0.5)
+
+
+@pytest.mark.parametrize("shape,dim,dtype", CASES)
+def test_a_key_whose_weight_fades_counts(i4s, shape, dim, dtype):
+    """The first key's probability is the largest at its time; later scores rise step by step until it is less than fp32
+    holds."""
+    say(shape, dim, dtype)
+    q, k, v, starts, lengths = make(shape, dim, dtype)
+    q[..., 0] = 1
+    k[:, :, 0] = (torch.arange(k.shape[0], device="cuda") * (400.0 * dim ** 0.5 / lengths[0][1]))[:, None].to(dtype)
+    poison(i4s, q, k, v, starts, lengths, 0, True, dim ** -0.5)
+
+
+@pytest.mark.parametrize("shape,dim,dtype", CASES)
+@pytest.mark.parametrize("where", KEYS)
+def test_a_key_of_score_minus_infinity_counts(i4s, shape, dim, dtype, where):
+    say(shape, dim, dtype, where)
+    q, k, v, starts, lengths = make(shape, dim, dtype)
+    key = key_of(where, lengths)
+    q[..., 0], k[key, :, 0] = 1, -INF
+    poison(i4s, q, k, v, starts, lengths, key, True, dim ** -0.5)
+
+
+@pytest.mark.parametrize("shape,dim,dtype", CASES)
+@pytest.mark.parametrize("where", KEYS)
+def test_only_scores_of_minus_infinity(i4s, shape, dim, dtype, where):
+    """0 and -inf where the values are finite, and the rule where they are not."""
+    say(shape, dim, dtype, where)
+    q, k, v, starts, lengths = make(shape, dim, dtype)
+    q[..., 0], k[..., 0] = 1, -INF
+    for causal in (True, False):
+        out, lse = attend(i4s, q, k, v, starts, lengths, causal, dim ** -0.5)
+        assert (out == 0).all() and torch.isneginf(lse).all()
+        poison(i4s, q, k, v, starts, lengths, key_of(where, lengths), causal, dim ** -0.5)
+
+
+@pytest.mark.parametrize("shape,dim,dtype", CASES)
+def test_infinities_of_both_signs(i4s, shape, dim, dtype):
+    """Of keys far apart, in either order, one of them of no weight: NaN for the rows that see both."""
+    say(shape, dim, dtype)
+    q, k, v, starts, lengths = make(shape, dim, dtype)
+    a, b = key_of("first", lengths), key_of("last", lengths)
+    q[..., 0], k[..., 0], k[a, :, 0] = 1, 0, -300 * dim ** 0.5
+    clean, _ = attend(i4s, q, k, v, starts, lengths, False, dim ** -0.5)
+    v[a, :, 5], v[b, :, 5], v[a, :, 9], v[b, :, 9] = INF, -INF, -INF, INF
+    out, _ = attend(i4s, q, k, v, starts, lengths, False, dim ** -0.5)
+    nq = lengths[0][0]
+    assert out[:nq, :, 5].isnan().all() and out[:nq, :, 9].isnan().all()
+    keep = out.clone()
+    keep[:nq, :, 5], keep[:nq, :, 9] = clean[:nq, :, 5], clean[:nq, :, 9]
+    assert torch.equal(keep, clean)
+
+
+@pytest.mark.parametrize("shape,dim,dtype", CASES)
+def test_scores_that_are_not_finite(i4s, shape, dim, dtype):
+    """A score of NaN or +inf makes its token's row NaN, and no other."""
+    say(shape, dim, dtype)
+    for bad in (NAN, INF):
+        q, k, v, starts, lengths = make(shape, dim, dtype)
+        q[..., 0], k[..., 0] = 1, 0
+        key = lengths[0][1] - 1
+        clean, clean_lse = attend(i4s, q, k, v, starts, lengths, True, dim ** -0.5)
+        k[key, :, 0] = bad
+        out, lse = attend(i4s, q, k, v, starts, lengths, True, dim ** -0.5)
+        hit = sees(starts, lengths, key, q.shape[0], True)
+        assert out[hit].isnan().all() and lse[hit].isnan().all()
+        assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
+
+
+def test_a_captured_call_with_values_that_are_not_finite(i4s):
+    """Replayed with finite and other values in turn: each replay is the eager call's result."""
+    say("captured")
+    q, k, v, starts, lengths = make("block", 128, BF16)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        attend(i4s, q, k, v, starts, lengths)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got, _ = attend(i4s, q, k, v, starts, lengths)
+    for value in (1.0, INF, NAN, 2.0, -INF, 0.5):
+        v[7, :, 3], v[202, 0, 100] = value, value
+        want, _ = attend(i4s, q, k, v, starts, lengths)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(3.0), want.nan_to_num(3.0)), value
