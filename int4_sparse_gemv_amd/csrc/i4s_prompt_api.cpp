@@ -65,19 +65,13 @@ i4s_status check_row_stride(int64_t stride, int32_t cols, const char *name) {
 Span vals_of(const i4s_mx &m, const char *name) { return {m.vals, i4s::mx_vals_bytes(m.rows, m.cols), name}; }
 Span scales_of(const i4s_mx &m, const char *name) { return {m.scales, i4s::mx_scales_bytes(m.rows, m.cols), name}; }
 
+// What the size of the workspace follows from: of x only whether it is given.
 i4s_status check_product(const i4s_mx_product_args *a) {
   if (!a) return fail(I4S_ERR_INVALID_ARGUMENT, "args is NULL");
   i4s_status st = check_mx(a->w, "w", false);
   if (st != I4S_OK) return st;
   st = check_mx_shape(a->tokens, a->w->cols);
   if (st != I4S_OK) return st;
-  if (a->x) {
-    st = check_mx(a->x, "x", false);
-    if (st != I4S_OK) return st;
-    if (a->x->rows != a->tokens || a->x->cols != a->w->cols)
-      return fail(I4S_ERR_INVALID_ARGUMENT, "x is [%d][%d], tokens=%d and w's cols=%d", a->x->rows, a->x->cols, a->tokens,
-                  a->w->cols);
-  }
   // the smallest blocks take 128 x 128 outputs
   if (((int64_t)a->tokens + 127) / 128 * (((int64_t)a->w->rows + 127) / 128) > kMaxBlocks)
     return fail(I4S_ERR_INVALID_ARGUMENT, "tokens=%d times w's rows=%d must be below 2^37", a->tokens, a->w->rows);
@@ -288,6 +282,9 @@ i4s_status i4s_mx_product(const i4s_mx_product_args *a, void *stream) {
   if (a->x) {
     st = check_mx(a->x, "x", true);
     if (st != I4S_OK) return st;
+    if (a->x->rows != a->tokens || a->x->cols != w.cols)
+      return fail(I4S_ERR_INVALID_ARGUMENT, "x is [%d][%d], tokens=%d and w's cols=%d", a->x->rows, a->x->cols, a->tokens,
+                  w.cols);
   } else {
     st = check_half(a->x_dtype, "x_dtype");
     if (st != I4S_OK) return st;

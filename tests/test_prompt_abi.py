@@ -145,6 +145,17 @@ def test_product_workspace(lib):
     assert P.i4s_mx_product_workspace_size(product(w=mx(cols=16)), n) == BAD
 
 
+def test_product_workspace_looks_only_whether_x_is_given(lib):
+    """The tokens in the format need no workspace, whatever their descriptor holds at this time."""
+    n = ctypes.c_uint64(7)
+    for x in (P.i4s_mx(), mx(49, 96, None, None)):
+        assert P.i4s_mx_product_workspace_size(product(x=x), n) == 0 and n.value == 0
+        assert P.i4s_mx_product(product(x=x), None) == BAD  # the call looks at it
+    a = product()
+    a.x = 8  # nothing lies there
+    assert P.i4s_mx_product_workspace_size(a, n) == 0 and n.value == 0
+
+
 # ---------------------------------------------------------------------------
 # attention of whole prompts
 
