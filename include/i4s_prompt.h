@@ -49,7 +49,9 @@ extern "C" {
 
 #define I4S_MX_FORMAT_VERSION 1
 
-/* A matrix in the microscaled format.  Plain data, like i4s_packed. */
+/* A matrix in the microscaled format.  Plain data, like i4s_packed.  A call
+ * takes matrices of ceil(rows/16) * ceil(cols/512) <= 2^25 - 4, about 2^38
+ * values. */
 typedef struct i4s_mx {
   int32_t rows;    /* 0 .. 2^24                                              */
   int32_t cols;    /* a multiple of 32, 32 .. 2^20                           */
@@ -64,8 +66,8 @@ typedef struct i4s_mx_buffers {
 } i4s_mx_buffers;
 
 /* Sizes of the buffers of a matrix.  Host-only and pure.  Errors:
- * I4S_ERR_INVALID_ARGUMENT for a size outside the ranges of i4s_mx or
- * out == NULL. */
+ * I4S_ERR_INVALID_ARGUMENT for a size outside the ranges of i4s_mx, rows and
+ * cols together included, or out == NULL. */
 i4s_status i4s_mx_sizes(int32_t rows, int32_t cols, i4s_mx_buffers *out /* host */);
 
 /* Quantizes x ([rows][cols] of dtype I4S_F16 or I4S_BF16; columns adjacent,
@@ -83,7 +85,9 @@ i4s_status i4s_mx_read(const i4s_mx *m /* host */, int32_t dtype, void *out, voi
 /* y = X W^T for tokens X [tokens][cols] and a weight W [rows][cols]:
  * y[t][n] = sum_k X[t][k] W[n][k], summed in fp32, rounded once to out_dtype.
  * X is given in the microscaled format or as 16-bit values, which the call
- * quantizes as i4s_mx_quantize does; y is the same, bit for bit. */
+ * quantizes as i4s_mx_quantize does; y is the same, bit for bit.
+ * ceil(tokens/128) * ceil(rows/128) is at most 2^23 - 1, about 2^37 outputs, and
+ * [tokens][cols] within the limit of i4s_mx. */
 typedef struct i4s_mx_product_args {
   const i4s_mx *w;         /* host; the weight                               */
   const i4s_mx *x;         /* host; the tokens, or NULL: x_values            */

@@ -72,7 +72,8 @@ i4s_status check_product(const i4s_mx_product_args *a) {
   if (st != I4S_OK) return st;
   st = check_mx_shape(a->tokens, a->w->cols);
   if (st != I4S_OK) return st;
-  // the smallest blocks take 128 x 128 outputs
+  // Blocks of a grid.  Those of less than 128 x 128 outputs are taken only while they are
+  // few (mx_product_plan), or for up to 64 tokens: two weight tiles each, up to 2^19.
   if (((int64_t)a->tokens + 127) / 128 * (((int64_t)a->w->rows + 127) / 128) > kMaxBlocks)
     return fail(I4S_ERR_INVALID_ARGUMENT, "tokens=%d times w's rows=%d must be below 2^37", a->tokens, a->w->rows);
   if (a->reserved) return fail(I4S_ERR_INVALID_ARGUMENT, "reserved=%d must be 0", a->reserved);

@@ -105,7 +105,8 @@ struct PromptKernelArgs {
   void *out;
   float *lse;
   float *part_o;   // [splits][num_tokens * q_heads][D]
-  float *part_ml;  // [splits][num_tokens * q_heads][2]: largest score, sum
+  float *part_ml;  // [splits][num_tokens * q_heads][2]: the reference (a q . k, at most
+                   // 8 / scale_log2 below the largest), the sum
 };
 hipError_t launch_prompt_attention(const PromptKernelArgs &a, const PromptPlan &p, int32_t head_dim, int32_t dtype,
                                    hipStream_t stream);

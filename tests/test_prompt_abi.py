@@ -156,6 +156,21 @@ def test_product_workspace_looks_only_whether_x_is_given(lib):
     assert P.i4s_mx_product_workspace_size(a, n) == 0 and n.value == 0
 
 
+@pytest.mark.parametrize("tokens,rows,cols,ok", [(1 << 24, 63 * 128, 32, True), (1 << 24, 63 * 128 + 1, 32, False),
+                                                 (63 * 128, 1 << 24, 32, True), (63 * 128 + 1, 1 << 24, 32, False),
+                                                 (16 * 16383, 16, 1 << 20, True), (16 * 16384, 16, 1 << 20, False),
+                                                 (16 * ((1 << 20) - 1), 16, 32 * 512, True), (16 << 20, 16, 32 * 512, False)])
+@pytest.mark.parametrize("given", [False, True])
+def test_product_limits(lib, tokens, rows, cols, ok, given):
+    """The bounds of sizes together, as the header states them."""
+    text = " ".join(re.sub(r"\n \* ?", " ", open(HEADER).read()).split())
+    assert "ceil(tokens/128) * ceil(rows/128) is at most 2^23 - 1" in text
+    assert "ceil(rows/16) * ceil(cols/512) <= 2^25 - 4" in text
+    n = ctypes.c_uint64()
+    a = product(w=mx(rows, cols), x=mx(tokens, cols, 6 * GIB, 7 * GIB) if given else None, tokens=tokens)
+    assert P.i4s_mx_product_workspace_size(a, n) == (0 if ok else BAD)
+
+
 # ---------------------------------------------------------------------------
 # attention of whole prompts
 
