@@ -83,7 +83,9 @@ i4s_status i4s_mx_quantize(const void *x, int32_t dtype, int64_t stride, const i
 i4s_status i4s_mx_read(const i4s_mx *m /* host */, int32_t dtype, void *out, void *stream);
 
 /* y = X W^T for tokens X [tokens][cols] and a weight W [rows][cols]:
- * y[t][n] = sum_k X[t][k] W[n][k], summed in fp32, rounded once to out_dtype.
+ * y[t][n] = sum_k X[t][k] W[n][k], summed in fp32, rounded once to y_dtype.  A
+ * sum that passes fp32's range on its way ends as an infinity (of its sign, if
+ * its terms have one) or NaN; below the normal range it keeps subnormal numbers.
  * X is given in the microscaled format or as 16-bit values, which the call
  * quantizes as i4s_mx_quantize does; y is the same, bit for bit.
  * ceil(tokens/128) * ceil(rows/128) is at most 2^23 - 1, about 2^37 outputs, and
