@@ -113,11 +113,15 @@ __global__ __launch_bounds__(kMxThreads) void mx_read_kernel(MxReadArgs a) {
       const uint32_t byte = four >> (8 * c) & 255u;
       const float scale = byte == kMxNaN ? __builtin_nanf("") : scale_value(byte);
       const f2_t p[4] = {two_values<0>(word), two_values<1>(word), two_values<2>(word), two_values<3>(word)};
-      typedef T vec __attribute__((ext_vector_type(8)));
-      vec y;
+      constexpr int kMany = 16 / sizeof(T);  // 16 bytes a store: out's alignment
+      typedef T vec __attribute__((ext_vector_type(kMany)));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = Y::of(p[e / 2][e % 2] * scale);
-      __builtin_nontemporal_store(y, reinterpret_cast<vec *>(out + row * a.cols + at));
+      for (int h = 0; h < 8; h += kMany) {
+        vec y;
+#pragma unroll
+        for (int e = 0; e < kMany; ++e) y[e] = Y::of(p[(h + e) / 2][e % 2] * scale);
+        __builtin_nontemporal_store(y, reinterpret_cast<vec *>(out + row * a.cols + at + h));
+      }
     }
   }
 }
