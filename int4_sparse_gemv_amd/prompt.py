@@ -32,7 +32,9 @@ class MXTensor:
 
     ``vals``: uint8 [ceil(rows / 16), 2 * ceil(cols / 256), 1024]; ``scales``:
     uint8 [ceil(rows / 16), ceil(cols / 512), 256] (the layout inside is the
-    format's).
+    format's).  What the tensors hold may change (``mx_quantize(x, out=...)``);
+    which tensors they are, and the sizes, may not: the descriptor has their
+    addresses.
     """
 
     def __init__(self, rows: int, cols: int, vals, scales):
@@ -48,11 +50,13 @@ class MXTensor:
         self._hold(rows, cols, vals, scales, vals.get_device())
 
     def _hold(self, rows, cols, vals, scales, index):
-        self.rows, self.cols, self.vals, self.scales, self.index = rows, cols, vals, scales, index
-        self.shape = rows, cols
-        self.descriptor = P.i4s_mx(rows, cols, vals.data_ptr(), scales.data_ptr())
-        self.address = ctypes.addressof(self.descriptor)
+        descriptor = P.i4s_mx(rows, cols, vals.data_ptr(), scales.data_ptr())
+        self.__dict__.update(rows=rows, cols=cols, vals=vals, scales=scales, index=index, shape=(rows, cols),
+                             descriptor=descriptor, address=ctypes.addressof(descriptor))
         return self
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"an MXTensor's {name} is set when it is made; make another one")
 
     @property
     def device(self):

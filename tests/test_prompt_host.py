@@ -61,3 +61,19 @@ def test_prompt_step_range(monkeypatch, capsys, args, ok):
         with pytest.raises(SystemExit) as e:
             bench.parse()
         assert e.value.code == 2 and "takes 1 to 65536" in capsys.readouterr().err
+
+
+def test_a_matrix_keeps_its_buffers():
+    """The descriptor has the addresses of the tensors that a matrix was made of: another tensor in their place is refused,
+    where the calls would go on with the old one's memory."""
+    torch = pytest.importorskip("torch")
+    from int4_sparse_gemv_amd import prompt
+    vals, scales = torch.zeros(2, 2, 1024, dtype=torch.uint8), torch.zeros(2, 1, 256, dtype=torch.uint8)
+    m = prompt.MXTensor.__new__(prompt.MXTensor)._hold(20, 64, vals, scales, -1)
+    for name, value in (("vals", vals.clone()), ("scales", scales.clone()), ("rows", 5), ("cols", 32), ("shape", (5, 32)),
+                        ("index", 0), ("descriptor", None), ("address", 0), ("other", 1)):
+        with pytest.raises(AttributeError):
+            setattr(m, name, value)
+    assert m.vals is vals and m.scales is scales and (m.rows, m.cols, m.shape) == (20, 64, (20, 64))
+    assert (m.descriptor.vals, m.descriptor.scales) == (vals.data_ptr(), scales.data_ptr())
+    m.vals[:] = 7  # what they hold is the caller's
