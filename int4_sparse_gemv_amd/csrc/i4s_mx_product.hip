@@ -207,9 +207,9 @@ __global__ __launch_bounds__(WAVES * 64) void mx_few_kernel(MxProductKernelArgs 
 // that every wave has read the step whose place they take, and the waits before
 // it that every wave's part of the step that is read next is there.
 //
-// 8191 x 13824 x 5120: 284 us = 4.1 PFLOP/s; 8192^3 4.4.  Bound by power: matrix
+// 8191 x 13824 x 5120: 270 us = 4.3 PFLOP/s; 8192^3 235, 4.7.  Bound by power: matrix
 // instructions alone on the same data run at 6.2 PFLOP/s and 1.5 GHz, and here
-// too the clock falls to 1.5 GHz, with the matrix cores busy 64 % of the cycles.
+// too the clock falls to 1.5 GHz, with the matrix cores busy 54 to 64 % of the cycles.
 // The stores take 5 us of a round of 256 blocks of 256 x 256.  All eight waves in
 // step, reading and then multiplying: 7 to 14 % slower (8192^3: 292 us, half a
 // step apart 257, with the loads among the products 250).  Four waves with

@@ -180,9 +180,10 @@ PromptPlan prompt_plan(const i4s_prompt_args &a) {
   const int64_t pairs = (int64_t)a.kv_heads * (a.num_seqs > 0 ? a.num_seqs : 1), large = (rows + 255) / 256;
   // Blocks of 32 rows where those are all; of 256 (head dimension 128) for long keys,
   // where their ends weigh little, and some rounds of the 256 compute units; else 128.
-  // Us, 256 / 128: 8191 tokens x 40 heads 670 / 695, x 16 (512 blocks of 256) 269 / 298;
-  // 16384 x 16 1001 / 1045; 4096 x 64 297 / 306, x 40 205 / 195; 16 x up to 2047 tokens,
-  // 8 x 4 heads 347 / 332, x up to 1023 151 / 123; head dimension 64, 4096 x 40 133 / 117.
+  // Us, 256 / 128: 8191 tokens x 40 heads 661 / 679, x 16 (512 blocks of 256) 265 / 289;
+  // 16384 x 16 991 / 1036; 6144 x 40 394 / 427; 4096 x 64 297 / 304, x 40 196 / 192; 16 x up
+  // to 2047 tokens, 8 x 4 heads 345 / 321, x up to 1023 146 / 114; head dimension 64, 4096
+  // x 40 131 / 114.
   const int64_t len = a.max_k > 0 && a.max_k < a.num_keys ? a.max_k : a.num_keys;
   p.rows = rows <= kPromptRows ? kPromptRows
            : a.head_dim == 128 && len >= 6144 && pairs * large >= 448 ? 8 * kPromptRows : 4 * kPromptRows;
@@ -191,15 +192,16 @@ PromptPlan prompt_plan(const i4s_prompt_args &a) {
   // Pairs of sequence and KV head that run together: as many as keep their keys in
   // the L2s, but enough that long rows of one are done next to short ones of others.
   // Us, for 8 / 160 / 320 blocks of an XCD and all: 16 x up to 2047 tokens, 8 x 4 heads
-  // (blocks of 256) 359 / 369 / 446 / 496; 8191 tokens, 40 heads 761 / 697 / 698 / 698; 16 x
-  // 1024 tokens, 40 heads 429 / 385 / 397 / 442.
+  // 321 / 321 / 325 / 421; 8191 tokens, 40 heads 730 / 667 / 667 / 668; 16 x 1024 tokens,
+  // 40 heads 299 / 286 / 301 / 316.
   p.group = 8 * ((160 + p.row_blocks - 1) / p.row_blocks);
   // The keys in pieces for about two blocks of 128 rows a compute unit, or one of
   // 32, but none shorter than 512 keys: partial results are fp32 and need a second
   // launch.  Us, for half as many / these / twice as many: 65536 keys, 8 x 4 rows 63 /
-  // 50 / 53; 128 tokens behind 32767, 8 x 4 heads 101 / 95 / 108; 4 x 16 behind 8191
-  // 43 / 46 / 47.  512 tokens, 40 heads in one piece / two of 256 keys 26 / 53; 1024
-  // tokens, 8 heads in pieces of 512 / 256 35 / 30.
+  // 49 / 52; 128 tokens behind 32639, 8 x 4 heads 100 / 93 / 104; 4 x 16 behind 8176
+  // 41 / 40 / 51.  512 tokens, 40 heads in one piece / two of 256 keys 19 / 43; 1024
+  // tokens, 8 heads in one / of 512 / 256 26 / 30 / 26; 2048 tokens in one / these, 8
+  // heads 47 / 49, 16 heads (256 blocks, two pieces) 48 / 82: not worth it there.
   const int64_t want = clamp_to<int64_t>((p.rows == kPromptRows ? 256 : 512) / units, 1, len > 512 ? (len + 511) / 512 : 1);
   const int64_t per = clamp_to<int64_t>((len + want * kPromptKeys - 1) / (want * kPromptKeys), 1, (1 << 30) / kPromptKeys);
   p.chunk = (int32_t)(per * kPromptKeys);

@@ -21,7 +21,9 @@
 //
 // Roundings: scores, sums and outputs are fp32.  A probability is rounded to
 // the values' type for its matrix instruction (at most 2^-8 of itself for
-// bf16, 2^-11 for fp16), the sum takes it unrounded; the output is rounded once.
+// bf16, 2^-11 for fp16), the sum takes it unrounded; the output is rounded once.  A
+// second term for what the first leaves would double the second product; so outputs are
+// 0.0021 (bf16; fp16 0.00026) off where their own rounding makes 0.0016 (0.0002).
 //
 // Values that are not finite cost the usual call nothing: 0 times one is a NaN, in the
 // rows that do not see it as in those whose probability of it is 0, and a block whose
@@ -31,8 +33,8 @@
 //
 // Long prompts are bound by the matrix cores, the LDS that feeds them (every wave
 // reads all keys and values for its 32 rows: half of the LDS's cycles) and power.
-// 8191 tokens, 40 heads of 128: 1231 us without the causal mask = 1.12 PFLOP/s, 670
-// with it; a large matrix product of the library reaches 1.15, matrix instructions
+// 8191 tokens, 40 heads of 128: 1225 us without the causal mask = 1.12 PFLOP/s, 661
+// with it; large matrix products of the library reach 1.15 to 1.36, matrix instructions
 // alone 1.9.  Us without the mask, step by step: operands read by the instruction that
 // uses them 1400; four instructions ahead, V's first ones before the softmax, 1300
 // (head dimension 256: 224, 178; two ahead 204; six the same as four); blocks of 256
