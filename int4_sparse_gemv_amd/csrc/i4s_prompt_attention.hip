@@ -22,8 +22,10 @@
 // Roundings: scores, sums and outputs are fp32.  A probability is rounded to
 // the values' type for its matrix instruction (at most 2^-8 of itself for
 // bf16, 2^-11 for fp16), the sum takes it unrounded; the output is rounded once.  A
-// second term for what the first leaves would double the second product; so outputs are
-// 0.0021 (bf16; fp16 0.00026) off where their own rounding makes 0.0016 (0.0002).
+// second term for what the first leaves would double the second product, which bounds
+// blocks of many rows: their outputs are 0.0021 (bf16; fp16 0.00026) off where their own
+// rounding makes 0.0016 (0.0002).  Blocks of few rows wait for memory, but round as the
+// others do: a short sequence has the same bits in a launch of either shape.
 //
 // Values that are not finite cost the usual call nothing: 0 times one is a NaN, in the
 // rows that do not see it as in those whose probability of it is 0, and a block whose
