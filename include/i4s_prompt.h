@@ -131,11 +131,11 @@ i4s_status i4s_mx_product(const i4s_mx_product_args *a /* host */, void *stream)
  * see does not matter to it, infinities and NaN included.  What it sees does,
  * whatever its probability: a NaN among the values, or infinities of both
  * signs, make that channel of its output NaN, other infinities make it that
- * infinity; a NaN among q . k_j, or one (or the difference of two) above fp32's
- * range, makes all of its output and lse NaN.  Scores, softmax statistics and
- * sums are held in fp32; probabilities are rounded to the type of v before they
- * multiply it (2^-8 of a probability for bf16; 2^-11 for fp16, or 2^-32 of the
- * row's largest where that is more). */
+ * infinity; a NaN among q . k_j, or one above fp32's range, makes all of its
+ * output and lse NaN, and so may two whose difference is above it.  Scores,
+ * softmax statistics and sums are held in fp32; probabilities are rounded to the
+ * type of v before they multiply it (2^-8 of a probability for bf16; 2^-11 for
+ * fp16, or 2^-32 of the row's largest where that is more). */
 typedef struct i4s_prompt_args {
   const void *q;             /* [num_tokens][q_heads][D]; k, v               */
   const void *k;             /* [num_keys][kv_heads][D]: channels adjacent,  */

@@ -193,6 +193,45 @@ def test_scores_that_are_not_finite(i4s, shape, dim, dtype):
         assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
 
 
+@pytest.mark.parametrize("shape,dim,dtype", CASES)
+def test_infinities_of_both_signs_the_last_of_no_weight(i4s, shape, dim, dtype):
+    say(shape, dim, dtype)
+    q, k, v, starts, lengths = make(shape, dim, dtype)
+    a, b = key_of("first", lengths), key_of("last", lengths)
+    q[..., 0], k[..., 0], k[b, :, 0] = 1, 0, -300 * dim ** 0.5
+    v[a, :, 5], v[b, :, 5], v[a, :, 9], v[b, :, 9], v[a, :, 11], v[b, :, 11] = INF, -INF, -INF, INF, INF, NAN
+    nq = lengths[0][0]
+    for causal in (True, False):
+        out, _ = attend(i4s, q, k, v, starts, lengths, causal, dim ** -0.5)
+        both = slice(nq - 1 if causal else 0, nq)
+        assert out[both, :, 5].isnan().all() and out[both, :, 9].isnan().all() and out[both, :, 11].isnan().all()
+        if causal:  # the tokens before do not see the last key
+            assert (out[:nq - 1, :, 5] == INF).all() and (out[:nq - 1, :, 9] == -INF).all() and (out[:nq - 1, :, 11] == INF).all()
+        assert out[:nq, :, 12:].isfinite().all() and out[nq:].isfinite().all()
+
+
+@pytest.mark.parametrize("shape,dim,dtype", CASES)
+@pytest.mark.parametrize("where", KEYS)
+def test_scores_that_are_not_finite_anywhere(i4s, shape, dim, dtype, where):
+    """A score of NaN or +inf, far above or below the others' tiles: its rows are NaN, beside values that are not finite too."""
+    say(shape, dim, dtype, where)
+    q, k, v, starts, lengths = make(shape, dim, dtype)
+    q[..., 0], k[..., 0] = 1, 0
+    key = key_of(where, lengths)
+    hit = sees(starts, lengths, key, q.shape[0], True)
+    for bad in (NAN, INF):
+        for values in (False, True):
+            kk, vv = k.clone(), v.clone()
+            if values:
+                vv[lengths[0][1] // 3, :, 7], vv[key, :, 9] = INF, NAN
+            clean, clean_lse = attend(i4s, q, kk, vv, starts, lengths, True, dim ** -0.5)
+            kk[key, :, 0] = bad
+            out, lse = attend(i4s, q, kk, vv, starts, lengths, True, dim ** -0.5)
+            assert out[hit].isnan().all() and lse[hit].isnan().all()
+            assert torch.equal(out[~hit].nan_to_num(3.0, INF, -INF), clean[~hit].nan_to_num(3.0, INF, -INF))
+            assert torch.equal(lse[~hit], clean_lse[~hit])
+
+
 def test_a_captured_call_with_values_that_are_not_finite(i4s):
     """Replayed with finite and other values in turn: each replay is the eager call's result."""
     say("captured")

@@ -82,6 +82,26 @@ def test_products_past_the_range(i4s, tokens, rows, a, b):
     assert not np.isfinite(y[np.abs(want) > 2.0 ** 128 + tol]).any()
 
 
+@pytest.mark.parametrize("tokens,rows", SHAPES)
+@pytest.mark.parametrize("block", [0, 1, 4, 20, 34])
+def test_a_block_of_nan_beside_sums_past_the_range(i4s, tokens, rows, block):
+    """Whether the NaN comes before or behind the sum's infinity, of either sign: every product with it is NaN."""
+    rng = np.random.default_rng(block)
+    cols = 1120
+    for sign in (0, 8):
+        x, w = (rng.integers(4, 8, (n, cols)).astype(np.uint8) for n in (tokens, rows))
+        sx, sw = np.full((tokens, cols // 32), 127, np.uint8), np.full((rows, cols // 32), 127, np.uint8)
+        sx[:, 2:30:3] = 254
+        sw[:, 2:30:3] = 254
+        clean = i4s.mx_product(held(i4s, x | sign, sx), held(i4s, w, sw), dtype=F32)
+        assert (clean == (-INF if sign else INF)).all()
+        sx[tokens - 1, block] = 255
+        sw[rows - 1, block] = 255
+        y = i4s.mx_product(held(i4s, x | sign, sx), held(i4s, w, sw), dtype=F32)
+        assert y[tokens - 1].isnan().all() and y[:, rows - 1].isnan().all()
+        assert torch.equal(y[:tokens - 1, :rows - 1], clean[:tokens - 1, :rows - 1])
+
+
 @pytest.mark.parametrize("dtype,sizes", [(F16, (2.0 ** -24, 2.0 ** -16, 2.0 ** 14)),
                                          (BF16, (2.0 ** -133, 2.0 ** -120, 2.0 ** 125))])
 @pytest.mark.parametrize("tokens", [3, 16, 70])
